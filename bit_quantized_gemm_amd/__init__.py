@@ -17,6 +17,10 @@ The function names are the C entry points:
   -> (Wq u8 [N, RB], sw), ``atom_gemm_w4a8(Xq, sx, Wq, sw, K)`` -> Y, ``atom_gemm_w4a8_group_acc(Xq, Wq, K)``
 * ``atom_linear(X, perm, Wq, sw, workspace)`` -> (Y, Xq, sx): quantize + GEMM, one persistent launch
   where the shape allows (``atom_linear_workspace_bytes(M, N, K)``; the workspace starts zeroed)
+* W8A8 layer (``include/atom_w8a8.h``, in ``w8a8.py``): ``atom_quantize_w8a8(X)`` -> (Xq, sx),
+  ``atom_gemm_w8a8(Xq, sx, Wq, sw, K)`` -> Y, ``linear_w8a8(X, Wq, sw, bias)`` -> Y
+* 4-bit KV cache (``include/atom_kv4.h``, in ``kv4.py``): ``kv4_cache(...)``, ``atom_kv4_append``,
+  ``atom_kv4_read``, ``atom_kv4_attention``
 * ``atom_row_bytes(K)``, ``atom_num_groups(K)``, ``atom_strerror(status)``
 """
 from __future__ import annotations
@@ -91,6 +95,8 @@ def load_library():
         "atom_linear": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, i64, vp]),
         "atom_gemm_noalloc": (ctypes.c_int, [vp, vp, vp, vp, i32, i32, i32, vp, vp]),
     }
+    sig.update(w8a8.signatures())
+    sig.update(kv4.signatures())
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -427,3 +433,13 @@ def atom_gemm_w4a8_ws(Xq, sx, Wq, sw, K, workspace, Y=None, stream=None):
     _check(load_library().atom_gemm_w4a8_ws(pX, pSx, pW, pSw, M, N, K, pY, pWs, nws, _stream(stream, Xq.device)),
            "atom_gemm_w4a8_ws")
     return Y
+
+
+# --------------------------------------------------------------------------- W8A8 layer, 4-bit KV cache
+from . import kv4, w8a8  # noqa: E402
+from .kv4 import (KV4Cache, atom_kv4_append, atom_kv4_attention, atom_kv4_attention_workspace_bytes,  # noqa: E402
+                  atom_kv4_read, kv4_cache)
+from .w8a8 import (atom_gemm_w8a8, atom_gemm_w8a8_workspace_bytes, atom_linear_w8a8_workspace_bytes,  # noqa: E402
+                   atom_quantize_w8a8, atom_w8a8_row_bytes, linear_w8a8)
+
+__all__ += w8a8.__all__ + kv4.__all__

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatom.so")
 
-SOURCES = ["atom_api.cpp", "select.hip", "quantize.hip", "gemm.hip", "gemm_small.hip", "gemm_w4a8.hip"]
+SOURCES = ["atom_api.cpp", "select.hip", "quantize.hip", "gemm.hip", "gemm_small.hip", "gemm_w4a8.hip",
+           "serve_api.cpp", "w8a8_quantize.hip", "gemm_w8a8.hip", "kv4_cache.hip", "kv4_attention.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -45,7 +46,7 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(4, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]

@@ -1,0 +1,359 @@
+// W8A8 GEMM for gfx950: Y[m,n] = round(sx[m] * sw[n] * sum_k qx[m,k] * qw[n,k] + bias[n]) from
+// int8 codes with one fp32 scale a row on both sides, on v_mfma_i32_{32x32x32,16x16x64}_i8.
+//
+// The whole sum over K is one exact int32 (127^2 * 65536 < 2^31), so the scales are applied once
+// in the epilogue, and K may be divided among waves or workgroups without changing a bit.
+//
+// Operand layout.  Both operands are rows of K bytes; in a K = 32 slice lane l supplies row
+// l & 31 and bytes 16 (l >> 5) .. + 15.  The weights are the first operand, so a 32x32 accumulator
+// holds its tile transposed: lane l owns token l & 31, element r is column
+// (r >> 2) * 8 + (l >> 5) * 4 + (r & 3): four runs of four columns.
+//
+// Two kernels.
+//   gemm_tile_kernel: bound by the matrix cores.  The workgroup's four waves each own a WM x WN
+//     part of a BM x BN tile.  Stages of 64 bytes of K are copied from global memory straight into
+//     a ring of LDS buffers (LDS-DMA), three stages ahead.  Stage rows are unpadded, 16-byte chunks
+//     at swizzled positions: the 16 lanes of a 16-byte read hit distinct bank groups.  A stage is two K
+//     slices; a wave holds one slice's operands while the other's are read, so the matrix cores
+//     never wait for LDS, and the one barrier a stage stands between its two slices' products.
+//   gemm_rows_kernel (few tokens): bound by reading the weights.  A workgroup owns 16 columns, its
+//     waves divide K, and each wave loads its operands straight into registers, a batch of
+//     16-byte loads in flight at once; the waves' integer sums meet in LDS.
+#include "lds_ring.h"
+#include "serve_internal.h"
+#include "atom_internal.h"
+
+namespace atom {
+namespace {
+
+constexpr int kStage = 64;    // bytes of K of one stage
+constexpr int kRing = 4;      // stage buffers
+
+// Position of 16-byte chunk c of staged row r: four rows cover the banks once, and the next bits
+// of the row choose one of the four positions.
+__device__ __forceinline__ int pos(int r, int c) { return c ^ ((r >> 2) & 3); }
+
+__device__ __forceinline__ i32x16 mma(i32x4 w, i32x4 x, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(w, x, c, 0, 0, 0);
+}
+
+// One output: (acc * sx) * sw + bias, each step in fp32.  acc converts to fp32 with one rounding
+// (relative 2^-24); Y's own rounding is 2^-11 or 2^-8.  The empty asm keeps the compiler from folding the fma and
+// Y's conversion into one instruction with one rounding in some kernels and not in others.
+__device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias) {
+  float y = __builtin_fmaf((float)acc * sx, sw, bias);
+  asm("" : "+v"(y));
+  return y;
+}
+
+// BM x BN output tile of four waves (2 x 2); splits > 1: piece p of tile t is workgroup
+// p * tiles + t and writes its int32 tile to part[(p * tiles + t) * BM * BN].
+template <class T, int BM, int BN, int WAVES>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
+    const int8_t* __restrict__ Xq, const float* __restrict__ sx, const int8_t* __restrict__ Wq,
+    const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y,
+    int tiles, int splits, int32_t* __restrict__ part) {
+  constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
+  constexpr int kDmaA = BM / 64, kDmaB = BN / 64;        // LDS-DMA instructions per wave and stage
+  constexpr int kPer = kDmaA + kDmaB;
+  __shared__ __attribute__((aligned(16))) uint8_t la0[BM * kStage], la1[BM * kStage], la2[BM * kStage],
+      la3[BM * kStage];
+  __shared__ __attribute__((aligned(16))) uint8_t lb0[BN * kStage], lb1[BN * kStage], lb2[BN * kStage],
+      lb3[BN * kStage];
+  auto LA = [&](int p) -> uint8_t* { return p == 0 ? la0 : p == 1 ? la1 : p == 2 ? la2 : la3; };
+  auto LB = [&](int p) -> uint8_t* { return p == 0 ? lb0 : p == 1 ? lb1 : p == 2 ? lb2 : lb3; };
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
+  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
+  int lin = (int)blockIdx.x, piece = 0;
+  if (splits > 1) {
+    piece = lin / tiles;
+    lin -= piece * tiles;
+  } else {
+    // workgroups go to the 8 XCDs in turn: give each a contiguous run of the tile order, so that
+    // the tiles of one L2 share their operands
+    const int per = tiles / 8, more = tiles % 8, x = lin % 8;
+    lin = x * per + min(x, more) + lin / 8;
+  }
+  const int2 tc = tile_coords(lin, tiles_m, tiles_n);
+  const int m0 = tc.x * BM, n0 = tc.y * BN;
+  const int stages = Kp / kStage;
+  const int sa = (int)((int64_t)stages * piece / splits), sb = (int)((int64_t)stages * (piece + 1) / splits);
+
+  // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 16 rows an
+  // instruction: lane i lands at row i / 4, position i % 4, and loads the chunk that lies there.
+  // Rows past M / N repeat the last one (their results are never stored).
+  const int rows_a = min(BM, M - m0), rows_b = min(BN, N - n0);
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(Xq + (size_t)m0 * Kp), (short)0, rows_a * Kp, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(Wq + (size_t)n0 * Kp), (short)0, rows_b * Kp, 0x00020000);
+  int va[kDmaA], vb[kDmaB];
+#pragma unroll
+  for (int h = 0; h < kDmaA; ++h) {
+    const int r = wave * (BM / 4) + 16 * h + lane / 4;
+    va[h] = min(r, rows_a - 1) * Kp + pos(r, lane & 3) * 16;
+  }
+#pragma unroll
+  for (int h = 0; h < kDmaB; ++h) {
+    const int r = wave * (BN / 4) + 16 * h + lane / 4;
+    vb[h] = min(r, rows_b - 1) * Kp + pos(r, lane & 3) * 16;
+  }
+  // Copies of stages behind the last repeat it (never read).
+  auto dma = [&](int p, int s) __attribute__((always_inline)) {
+    const int off = min(s, stages - 1) * kStage;
+#pragma unroll
+    for (int h = 0; h < kDmaA; ++h) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 16 * h) * kStage, va[h], off);
+#pragma unroll
+    for (int h = 0; h < kDmaB; ++h) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 16 * h) * kStage, vb[h], off);
+  };
+  const int swz = (l32 >> 2) & 3;
+  auto read = [&](const uint8_t* buf, int row, int t) __attribute__((always_inline)) {   // slice t of a tile row
+    return *reinterpret_cast<const i32x4*>(buf + row * kStage + (((2 * t + kh) ^ swz) << 4));
+  };
+
+  i32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = i32x16{};
+  i32x4 a0[TM], b0[TN], a1[TM], b1[TN];
+  auto load = [&](int p, int t, i32x4 (&a)[TM], i32x4 (&b)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[i] = read(LA(p), wm * WM + 32 * i + l32, t);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) b[j] = read(LB(p), wn * WN + 32 * j + l32, t);
+  };
+  auto multiply = [&](const i32x4 (&a)[TM], const i32x4 (&b)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma(b[j], a[i], acc[i][j]);
+  };
+
+  // Ring.  Stage t lives in buffer (t - sa) % 4.  On entry of stage s its first slice is in
+  // registers and its copy is visible to every wave; stages s+1, s+2 are in flight.  Its buffer's
+  // predecessor, stage s-1, was read by all waves before the last barrier, so stage s+3 may be copied
+  // there.  The barrier comes once this wave's reads of stage s are done and its copy of stage
+  // s+1 has landed.
+  dma(0, sa);
+  dma(1, sa + 1);
+  dma(2, sa + 2);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(2 * kPer));
+  wg_barrier();
+  load(0, 0, a0, b0);
+  auto stage = [&](auto ring, int s) __attribute__((always_inline)) {
+    constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext, p3 = (p + 3) % kRing;
+    load(p, 1, a1, b1);
+    dma(p3, s + 3);
+    multiply(a0, b0);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(2 * kPer));
+    wg_barrier();
+    load(p1, 0, a0, b0);      // behind the last stage: the repeated copy, unused
+    multiply(a1, b1);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  {
+    int s = sa;
+    for (; s + kRing <= sb; s += kRing) ring_turn<0, kRing>(stage, s);
+    ring_tail<0, kRing>(stage, s, sb);
+  }
+  __builtin_amdgcn_s_waitcnt(0);                          // no copy into LDS outlives the workgroup
+
+  if (splits > 1) {
+    int32_t* tile = part + ((size_t)piece * tiles + lin) * (BM * BN);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<i32x4*>(tile + (wm * WM + 32 * i + l32) * BN + wn * WN + 32 * j + 8 * q + 4 * kh) =
+              i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * kh;
+      float w[4], b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = min(n + e, N - 1);
+        w[e] = sw[c];
+        b[e] = bias ? T::load(bias[c]) : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const int m = m0 + wm * WM + 32 * i + l32;
+        if (m >= M) continue;
+        const float x = sx[m];
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = scaled(acc[i][j][4 * q + e], x, w[e], b[e]);
+        uint16_t* dst = Y + (size_t)m * N + n;
+        if (n + 4 <= N && (N & 3) == 0) {
+          *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (n + e < N) dst[e] = T::store(y[e]);
+        }
+      }
+    }
+}
+
+// Adds the integer pieces of a split product and writes Y.  One thread per four columns of a tile row.
+template <class T, int BM, int BN>
+__global__ __launch_bounds__(256) void finish_kernel(const int32_t* __restrict__ part, const float* __restrict__ sx,
+                                                     const float* __restrict__ sw, const uint16_t* __restrict__ bias,
+                                                     int M, int N, uint16_t* __restrict__ Y, int tiles, int splits) {
+  constexpr int kPerTile = BM * BN / 4 / 256;             // workgroups per tile
+  const int lin = blockIdx.x / kPerTile;
+  const int2 tc = tile_coords(lin, (M + BM - 1) / BM, (N + BN - 1) / BN);
+  const int e4 = (blockIdx.x % kPerTile) * 256 + threadIdx.x;
+  const int r = e4 / (BN / 4), c = e4 % (BN / 4) * 4;
+  const int m = tc.x * BM + r, n = tc.y * BN + c;
+  if (m >= M || n >= N) return;
+  i32x4 a = {};
+  for (int p = 0; p < splits; ++p)
+    a += *reinterpret_cast<const i32x4*>(part + ((size_t)p * tiles + lin) * (BM * BN) + r * BN + c);
+  const float x = sx[m];
+  uint16_t* dst = Y + (size_t)m * N + n;
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int cc = min(n + e, N - 1);
+    y[e] = scaled(a[e], x, sw[cc], bias ? T::load(bias[cc]) : 0.0f);
+  }
+  if (n + 4 <= N && (N & 3) == 0) {
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+  } else {
+    for (int e = 0; e < 4; ++e)
+      if (n + e < N) dst[e] = T::store(y[e]);
+  }
+}
+
+// At most 16 RT tokens.  Lane l of a K = 64 slice supplies row l & 15, bytes 16 (l >> 4) .. + 15 of
+// both operands; the accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
+constexpr int kBatch = 4;      // units of 128 bytes of K whose loads a wave has in flight
+template <class T, int RT>
+__global__ void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
+                                 const int8_t* __restrict__ Wq, const float* __restrict__ sw,
+                                 const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) int32_t sums[];   // [waves][RT][16 tokens][16 columns]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
+  const int units = Kp / 128;
+  const int ua = units * wave / waves, ub = units * (wave + 1) / waves;
+  const int8_t* w = Wq + (size_t)min(n0 + l16, N - 1) * Kp + 16 * q;
+  const int8_t* x[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) x[i] = Xq + (size_t)min(16 * i + l16, M - 1) * Kp + 16 * q;
+  i32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = i32x4{};
+  for (int u = ua; u < ub; u += kBatch) {
+    i32x4 b[kBatch][2], a[RT][kBatch][2];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)      // past the range's end: the last unit again, not multiplied
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int off = min(u + k, ub - 1) * 128 + 64 * t;
+        b[k][t] = *reinterpret_cast<const i32x4*>(w + off);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) a[i][k][t] = *reinterpret_cast<const i32x4*>(x[i] + off);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (u + k < ub) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[k][t], a[i][k][t], acc[i], 0, 0, 0);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    *reinterpret_cast<i32x4*>(sums + ((wave * RT + i) * 16 + l16) * 16 + 4 * q) = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < RT * 256; e += blockDim.x) {
+    const int m = e >> 4, n = n0 + (e & 15);
+    if (m >= M || n >= N) continue;
+    int s = 0;
+    for (int v = 0; v < waves; ++v) s += sums[v * RT * 256 + e];
+    Y[(size_t)m * N + n] = T::store(scaled(s, sx[m], sw[n], bias ? T::load(bias[n]) : 0.0f));
+  }
+}
+
+// Tile sizes of the tiled kinds
+constexpr int kKinds = 4;
+constexpr int kBM[kKinds] = {16, 64, 128, 256}, kBN[kKinds] = {16, 128, 128, 256};
+
+template <class T>
+void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const uint16_t* bias, int M, int N,
+            int K, uint16_t* Y, int32_t* part, const W8Plan& p, hipStream_t st) {
+  const int Kp = (K + 127) / 128 * 128;
+  if (p.kind == 0) {
+    const int waves = min(16, max(4, (Kp / 128 + kBatch - 1) / kBatch));
+    if (M <= 16)
+      hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
+                         bias, M, N, Kp, Y);
+    else
+      hipLaunchKernelGGL((gemm_rows_kernel<T, 2>), dim3(p.tiles), dim3(64 * waves), waves * 2048, st, Xq, sx, Wq, sw,
+                         bias, M, N, Kp, Y);
+    return;
+  }
+  const dim3 grid(p.tiles * p.splits);
+#define ATOM_TILE(KIND, BM, BN, W)                                                                                   \
+  if (p.kind == KIND) {                                                                                              \
+    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, W>), grid, dim3(256), 0, st, Xq, sx, Wq, sw, bias, M, N, Kp, Y,  \
+                       p.tiles, p.splits, part);                                                                     \
+    if (p.splits > 1)                                                                                                \
+      hipLaunchKernelGGL((finish_kernel<T, BM, BN>), dim3(p.tiles * (BM * BN / 1024)), dim3(256), 0, st, part, sx,   \
+                         sw, bias, M, N, Y, p.tiles, p.splits);                                                      \
+  }
+  ATOM_TILE(1, 64, 128, 2)
+  ATOM_TILE(2, 128, 128, 2)
+  ATOM_TILE(3, 256, 256, 1)
+#undef ATOM_TILE
+}
+
+}  // namespace
+
+// The plan of a shape.  Up to 32 tokens: the few-rows kernel.  Otherwise the largest tile whose grid
+// fills the compute units, or the smallest one with K divided so that it does.
+W8Plan w8_plan(int M, int N, int K) {
+  auto tiles = [&](int kind) {
+    return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
+  };
+  if (M <= 32) return W8Plan{0, (N + 15) / 16, 1};
+  const int cus = compute_units();
+  if (tiles(3) >= cus * 3 / 4) return W8Plan{3, tiles(3), 1};
+  if (tiles(2) >= cus) return W8Plan{2, tiles(2), 1};
+  const int stages = (K + 127) / 128 * 2;
+  const int t = tiles(1);
+  const int splits = max(1, min(min(8, stages / 8), (2 * cus + t - 1) / t));
+  return W8Plan{1, t, splits};
+}
+
+int64_t w8_workspace_bytes(const W8Plan& p) {
+  return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0;
+}
+
+hipError_t launch_gemm_w8a8(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const uint16_t* bias,
+                            int M, int N, int K, bool bf16, uint16_t* Y, int32_t* part, const W8Plan& plan,
+                            hipStream_t stream) {
+  if (bf16)
+    launch<Bf16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
+  else
+    launch<Fp16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
+  return hipGetLastError();
+}
+
+}  // namespace atom

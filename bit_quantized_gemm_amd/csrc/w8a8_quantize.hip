@@ -1,0 +1,122 @@
+// Row quantize of the W8A8 layer for gfx950: one fp32 scale and K int8 codes for each row of an
+// fp16 or bf16 matrix, codes = clamp(rint(fl32(x / s)), -127, 127), s = fl32(max|x| / 127).
+//
+// What bounds it: HBM, 2 K bytes in and K + 4 out for a row (3 K in all).  The scale needs the whole row before the first
+// code, so a row is read once into registers by the threads that share it, its maximum is joined
+// (in a wave by DPP-free shuffles, across waves through LDS) and the codes are made from the registers.
+// The threads of a row follow its length: a wave for short rows (four rows a workgroup, no
+// barrier), 256 threads up to 16384 elements, 1024 beyond.  Rows whose elements no
+// 16-byte load fits (odd K or stride, shifted views) are read element by element.
+//
+// The codes must be those of an IEEE divide: x / s lands exactly between two codes whenever x is
+// max / 2 (a common value in bf16), and the nearest fp32 quotient decides.  See quotient().
+#include "serve_internal.h"
+
+namespace atom {
+namespace {
+
+template <class T, int THREADS, int CH, bool VEC>
+__global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                                               int rows, int K, int Kp,
+                                                                               int8_t* __restrict__ Xq,
+                                                                               float* __restrict__ sx) {
+  constexpr int kBlock = THREADS <= 64 ? 256 : THREADS;
+  constexpr int kRows = kBlock / THREADS;               // rows of one workgroup
+  const int t = threadIdx.x % THREADS;
+  const int row = blockIdx.x * kRows + threadIdx.x / THREADS;
+  if (kRows > 1 && row >= rows) return;                 // whole waves: no barrier follows
+  const uint16_t* x = X + (size_t)row * ldx;
+
+  // chunk c = t + i * THREADS: elements 8 c .. 8 c + 7, zeros behind K
+  uint32_t w[CH][4];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + i * THREADS;
+    if (VEC) {
+      u32x4 v = {0, 0, 0, 0};
+      if (8 * c < K) v = *reinterpret_cast<const u32x4*>(x + 8 * c);   // VEC: K % 8 == 0
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i][j] = v[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = 8 * c + 2 * j;
+        w[i][j] = (e < K ? (uint32_t)x[e] : 0u) | (e + 1 < K ? (uint32_t)x[e + 1] << 16 : 0u);
+      }
+    }
+  }
+  // |x| as integers: the order of the bits is the order of the values
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(w[i][j] & 0x7FFFu, (w[i][j] >> 16) & 0x7FFFu));
+#pragma unroll
+  for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+  if constexpr (THREADS > 64) {
+    __shared__ uint32_t wave_max[THREADS / 64];
+    if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) m = max(m, wave_max[i]);
+  }
+  const float s = T::load(m) / 127.0f;
+  if (t == 0) sx[row] = s;
+  const float r = s > 0.0f ? 1.0f / s : 0.0f;
+  const bool tiny = s < 0x1p-100f;                      // bf16 rows next to zero: the plain divide
+  int8_t* q = Xq + (size_t)row * Kp;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = t + i * THREADS;
+    if (8 * c >= Kp) continue;
+    uint32_t o[2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = elem<T>(w[i][2 * half + j / 2], j & 1);
+        float u = tiny ? (s > 0.0f ? v / s : 0.0f) : quotient(v, s, r);
+        u = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(u), -127.0f), 127.0f);
+        b[j] = (uint32_t)(int)u & 0xFFu;
+      }
+      o[half] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+    }
+    *reinterpret_cast<u32x2*>(q + 8 * c) = u32x2{o[0], o[1]};
+  }
+}
+
+template <class T, int THREADS, int CH>
+void launch(const uint16_t* X, int64_t ldx, bool vec, int rows, int K, int Kp, int8_t* Xq, float* sx, hipStream_t st) {
+  constexpr int kBlock = THREADS <= 64 ? 256 : THREADS;
+  const dim3 grid((rows + kBlock / THREADS - 1) / (kBlock / THREADS));
+  if (vec)
+    hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, true>), grid, dim3(kBlock), 0, st, X, ldx, rows, K, Kp, Xq, sx);
+  else
+    hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, false>), grid, dim3(kBlock), 0, st, X, ldx, rows, K, Kp, Xq, sx);
+}
+
+template <class T>
+void dispatch(const uint16_t* X, int64_t ldx, int rows, int K, int8_t* Xq, float* sx, hipStream_t st) {
+  const int Kp = (K + 127) / 128 * 128;
+  const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
+  if (Kp <= 512) launch<T, 64, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 2048) launch<T, 64, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 4096) launch<T, 256, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 8192) launch<T, 256, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 16384) launch<T, 256, 8>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else launch<T, 1024, 8>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_w8a8(const uint16_t* X, int64_t ldx, bool bf16, int rows, int K, int8_t* Xq, float* sx,
+                                hipStream_t stream) {
+  if (bf16)
+    dispatch<Bf16>(X, ldx, rows, K, Xq, sx, stream);
+  else
+    dispatch<Fp16>(X, ldx, rows, K, Xq, sx, stream);
+  return hipGetLastError();
+}
+
+}  // namespace atom
