@@ -10,12 +10,13 @@
 // (r >> 2) * 8 + (l >> 5) * 4 + (r & 3): four runs of four columns.
 //
 // Two kernels.
-//   gemm_tile_kernel: bound by the matrix cores.  The workgroup's four waves each own a WM x WN
-//     part of a BM x BN tile.  Stages of 64 bytes of K are copied from global memory straight into
-//     a ring of LDS buffers (LDS-DMA), three stages ahead.  Stage rows are unpadded, 16-byte chunks
-//     at swizzled positions: the 16 lanes of a 16-byte read hit distinct bank groups.  A stage is two K
-//     slices; a wave holds one slice's operands while the other's are read, so the matrix cores
-//     never wait for LDS, and the one barrier a stage stands between its two slices' products.
+//   gemm_tile_kernel: bound by the matrix cores, and at the largest sizes by the power they draw (4096 x 28672 x 8192 at
+//     2.5 POP/s on quantized normal data, 3.0 on zeros).  The workgroup's four waves each own a quarter of a BM x BN tile.
+//     Stages of 128 bytes of K are copied from global memory straight into a ring of LDS buffers (LDS-DMA): whole
+//     cache lines, because a line fetched in two halves by two stages came twice from the L2 (256 x 256 tiles, 64-byte
+//     stages: 1000 us instead of 935).  Stage rows are unpadded, 16-byte chunks at swizzled positions: the 16 lanes of a
+//     16-byte read hit distinct bank groups.  A stage is four K slices; a wave multiplies one slice while the next one's
+//     operands are read, one read or copy between two products.
 //   gemm_rows_kernel (few tokens): bound by reading the weights.  A workgroup owns 16 columns, its
 //     waves divide K, and each wave loads its operands straight into registers, a batch of
 //     16-byte loads in flight at once; the waves' integer sums meet in LDS.
@@ -26,12 +27,11 @@
 namespace atom {
 namespace {
 
-constexpr int kStage = 64;    // bytes of K of one stage
-constexpr int kRing = 4;      // stage buffers
+constexpr int kStage = 128;   // bytes of K of one stage: a cache line of each row
 
-// Position of 16-byte chunk c of staged row r: four rows cover the banks once, and the next bits
-// of the row choose one of the four positions.
-__device__ __forceinline__ int pos(int r, int c) { return c ^ ((r >> 2) & 3); }
+// Position of 16-byte chunk c of staged row r: two rows cover the banks once, and the next bits of the row
+// choose one of the eight positions.
+__device__ __forceinline__ int pos(int r, int c) { return c ^ ((r >> 1) & 7); }
 
 __device__ __forceinline__ i32x16 mma(i32x4 w, i32x4 x, i32x16 c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(w, x, c, 0, 0, 0);
@@ -46,22 +46,48 @@ __device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias)
   return y;
 }
 
-// BM x BN output tile of four waves (2 x 2); splits > 1: piece p of tile t is workgroup
+// Eight outputs of a row, `left` of them inside it; wide: the row's start is 16-byte aligned.
+template <class T>
+__device__ __forceinline__ void store8(uint16_t* dst, const float (&y)[8], int left, bool wide) {
+  if (wide && left >= 8) {
+    *reinterpret_cast<u32x4*>(dst) =
+        u32x4{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) dst[e] = T::store(y[e]);
+  }
+}
+
+// Order of a slice: NM products, each followed by its share of ND LDS reads and NV copies.  Left to itself the
+// compiler puts the reads behind the products, so that every slice ends in a wait for LDS.
+template <int NM, int ND, int NV>
+__device__ __forceinline__ void interleave() {
+  if constexpr (NM > 0) {
+    constexpr int nd = (ND + NM - 1) / NM, nv = (NV + NM - 1) / NM;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (nd > 0) __builtin_amdgcn_sched_group_barrier(0x100, nd, 0);
+    if constexpr (nv > 0) __builtin_amdgcn_sched_group_barrier(0x020, nv, 0);
+    interleave<NM - 1, ND - nd, NV - nv>();
+  }
+}
+
+// BM x BN output tile of four waves (2 x 2), RING stage buffers.  splits > 1: piece p of tile t is workgroup
 // p * tiles + t and writes its int32 tile to part[(p * tiles + t) * BM * BN].
-template <class T, int BM, int BN, int WAVES>
+template <class T, int BM, int BN, int RING, int WAVES>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
     const int8_t* __restrict__ Xq, const float* __restrict__ sx, const int8_t* __restrict__ Wq,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y,
     int tiles, int splits, int32_t* __restrict__ part) {
   constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
-  constexpr int kDmaA = BM / 64, kDmaB = BN / 64;        // LDS-DMA instructions per wave and stage
+  constexpr int kDmaA = BM / 32, kDmaB = BN / 32;        // LDS-DMA instructions per wave and stage
   constexpr int kPer = kDmaA + kDmaB;
-  __shared__ __attribute__((aligned(16))) uint8_t la0[BM * kStage], la1[BM * kStage], la2[BM * kStage],
-      la3[BM * kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lb0[BN * kStage], lb1[BN * kStage], lb2[BN * kStage],
-      lb3[BN * kStage];
-  auto LA = [&](int p) -> uint8_t* { return p == 0 ? la0 : p == 1 ? la1 : p == 2 ? la2 : la3; };
-  auto LB = [&](int p) -> uint8_t* { return p == 0 ? lb0 : p == 1 ? lb1 : p == 2 ? lb2 : lb3; };
+  constexpr int kA = BM * kStage, kB = BN * kStage;
+  // each stage buffer its own object: the compiler knows that a copy into one does not write another
+  __shared__ __attribute__((aligned(16))) uint8_t la0[kA], la1[kA], la2[kA];
+  __shared__ __attribute__((aligned(16))) uint8_t lb0[kB], lb1[kB], lb2[kB];   // (buffers past RING take no LDS)
+  auto LA = [&](int p) -> uint8_t* { return p == 0 ? la0 : p == 1 ? la1 : la2; };
+  auto LB = [&](int p) -> uint8_t* { return p == 0 ? lb0 : p == 1 ? lb1 : lb2; };
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
@@ -81,8 +107,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   const int stages = Kp / kStage;
   const int sa = (int)((int64_t)stages * piece / splits), sb = (int)((int64_t)stages * (piece + 1) / splits);
 
-  // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 16 rows an
-  // instruction: lane i lands at row i / 4, position i % 4, and loads the chunk that lies there.
+  // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 8 rows an
+  // instruction: lane i lands at row i / 8, position i % 8, and loads the chunk that lies there.
   // Rows past M / N repeat the last one (their results are never stored).
   const int rows_a = min(BM, M - m0), rows_b = min(BN, N - n0);
   const __amdgpu_buffer_rsrc_t ra =
@@ -92,23 +118,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   int va[kDmaA], vb[kDmaB];
 #pragma unroll
   for (int h = 0; h < kDmaA; ++h) {
-    const int r = wave * (BM / 4) + 16 * h + lane / 4;
-    va[h] = min(r, rows_a - 1) * Kp + pos(r, lane & 3) * 16;
+    const int r = wave * (BM / 4) + 8 * h + lane / 8;
+    va[h] = min(r, rows_a - 1) * Kp + pos(r, lane & 7) * 16;
   }
 #pragma unroll
   for (int h = 0; h < kDmaB; ++h) {
-    const int r = wave * (BN / 4) + 16 * h + lane / 4;
-    vb[h] = min(r, rows_b - 1) * Kp + pos(r, lane & 3) * 16;
+    const int r = wave * (BN / 4) + 8 * h + lane / 8;
+    vb[h] = min(r, rows_b - 1) * Kp + pos(r, lane & 7) * 16;
   }
   // Copies of stages behind the last repeat it (never read).
   auto dma = [&](int p, int s) __attribute__((always_inline)) {
     const int off = min(s, stages - 1) * kStage;
 #pragma unroll
-    for (int h = 0; h < kDmaA; ++h) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 16 * h) * kStage, va[h], off);
+    for (int h = 0; h < kDmaA; ++h) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 8 * h) * kStage, va[h], off);
 #pragma unroll
-    for (int h = 0; h < kDmaB; ++h) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 16 * h) * kStage, vb[h], off);
+    for (int h = 0; h < kDmaB; ++h) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 8 * h) * kStage, vb[h], off);
   };
-  const int swz = (l32 >> 2) & 3;
+  const int swz = (l32 >> 1) & 7;
   auto read = [&](const uint8_t* buf, int row, int t) __attribute__((always_inline)) {   // slice t of a tile row
     return *reinterpret_cast<const i32x4*>(buf + row * kStage + (((2 * t + kh) ^ swz) << 4));
   };
@@ -132,33 +158,41 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
       for (int j = 0; j < TN; ++j) acc[i][j] = mma(b[j], a[i], acc[i][j]);
   };
 
-  // Ring.  Stage t lives in buffer (t - sa) % 4.  On entry of stage s its first slice is in
-  // registers and its copy is visible to every wave; stages s+1, s+2 are in flight.  Its buffer's
-  // predecessor, stage s-1, was read by all waves before the last barrier, so stage s+3 may be copied
-  // there.  The barrier comes once this wave's reads of stage s are done and its copy of stage
-  // s+1 has landed.
-  dma(0, sa);
-  dma(1, sa + 1);
-  dma(2, sa + 2);
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(2 * kPer));
+  // Ring.  Stage t lives in buffer (t - sa) % RING.  On entry of stage s its first slice is in registers and its
+  // copy is visible to every wave; stages s+1 .. s+RING-1 are in flight.  The barrier comes once this wave's reads
+  // of stage s are done and its copy of stage s+1 has landed: behind it the last slice is multiplied while the
+  // next stage's first is read and stage s+RING is copied into the buffer that stage s has left.
+#pragma unroll
+  for (int p = 0; p < RING; ++p) dma(p, sa + p);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 1) * kPer));
   wg_barrier();
   load(0, 0, a0, b0);
   auto stage = [&](auto ring, int s) __attribute__((always_inline)) {
-    constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext, p3 = (p + 3) % kRing;
+    constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext;
     load(p, 1, a1, b1);
-    dma(p3, s + 3);
     multiply(a0, b0);
+    interleave<TM * TN, TM + TN, 0>();
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(2 * kPer));
-    wg_barrier();
-    load(p1, 0, a0, b0);      // behind the last stage: the repeated copy, unused
+    load(p, 2, a0, b0);
     multiply(a1, b1);
+    interleave<TM * TN, TM + TN, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    load(p, 3, a1, b1);
+    multiply(a0, b0);
+    interleave<TM * TN, TM + TN, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 2) * kPer));
+    wg_barrier();
+    load(p1, 0, a0, b0);      // behind the last stage: a repeated copy, unused
+    dma(p, s + RING);
+    multiply(a1, b1);
+    interleave<TM * TN, TM + TN, kPer>();
     __builtin_amdgcn_sched_barrier(0);
   };
   {
     int s = sa;
-    for (; s + kRing <= sb; s += kRing) ring_turn<0, kRing>(stage, s);
-    ring_tail<0, kRing>(stage, s, sb);
+    for (; s + RING <= sb; s += RING) ring_turn<0, RING>(stage, s);
+    ring_tail<0, RING>(stage, s, sb);
   }
   __builtin_amdgcn_s_waitcnt(0);                          // no copy into LDS outlives the workgroup
 
@@ -174,36 +208,45 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
               i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     return;
   }
+  // Epilogue through LDS, 32 rows of a wave at a time: the accumulators' columns lie four to a lane and 32 rows to an
+  // instruction, and stores of that shape send 16 bytes each to rows a multiple of 4 KB apart, all in one channel of the L2
+  // (4096 x 28672 outputs of K = 256: 236 us so, 114 us row by row; of K = 8192: 935 and 762 us).  Chunk c of 4 columns of row r lies at position
+  // c ^ (r & 15): both the writes (16 rows of one chunk) and the reads (a row's chunks) cover all banks.
+  wg_barrier();                                           // every wave has read its last stage
+  constexpr int kLanes = WN / 8;                          // lanes of a row: 8 columns each
+  i32x4* own = reinterpret_cast<i32x4*>(wave == 0 ? la0 : wave == 1 ? la1 : RING == 2 ? (wave == 2 ? lb0 : lb1)
+                                                                                      : (wave == 2 ? la2 : lb0));
+  static_assert(32 * WN * 4 <= kA && 32 * WN * 4 <= kB, "a wave's rows fit a stage buffer");
+  const int c8 = lane % kLanes, n = n0 + wn * WN + 8 * c8;
+  float w[8], b[8];
 #pragma unroll
-  for (int j = 0; j < TN; ++j)
+  for (int e = 0; e < 8; ++e) {
+    const int c = min(n + e, N - 1);
+    w[e] = sw[c];
+    b[e] = bias ? T::load(bias[c]) : 0.0f;
+  }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * kh;
-      float w[4], b[4];
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        own[l32 * (WN / 4) + ((8 * j + 2 * q + kh) ^ (l32 & 15))] =
+            i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+#pragma unroll
+    for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
+      const int m = m0 + wm * WM + 32 * i + r;
+      const i32x4 lo = own[r * (WN / 4) + ((2 * c8) ^ (r & 15))], hi = own[r * (WN / 4) + ((2 * c8 + 1) ^ (r & 15))];
+      const float x = sx[min(m, M - 1)];
+      float y[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int c = min(n + e, N - 1);
-        w[e] = sw[c];
-        b[e] = bias ? T::load(bias[c]) : 0.0f;
+        y[e] = scaled(lo[e], x, w[e], b[e]);
+        y[e + 4] = scaled(hi[e], x, w[e + 4], b[e + 4]);
       }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const int m = m0 + wm * WM + 32 * i + l32;
-        if (m >= M) continue;
-        const float x = sx[m];
-        float y[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = scaled(acc[i][j][4 * q + e], x, w[e], b[e]);
-        uint16_t* dst = Y + (size_t)m * N + n;
-        if (n + 4 <= N && (N & 3) == 0) {
-          *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < N) dst[e] = T::store(y[e]);
-        }
-      }
+      if (m < M) store8<T>(Y + (size_t)m * N + n, y, N - n, (N & 7) == 0);
     }
+  }
 }
 
 // Adds the integer pieces of a split product and writes Y.  One thread per four columns of a tile row.
@@ -239,11 +282,11 @@ __global__ __launch_bounds__(256) void finish_kernel(const int32_t* __restrict__
 
 // At most 16 RT tokens.  Lane l of a K = 64 slice supplies row l & 15, bytes 16 (l >> 4) .. + 15 of
 // both operands; the accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
-constexpr int kBatch = 4;      // units of 128 bytes of K whose loads a wave has in flight
 template <class T, int RT>
 __global__ void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
                                  const int8_t* __restrict__ Wq, const float* __restrict__ sw,
                                  const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y) {
+  constexpr int kBatch = 4;      // units of 128 bytes of K whose loads a wave has in flight
   extern __shared__ __attribute__((aligned(16))) int32_t sums[];   // [waves][RT][16 tokens][16 columns]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
@@ -291,16 +334,16 @@ __global__ void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __r
   }
 }
 
-// Tile sizes of the tiled kinds
-constexpr int kKinds = 4;
-constexpr int kBM[kKinds] = {16, 64, 128, 256}, kBN[kKinds] = {16, 128, 128, 256};
+// The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
+constexpr int kKinds = 5;
+constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
 
 template <class T>
 void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const uint16_t* bias, int M, int N,
             int K, uint16_t* Y, int32_t* part, const W8Plan& p, hipStream_t st) {
   const int Kp = (K + 127) / 128 * 128;
   if (p.kind == 0) {
-    const int waves = min(16, max(4, (Kp / 128 + kBatch - 1) / kBatch));
+    const int waves = min(16, max(4, (Kp / 128 + 3) / 4));
     if (M <= 16)
       hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
                          bias, M, N, Kp, Y);
@@ -310,36 +353,56 @@ void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw
     return;
   }
   const dim3 grid(p.tiles * p.splits);
-#define ATOM_TILE(KIND, BM, BN, W)                                                                                   \
+#define ATOM_TILE(KIND, BM, BN, RING, W)                                                                             \
   if (p.kind == KIND) {                                                                                              \
-    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, W>), grid, dim3(256), 0, st, Xq, sx, Wq, sw, bias, M, N, Kp, Y,  \
-                       p.tiles, p.splits, part);                                                                     \
+    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W>), grid, dim3(256), 0, st, Xq, sx, Wq, sw, bias, M, N,   \
+                       Kp, Y, p.tiles, p.splits, part);                                                              \
     if (p.splits > 1)                                                                                                \
       hipLaunchKernelGGL((finish_kernel<T, BM, BN>), dim3(p.tiles * (BM * BN / 1024)), dim3(256), 0, st, part, sx,   \
                          sw, bias, M, N, Y, p.tiles, p.splits);                                                      \
   }
-  ATOM_TILE(1, 64, 128, 2)
-  ATOM_TILE(2, 128, 128, 2)
-  ATOM_TILE(3, 256, 256, 1)
+  ATOM_TILE(1, 64, 128, 3, 2)
+  ATOM_TILE(2, 128, 128, 2, 2)
+  ATOM_TILE(3, 256, 128, 3, 1)
+  ATOM_TILE(4, 256, 256, 2, 1)
 #undef ATOM_TILE
 }
 
 }  // namespace
 
-// The plan of a shape.  Up to 32 tokens: the few-rows kernel.  Otherwise the largest tile whose grid
-// fills the compute units, or the smallest one with K divided so that it does.
+// The plan of a shape.  Up to 32 tokens: the few-rows kernel (32 x 4096 x 4096: 8 us against 12 us in 64 x 128 tiles).
+// Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
+// epilogue) and `full` ns for each element of K when every compute unit holds `slots` workgroups, `one` ns when it holds
+// one (fitted to 1024 x 11008 x 4096, 2048 x 4096 x 11008, 4096 x 28672 x 8192, 512 x 4096 x 4096 and 1500 x 6000 x 700 on
+// 256 units).  A grid that leaves half the units idle over a long K, or most of them over a shorter one, has K
+// divided up to four ways (with the second kernel 200 x 1024 x 8192: 22.5 -> 14 us, 64 x 4096 x 4096: 13 -> 11.5 us); over
+// a short one the second kernel costs more than it saves (100 x 1000 x 1000: 6.0 -> 6.9 us).
 W8Plan w8_plan(int M, int N, int K) {
   auto tiles = [&](int kind) {
     return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
   };
   if (M <= 32) return W8Plan{0, (N + 15) / 16, 1};
+  struct Cost {
+    int slots;
+    double full, one, fixed;
+  };
+  constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.5}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
   const int cus = compute_units();
-  if (tiles(3) >= cus * 3 / 4) return W8Plan{3, tiles(3), 1};
-  if (tiles(2) >= cus) return W8Plan{2, tiles(2), 1};
-  const int stages = (K + 127) / 128 * 2;
-  const int t = tiles(1);
-  const int splits = max(1, min(min(8, stages / 8), (2 * cus + t - 1) / t));
-  return W8Plan{1, t, splits};
+  int best = 1;
+  double least = 0.0;
+  for (int kind = 1; kind < kKinds; ++kind) {
+    const Cost& c = cost[kind];
+    const int64_t per = ((int64_t)tiles(kind) + cus - 1) / cus;     // workgroups of the busiest unit
+    const int64_t full = per / c.slots, rest = per % c.slots;
+    const double t = 1e-3 * K * (full * c.full + (rest ? c.one : 0.0)) + (full + (rest ? 1 : 0)) * c.fixed;
+    if (kind == 1 || t < least) {
+      least = t;
+      best = kind;
+    }
+  }
+  const int t = tiles(best), stages = (K + 127) / 128;
+  const int splits = best == 1 && (stages >= 48 ? 2 : 8) * t <= cus && stages >= 24 ? min(min(4, cus / t), stages / 12) : 1;
+  return W8Plan{best, t, splits};
 }
 
 int64_t w8_workspace_bytes(const W8Plan& p) {

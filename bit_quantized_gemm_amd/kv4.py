@@ -19,7 +19,7 @@ from typing import NamedTuple
 
 import bit_quantized_gemm_amd as _bq
 
-from .w8a8 import check_device, check_rows, empty, float_type, on_device
+from .w8a8 import check_device, check_rows, empty, fast_device, float_type, on_device
 
 __all__ = ["KV4Cache", "kv4_cache", "atom_kv4_append", "atom_kv4_read", "atom_kv4_attention",
            "atom_kv4_attention_workspace_bytes"]
@@ -90,6 +90,34 @@ def _cache(cache, more=()):
     return _CCache(p[0], p[1], p[2], p[3], pages, page, heads, 2 * half), p[4:]
 
 
+def _fast_cache(cache, d):
+    """The C struct of a cache of well-formed tensors on device d, else None."""
+    torch = _bq._torch()
+    try:
+        k, k_par, v, v_par = cache
+        pages, heads, page, half = k.shape
+        par, u8, f16 = (pages, heads, page, 2), torch.uint8, torch.float16
+        if (half in (32, 64, 128) and page in (16, 32, 64, 128, 256) and 1 <= heads <= 1024 and pages
+                and k.dtype is u8 and v.dtype is u8 and k_par.dtype is f16 and v_par.dtype is f16
+                and v.shape == (pages, heads, page >> 2, half >> 1, 8) and k_par.shape == par and v_par.shape == par
+                and k.is_contiguous() and k_par.is_contiguous() and v.is_contiguous() and v_par.is_contiguous()
+                and k.get_device() == d and k_par.get_device() == d and v.get_device() == d and v_par.get_device() == d):
+            return _CCache(k.data_ptr(), k_par.data_ptr(), v.data_ptr(), v_par.data_ptr(), pages, page, heads, 2 * half)
+    except (AttributeError, TypeError, ValueError):
+        pass
+    return None
+
+
+def _fast_rows(t, heads, dim, dtype, d):
+    """The row distance of well-formed [tokens, heads, dim] rows on device d, else 0."""
+    s = t.stride()
+    inner = heads * dim
+    if (t.dtype is dtype and s[2] == 1 and (s[1] == dim or heads == 1) and t.get_device() == d
+            and (s[0] >= inner or t.shape[0] == 1)):
+        return s[0] if t.shape[0] > 1 else inner
+    return 0
+
+
 def _same_device(t, name, cache):
     check_device(t, name)
     if t.get_device() != cache[0].get_device():
@@ -107,6 +135,20 @@ def atom_kv4_append(K, V, slots, cache, stream=None):
     apart) into the cache's slots (int64 [tokens]: page * page size + place; one outside the cache, such as
     -1, skips its token).  Two tokens of one call must not share a slot."""
     torch = _bq._torch()
+    T = torch.Tensor
+    if stream is None and type(K) is T and type(V) is T and type(slots) is T and K.is_cuda and K.dim() == 3:
+        d, t = fast_device(K), K.dtype
+        c = _fast_cache(cache, d) if d >= 0 and (t is torch.float16 or t is torch.bfloat16) else None
+        if (c is not None and K.shape == V.shape == (slots.shape[0], c.heads, c.dim) and slots.dtype is torch.int64
+                and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == d):
+            ks, vs = _fast_rows(K, c.heads, c.dim, t, d), _fast_rows(V, c.heads, c.dim, t, d)
+            if ks and vs:
+                status = _bq.load_library().atom_kv4_append(K.data_ptr(), ks, V.data_ptr(), vs, slots.data_ptr(), K.shape[0],
+                                                            int(t is torch.bfloat16), c,
+                                                            torch._C._cuda_getCurrentRawStream(d))
+                if status:
+                    _bq._check(status, "atom_kv4_append")
+                return
     n = _tokens(slots)
     kind = float_type(K, "K")
     if float_type(V, "V") != kind:
@@ -125,6 +167,19 @@ def atom_kv4_read(cache, slots, dtype=None, K=None, V=None, stream=None):
     """(K, V) [tokens, heads, dim] that the codes in `slots` stand for, in `dtype` (default fp16, or K's);
     zeros for a slot outside the cache."""
     torch = _bq._torch()
+    if stream is None and K is None and V is None and type(slots) is torch.Tensor and slots.is_cuda:
+        d = fast_device(slots)
+        t = torch.float16 if dtype is None else dtype
+        c = _fast_cache(cache, d) if d >= 0 and (t is torch.float16 or t is torch.bfloat16) else None
+        if c is not None and slots.dtype is torch.int64 and slots.dim() == 1 and slots.is_contiguous():
+            n, device = slots.shape[0], slots.device
+            K = torch.empty((n, c.heads, c.dim), dtype=t, device=device)
+            V = torch.empty((n, c.heads, c.dim), dtype=t, device=device)
+            status = _bq.load_library().atom_kv4_read(c, slots.data_ptr(), n, int(t is torch.bfloat16), K.data_ptr(),
+                                                      V.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if status:
+                _bq._check(status, "atom_kv4_read")
+            return K, V
     n = _tokens(slots)
     if dtype is None:
         dtype = K.dtype if K is not None else torch.float16
@@ -162,9 +217,47 @@ def atom_kv4_attention(Q, cache, table, lens, q_start, scale=None, max_len=None,
     one that sees none gets zeros, rows outside every sequence are left as they were.  `scale` defaults
     to dim ** -0.5.  `max_len` and `max_q` bound the lengths and query counts on the host (by default what
     the table and Q can hold; tighter bounds choose a better launch): tokens and queries behind them are
-    left out.  `workspace`: 1-D uint8 of ``atom_kv4_attention_workspace_bytes`` bytes (calls that may overlap need one each), else a torch buffer
-    is taken for the call when one is needed."""
+    left out.  `workspace`: 1-D uint8 of ``atom_kv4_attention_workspace_bytes`` bytes (calls that may overlap
+    need one each), else a torch buffer is taken for the call when one is needed."""
     torch = _bq._torch()
+    T = torch.Tensor
+    if (stream is None and type(Q) is T and type(table) is T and type(lens) is T and type(q_start) is T and Q.is_cuda
+            and Q.dim() == 3 and table.dim() == 2):
+        d, t = fast_device(Q), Q.dtype
+        c = _fast_cache(cache, d) if d >= 0 and (t is torch.float16 or t is torch.bfloat16) else None
+        total, q_heads, dim = Q.shape
+        batch, width = table.shape
+        i32 = torch.int32
+        if (c is not None and total and dim == c.dim and q_heads >= c.heads and q_heads % c.heads == 0
+                and table.dtype is i32 and lens.dtype is i32 and q_start.dtype is i32 and batch and width
+                and lens.shape == (batch,) and q_start.shape == (batch + 1,) and table.is_contiguous()
+                and lens.is_contiguous() and q_start.is_contiguous() and table.get_device() == d
+                and lens.get_device() == d and q_start.get_device() == d
+                and (out is None or type(out) is T and out.dtype is t and out.shape == Q.shape and out.is_contiguous()
+                     and out.get_device() == d)
+                and (workspace is None or type(workspace) is T and workspace.dtype is torch.uint8
+                     and workspace.dim() == 1 and workspace.is_contiguous() and workspace.get_device() == d)):
+            qs = _fast_rows(Q, q_heads, dim, t, d)
+            if qs:
+                capacity = width * c.page
+                max_len = capacity if max_len is None else max(1, min(int(max_len), capacity))
+                max_q = total if max_q is None else max(1, min(int(max_q), total))
+                if out is None:
+                    out = torch.empty((total, q_heads, dim), dtype=t, device=Q.device)
+                if workspace is None:
+                    have = _attention_bytes(total, q_heads, c.heads, dim, batch, max_q, max_len)
+                    if have:
+                        workspace = torch.empty(have, dtype=torch.uint8, device=Q.device)
+                else:
+                    have = workspace.numel()
+                status = _bq.load_library().atom_kv4_attention(
+                    Q.data_ptr(), qs, c, table.data_ptr(), width, lens.data_ptr(), q_start.data_ptr(), total, q_heads,
+                    batch, max_q, max_len, dim ** -0.5 if scale is None else float(scale), int(t is torch.bfloat16),
+                    out.data_ptr(), None if workspace is None else workspace.data_ptr(), have,
+                    torch._C._cuda_getCurrentRawStream(d))
+                if status:
+                    _bq._check(status, "atom_kv4_attention")
+                return out
     if getattr(Q, "dim", lambda: -1)() != 3:
         raise _bq.AtomError("Q must be a 3-D tensor")
     kind = float_type(Q, "Q")
