@@ -48,6 +48,11 @@ struct Args {
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }   // 1 ulp; 2^-inf = 0
 __device__ __forceinline__ float max3(float a, float b, float c) { return __builtin_fmaxf(__builtin_fmaxf(a, b), c); }
 
+template <int B>
+struct Half {
+  static constexpr int value = B;
+};
+
 // max over lanes l, l ^ 32 and (kAll) l ^ 16 of a wave
 template <bool kAll>
 __device__ __forceinline__ float join_max(float x) {
@@ -75,7 +80,7 @@ __device__ __forceinline__ h8v query_operand(const float (&x)[8], float f) {
 }
 
 // A query row spread over the lanes that share column l: its operands, and the constants of its scores.
-template <class T, int WORDS, bool kAll>
+template <class T, int WORDS>
 __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v (&op)[WORDS], float& sum, float& c1) {
   u32x4 raw[WORDS];
 #pragma unroll
@@ -85,7 +90,7 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
   for (int w = 0; w < WORDS; ++w)
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1)));
-  top = join_max<kAll>(top);
+  top = join_max<true>(top);
   const int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // floor(log2 top); -127 for 0, 128 for inf
   const int e = max(-100, min(100, ex == 128 ? 0 : 13 - ex));
   const float f = __builtin_ldexpf(1.0f, e);
@@ -99,17 +104,10 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += x[i] * f;
   }
-  sum = join_sum<kAll>(s) * 0x1p-24f;
+  sum = join_sum<true>(s) * 0x1p-24f;
   // positive and finite, so that it keeps the scores' order and -inf stays -inf
   c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(scale * kLog2e, 24 - e), 1e-37f), 3e38f);
 }
-
-// Running statistics of one column's sums.
-struct Stat {
-  float m;       // the largest y = score / c1 seen (or -inf)
-  float ref;     // what is subtracted in the exponent: c1 * m + E (0 while m = -inf)
-  float l;       // this lane's part of sum p 2^-E
-};
 
 __device__ __forceinline__ float low_half(uint32_t w) { return elem<Fp16>(w, 0); }
 __device__ __forceinline__ float high_half(uint32_t w) { return elem<Fp16>(w, 1); }
@@ -120,15 +118,16 @@ __device__ __forceinline__ float exponent_of(uint32_t word) {
 }
 
 // ------------------------------------------------------------------ few query rows: bound by the cache's bytes
-// One workgroup: a chunk of one sequence's tokens in one kv head against NR * 16 query rows.  Its four
-// waves take turns at units of 32 tokens, loaded straight into registers (16 bytes a lane), the next
-// unit's while the current one is multiplied, and join their sums at the end through LDS.
-template <class T, int D, int NR>
-__global__ __launch_bounds__(256) void decode_kernel(Args a) {
+// One workgroup: a chunk of one sequence's tokens in one kv head against 16 query rows.  Its WAVES waves
+// take turns at units of 32 tokens, loaded straight into registers (16 bytes a lane), and join their sums at the end
+// through LDS.  A unit's keys are replaced by the next unit's as soon as the score product has read them, its values
+// after theirs: one unit of registers, so that four waves fit a SIMD (D = 128) and hide each other's latency.
+template <class T, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 2 : 4))) void decode_kernel(Args a) {
   constexpr int W = D / 32;                  // words of codes a lane holds of a 16-token tile: keys and values
   constexpr int NT = D / 16;                 // 16-channel tiles of the output
-  __shared__ float sm[4][NR * 16], sl[4][NR * 16];
-  __shared__ __attribute__((aligned(16))) f32x4 so[2][NT][64];
+  __shared__ float sm[WAVES][16], sl[WAVES][16];
+  __shared__ __attribute__((aligned(16))) f32x4 so[WAVES / 2][NT][64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, h = lane >> 4;
@@ -139,84 +138,102 @@ __global__ __launch_bounds__(256) void decode_kernel(Args a) {
   const int b = bh / a.heads, head = bh - b * a.heads;
   const kv4::Sequence seq = kv4::sequence(a.q_start[b], a.q_start[b + 1], a.lens[b], a.total_q, a.max_q, a.max_len,
                                           a.width << a.log_page);
-  const int rows = seq.queries * a.group, r0 = tile * NR * 16;
+  const int rows = seq.queries * a.group, r0 = tile * 16;
   if (r0 >= rows) return;
-  const int last = min(r0 + NR * 16, rows) - 1;
+  const int last = min(r0 + 16, rows) - 1;
   const int begin = chunk * a.chunk_tokens;
   const int end = min(begin + a.chunk_tokens, kv4::visible(seq, last / a.group));
   if (chunk > 0 && begin >= end) return;     // the joining kernel leaves such chunks out
   const int all = min(kv4::visible(seq, r0 / a.group), seq.tokens);   // tokens every row of the tile sees
 
-  h8v q[NR][W];
-  float qs[NR], c1[NR];
-  int limit[NR];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int r = min(r0 + 16 * n + l16, rows - 1), i = r / a.group;
-    const uint16_t* src = a.q + (int64_t)(seq.first + i) * a.q_stride + (int64_t)(head * a.group + r - i * a.group) * D;
-    load_query<T, W, true>(src + 8 * W * h, a.scale, q[n], qs[n], c1[n]);
-    limit[n] = kv4::visible(seq, i);
-  }
-
-  struct Raw {
-    uint32_t k[2][W], v[2][W];
-    u32x4 kp[2], vp[2];
-  };
+  // Addresses: row of the first token of each 16-token tile of a unit (units start at multiples of 32 tokens).
   const int32_t* table = a.table + (int64_t)b * a.width;
-  auto load = [&](Raw& x, int base) __attribute__((always_inline)) {
+  auto row_of = [&](int tok) __attribute__((always_inline)) {
+    const int page = kv4::page_id(table[kv4::table_column(tok, a.log_page, a.width)], a.pages);
+    return kv4::row_index(page, head, a.heads, a.log_page, tok & ((1 << a.log_page) - 1));
+  };
+  struct Rows {
+    int64_t r[2];
+  };
+  auto rows_of = [&](int base) __attribute__((always_inline)) {
+    Rows x;
+    x.r[0] = row_of(base);
+    x.r[1] = a.log_page >= 5 ? x.r[0] + 16 : row_of(base + 16);
+    return x;
+  };
+  uint32_t k[2][W], v[2][W];
+  u32x4 kp[2], vp[2];
+  auto words = [&](uint32_t (&x)[W], const uint32_t* src) __attribute__((always_inline)) {
+    if constexpr (W == 2) {
+      const u32x2 y = *reinterpret_cast<const u32x2*>(src);
+      x[0] = y[0], x[1] = y[1];
+    } else {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int tok = base + 16 * t;
-      const int page = kv4::page_id(table[kv4::table_column(tok, a.log_page, a.width)], a.pages);
-      const int64_t row = kv4::row_index(page, head, a.heads, a.log_page, tok & ((1 << a.log_page) - 1));
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(a.k + row * (D / 2)) + l16 * (D / 8) + h * W;
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + row * (D / 2)) + h * (D / 2) + l16 * W;
-      if constexpr (W == 2) {
-        const u32x2 kk = *reinterpret_cast<const u32x2*>(k), vv = *reinterpret_cast<const u32x2*>(v);
+      for (int g = 0; g < W; g += 4) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(src + g);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) x.k[t][j] = kk[j], x.v[t][j] = vv[j];
-      } else {
-#pragma unroll
-        for (int g = 0; g < W / 4; ++g) {
-          const u32x4 kk = *reinterpret_cast<const u32x4*>(k + 4 * g), vv = *reinterpret_cast<const u32x4*>(v + 4 * g);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x.k[t][4 * g + j] = kk[j], x.v[t][4 * g + j] = vv[j];
-        }
+        for (int j = 0; j < 4; ++j) x[g + j] = y[j];
       }
-      x.kp[t] = *reinterpret_cast<const u32x4*>(a.k_par + row + 4 * h);
-      x.vp[t] = *reinterpret_cast<const u32x4*>(a.v_par + row + 4 * h);
     }
   };
+  const int k_off = l16 * (D / 8) + h * W, v_off = h * (D / 2) + l16 * W;
+  auto load_keys = [&](const Rows& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) words(k[t], reinterpret_cast<const uint32_t*>(a.k + r.r[t] * (D / 2)) + k_off);
+  };
+  auto load_key_parameters = [&](const Rows& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) kp[t] = *reinterpret_cast<const u32x4*>(a.k_par + r.r[t] + 4 * h);
+  };
+  auto load_values = [&](const Rows& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      words(v[t], reinterpret_cast<const uint32_t*>(a.v + r.r[t] * (D / 2)) + v_off);
+      vp[t] = *reinterpret_cast<const u32x4*>(a.v_par + r.r[t] + 4 * h);
+    }
+  };
+  int base = begin + 32 * wave;
+  if (base < end) {
+    const Rows r = rows_of(base);
+    load_keys(r);
+    load_key_parameters(r);
+    load_values(r);
+  }
 
-  f32x4 o[NR][NT], zs[NR];
-  Stat st[NR];
+  h8v q[W];
+  float qs, c1;
+  const int row = min(r0 + l16, rows - 1), qi = row / a.group;
+  load_query<T, W>(a.q + (int64_t)(seq.first + qi) * a.q_stride + (int64_t)(head * a.group + row - qi * a.group) * D + 8 * W * h,
+                   a.scale, q, qs, c1);
+  const int limit = kv4::visible(seq, qi);
+
+  f32x4 o[NT], zs = {};
+  float m = kNegInf, ref = 0.0f, l = 0.0f;   // the largest y = score / c1 so far; c1 m + E; this lane's part of sum p 2^-E
   uint32_t top_v = 0;                        // parameter word of the largest value scale so far (E of its high half)
   float E = -24.0f;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    zs[n] = f32x4{};
-#pragma unroll
-    for (int i = 0; i < NT; ++i) o[n][i] = f32x4{};
-    st[n] = Stat{kNegInf, 0.0f, 0.0f};
-  }
+  for (int i = 0; i < NT; ++i) o[i] = f32x4{};
 
-  Raw cur, next;
-  int base = begin + 32 * wave;
-  if (base < end) load(cur, base);
-  for (; base < end; base += 128) {
-    if (base + 128 < end) load(next, base + 128);
+  for (; base < end; base += 32 * WAVES) {
+    const Rows next = rows_of(min(base + 32 * WAVES, end - 1) & ~31);    // behind the last unit: in the chunk, unused
+    f32x4 s[2] = {};
+#pragma unroll
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(unpack_keys(k[t][w]), q[w], s[t], 0, 0, 0);
+    load_keys(next);
     uint32_t word = 0;
     if (base + 32 > seq.tokens) {            // what lies behind the sequence's end is no number
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (base + 16 * t + 4 * h + r >= seq.tokens) cur.kp[t][r] = cur.vp[t][r] = 0;
+          if (base + 16 * t + 4 * h + r >= seq.tokens) kp[t][r] = vp[t][r] = 0;
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) word = max(word, cur.vp[t][r]);
+      for (int r = 0; r < 4; ++r) word = max(word, vp[t][r]);
     const bool raise_v = __any(word > (top_v | 0xFFFFu));
     if (raise_v) {
       word = max(word, (uint32_t)__shfl_xor((int)word, 16));
@@ -225,51 +242,37 @@ __global__ __launch_bounds__(256) void decode_kernel(Args a) {
     }
     const float newE = raise_v ? exponent_of(top_v) : E;
 
-    h8v p[NR];
-    const bool masked = base + 32 > all;
+    float y[8], top = kNegInf;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      f32x4 s[2] = {};
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t par = kp[j >> 2][j & 3];
+      y[j] = __builtin_fmaf(-low_half(par), qs, s[j >> 2][j & 3]) * high_half(par);
+    }
+    load_key_parameters(next);
+    if (base + 32 > all) {
 #pragma unroll
-      for (int w = 0; w < W; ++w)
+      for (int j = 0; j < 8; ++j)
+        if (base + 16 * (j >> 2) + 4 * h + (j & 3) >= limit) y[j] = kNegInf;
+    }
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(unpack_keys(cur.k[t][w]), q[n][w], s[t], 0, 0, 0);
-      float y[8], top = kNegInf;
+    for (int j = 0; j < 8; j += 2) top = max3(top, y[j], y[j + 1]);
+    if (__any(top > m) || raise_v) {
+      const float new_m = __builtin_fmaxf(m, join_max<true>(top));
+      const float new_ref = new_m == kNegInf ? 0.0f : __builtin_fmaf(c1, new_m, newE);
+      const float f = m == kNegInf ? 0.0f : exp2_fast(ref - new_ref);
+      m = new_m;
+      ref = new_ref;
+      l *= f;
+      zs *= f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < NT; ++i) o[i] *= f;
+    }
+    h8v p;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t par = cur.kp[t][r];
-          y[4 * t + r] = __builtin_fmaf(-low_half(par), qs[n], s[t][r]) * high_half(par);
-        }
-      if (masked) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (base + 16 * (j >> 2) + 4 * h + (j & 3) >= limit[n]) y[j] = kNegInf;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) top = max3(top, y[j], y[j + 1]);
-      if (__any(top > st[n].m) || raise_v) {
-        const float m = __builtin_fmaxf(st[n].m, join_max<true>(top));
-        const float ref = m == kNegInf ? 0.0f : __builtin_fmaf(c1[n], m, newE);
-        const float f = st[n].m == kNegInf ? 0.0f : exp2_fast(st[n].ref - ref);
-        st[n].m = m;
-        st[n].ref = ref;
-        st[n].l *= f;
-        zs[n] *= f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[n][i] *= f;
-      }
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float e = exp2_fast(__builtin_fmaf(y[j], c1[n], -st[n].ref));
-        st[n].l += e;
-        w[j] = e * high_half(cur.vp[j >> 2][j & 3]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) p[n][j] = (_Float16)w[j];
+    for (int j = 0; j < 8; ++j) {
+      const float e = exp2_fast(__builtin_fmaf(y[j], c1, -ref));
+      l += e;
+      p[j] = (_Float16)(e * high_half(vp[j >> 2][j & 3]));
     }
     E = newE;
 
@@ -279,112 +282,105 @@ __global__ __launch_bounds__(256) void decode_kernel(Args a) {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int r = 0; r < 2; ++r)
-        zp[2 * t + r] = __builtin_amdgcn_perm(cur.vp[t][2 * r + 1], cur.vp[t][2 * r], 0x05040100u);
-#pragma unroll
-    for (int n = 0; n < NR; ++n)
-      zs[n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, zp), p[n], zs[n], 0, 0, 0);
+        zp[2 * t + r] = __builtin_amdgcn_perm(vp[t][2 * r + 1], vp[t][2 * r], 0x05040100u);
+    zs = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, zp), p, zs, 0, 0, 0);
 #pragma unroll
     for (int u = 0; u < W / 2; ++u) {
-      const u32x4 lo = {cur.v[0][2 * u], cur.v[0][2 * u + 1], cur.v[1][2 * u], cur.v[1][2 * u + 1]};
+      const u32x4 lo = {v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1]};
       const u32x4 hi = lo >> 8;
       const u32x4 op[4] = {lo & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int n = 0; n < NR; ++n)
-          o[n][4 * u + i] =
-              __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, op[i]), p[n], o[n][4 * u + i], 0, 0, 0);
+        o[4 * u + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, op[i]), p, o[4 * u + i], 0, 0, 0);
     }
-    cur = next;
+    load_values(next);
   }
 
   // Join the waves: everything to the largest reference (log2), then a tree over the sums.
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const float l = join_sum<true>(st[n].l);
-    if (h == 0) {
-      sm[wave][16 * n + l16] = st[n].m == kNegInf ? kNegInf : st[n].ref;
-      sl[wave][16 * n + l16] = l;
-    }
+  l = join_sum<true>(l);
+  if (h == 0) {
+    sm[wave][l16] = m == kNegInf ? kNegInf : ref;
+    sl[wave][l16] = l;
   }
   __syncthreads();
+  float M = kNegInf;
+  l = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float M = kNegInf, l = 0.0f;
+  for (int x = 0; x < WAVES; ++x) M = __builtin_fmaxf(M, sm[x][l16]);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) M = __builtin_fmaxf(M, sm[v][16 * n + l16]);
+  for (int x = 0; x < WAVES; ++x)
+    if (M != kNegInf) l += sl[x][l16] * exp2_fast(sm[x][l16] - M);
+  const float f = M == kNegInf ? 0.0f : exp2_fast(sm[wave][l16] - M);
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (M != kNegInf) l += sl[v][16 * n + l16] * exp2_fast(sm[v][16 * n + l16] - M);
-    const float f = M == kNegInf ? 0.0f : exp2_fast(sm[wave][16 * n + l16] - M);
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int r = 0; r < 4; ++r) o[i][r] = f * __builtin_fmaf(o[i][r], i & 1 ? 0x1p20f : 0x1p24f, -zs[0]);
+  for (int half = WAVES / 2; half; half >>= 1) {
+    if (half < WAVES / 2) __syncthreads();   // the step before has read its buffers
+    if (wave >= half && wave < 2 * half) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        o[n][i][r] = f * __builtin_fmaf(o[n][i][r], i & 1 ? 0x1p20f : 0x1p24f, -zs[n][0]);
-    if (n > 0) __syncthreads();              // the buffers of the row tile before
-    if (wave >= 2)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) so[wave - 2][i][lane] = o[n][i];
-    __syncthreads();
-    if (wave < 2)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) o[n][i] += so[wave][i][lane];
-    __syncthreads();
-    if (wave == 1)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) so[0][i][lane] = o[n][i];
-    __syncthreads();
-    if (wave == 0) {
-#pragma unroll
-      for (int i = 0; i < NT; ++i) o[n][i] += so[0][i][lane];
-      const int r = r0 + 16 * n + l16;
-      if (r < rows) {
-        const int i = r / a.group;
-        const int64_t id = (int64_t)(seq.first + i) * a.q_heads + head * a.group + r - i * a.group;
-        if (a.chunks == 1) {
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-          for (int g = 0; g < 4; ++g)        // register g: channels NT * (4 h + g) .. + NT - 1
-#pragma unroll
-            for (int j = 0; j < NT; j += 4)
-              *reinterpret_cast<u32x2*>(a.out + id * D + NT * (4 * h + g) + j) =
-                  u32x2{pack2<T>(o[n][j][g] * inv, o[n][j + 1][g] * inv),
-                        pack2<T>(o[n][j + 2][g] * inv, o[n][j + 3][g] * inv)};
-        } else {
-          const int64_t all_rows = (int64_t)a.total_q * a.q_heads;
-          float* dst = a.part + (chunk * all_rows + id) * D;
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-#pragma unroll
-            for (int j = 0; j < NT; j += 4)
-              *reinterpret_cast<f32x4*>(dst + NT * (4 * h + g) + j) =
-                  f32x4{o[n][j][g], o[n][j + 1][g], o[n][j + 2][g], o[n][j + 3][g]};
-          if (h == 0) {
-            float* ml = a.part + a.chunks * all_rows * D + (chunk * all_rows + id) * 2;
-            ml[0] = M;
-            ml[1] = l;
-          }
-        }
-      }
+      for (int i = 0; i < NT; ++i) so[wave - half][i][lane] = o[i];
     }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[i] += so[wave][i][lane];
+    }
+  }
+  if (wave > 0 || r0 + l16 >= rows) return;
+  // register g of o[j]: channel NT * (4 h + g) + j
+  const int64_t id = (int64_t)(seq.first + qi) * a.q_heads + head * a.group + row - qi * a.group;
+  if (a.chunks == 1) {
+    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int j = 0; j < NT; j += 4)
+        *reinterpret_cast<u32x2*>(a.out + id * D + NT * (4 * h + g) + j) =
+            u32x2{pack2<T>(o[j][g] * inv, o[j + 1][g] * inv), pack2<T>(o[j + 2][g] * inv, o[j + 3][g] * inv)};
+    return;
+  }
+  const int64_t all_rows = (int64_t)a.total_q * a.q_heads;
+  float* dst = a.part + (chunk * all_rows + id) * D;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+#pragma unroll
+    for (int j = 0; j < NT; j += 4)
+      *reinterpret_cast<f32x4*>(dst + NT * (4 * h + g) + j) = f32x4{o[j][g], o[j + 1][g], o[j + 2][g], o[j + 3][g]};
+  if (h == 0) {
+    float* ml = a.part + a.chunks * all_rows * D + (chunk * all_rows + id) * 2;
+    ml[0] = M;
+    ml[1] = l;
   }
 }
 
 // ------------------------------------------------------------------ many query rows: bound by the vector ALUs and matrix cores
-// One workgroup: 128 query rows of one sequence and kv head, 32 a wave, against a chunk of the tokens in
-// tiles of 64.  The packed tile is staged in LDS once for the four waves (two buffers, the next tile's
-// loads in registers meanwhile); each wave unpacks it for itself.
+// One workgroup of four waves: 128 query rows of one sequence and kv head, 32 a wave, against a chunk of the tokens in
+// tiles of 64.  A tile is unpacked once for all waves on its way into LDS, as fp16 operands with the zero point already
+// taken off (q - zero is a small integer: its multiple of 2^-24 is exact), two buffers, the next tile's loads in registers
+// meanwhile.  That leaves a wave per score one fma (scale and running maximum), half a maximum, the exponential, the
+// sum, the value scale and half a conversion.
+//
+// LDS.  Keys: row of a token, 16-byte chunk c (a word's eight channels) at position c ^ (token & 15), D = 64: c ^ (token / 2 & 7).  Values: row of a
+// channel, 64 tokens in the order in which a lane of the score product holds them (16 at a time: 0-3, 8-11 for
+// lanes 0-31, 4-7, 12-15 for the others); chunk c at position c ^ (d & 7) ^ (d / 8 & 7).  Sixteen lanes of a 16-byte read hit all banks.
+//
+// The scale of the queries (a power of two) is one for the workgroup, so that a token's factor c1 * s can be made when it
+// is staged.  Rows far smaller than the largest one keep an absolute error of 2^-31 of the largest row's scores.
+//
+// Running maximum: ref = m + E with m the largest score of the wave's first tile, raised only when some score of the
+// wave exceeds it by 8 (weights are at most 2^8 then) or some value scale exceeds 2^E.
 template <class T, int D>
-__global__ __launch_bounds__(256) void prompt_kernel(Args a) {
-  constexpr int S = D / 16;                  // K = 16 slices of the key product; a lane's words of a token row
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void prompt_kernel(Args a) {
+  constexpr int NW = 4;                      // waves
+  constexpr int S = D / 16;                  // K = 16 slices of the key product
   constexpr int NT = D / 32;                 // 32-channel tiles of the output
-  constexpr int kRow = D / 2 + 16;           // staged key row: an odd number of 16-byte slots
-  constexpr int PW = D / 32;                 // words of keys, and of values, that a thread stages
   constexpr int kTile = 64;
-  __shared__ __attribute__((aligned(16))) uint8_t lk[2][kTile * kRow];
-  __shared__ __attribute__((aligned(16))) uint8_t lv[2][kTile * D / 2];
-  __shared__ __attribute__((aligned(16))) uint32_t lp[2][2][kTile];        // key, then value parameters
+  constexpr int W = D / (8 * NW);            // words of key codes, and of value codes, that a thread stages
+  constexpr int kLds = kTile * D * 2;        // bytes of a tile's keys, or values, in LDS
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][kLds];
+  __shared__ __attribute__((aligned(16))) float lf[2][2][kTile];           // c1 * key scale, value scale
+  __shared__ float lmax[NW];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -396,213 +392,371 @@ __global__ __launch_bounds__(256) void prompt_kernel(Args a) {
   const int b = bh / a.heads, head = bh - b * a.heads;
   const kv4::Sequence seq = kv4::sequence(a.q_start[b], a.q_start[b + 1], a.lens[b], a.total_q, a.max_q, a.max_len,
                                           a.width << a.log_page);
-  const int rows = seq.queries * a.group, r0 = tile * 128;
+  const int rows = seq.queries * a.group, r0 = tile * (32 * NW);
   if (r0 >= rows) return;
   const int begin = chunk * a.chunk_tokens;
-  const int end = min(begin + a.chunk_tokens, kv4::visible(seq, (min(r0 + 128, rows) - 1) / a.group));
+  const int end = min(begin + a.chunk_tokens, kv4::visible(seq, (min(r0 + 32 * NW, rows) - 1) / a.group));
   if (chunk > 0 && begin >= end) return;
 
-  const int row = r0 + 32 * wave + l32, qi = min(row, rows - 1) / a.group;
-  const int64_t id = (int64_t)(seq.first + qi) * a.q_heads + head * a.group + min(row, rows - 1) - qi * a.group;
-  h8v q[S];
-  float qs, c1;
-  load_query<T, S, false>(a.q + (int64_t)(seq.first + qi) * a.q_stride +
-                              (int64_t)(head * a.group + min(row, rows - 1) - qi * a.group) * D + 8 * S * h,
-                          a.scale, q, qs, c1);
+  const int row = min(r0 + 32 * wave + l32, rows - 1), qi = row / a.group;
   const int limit = kv4::visible(seq, qi);
-  // of this wave's rows: the tokens that all of them see, and that any of them sees
-  const int w0 = min(r0 + 32 * wave, rows - 1), w1 = min(r0 + 32 * wave + 31, rows - 1);
-  const int all = min(kv4::visible(seq, w0 / a.group), seq.tokens);
-  const int any = r0 + 32 * wave < rows ? min(end, kv4::visible(seq, w1 / a.group)) : 0;
+  // the tokens that all of this wave's rows see
+  const int all = min(kv4::visible(seq, min(r0 + 32 * wave, rows - 1) / a.group), seq.tokens);
 
-  // staging: thread t carries PW words of token t / 4's keys, PW words of 4-token block t / 16's values, and
-  // (t < 128) one parameter word
+  // ---- queries: lane half h holds words 2 s + h of its row
+  h8v q[S];
+  float c1;
+  {
+    const uint16_t* src = a.q + (int64_t)(seq.first + qi) * a.q_stride + (int64_t)(head * a.group + row - qi * a.group) * D + 8 * h;
+    u32x4 raw[S];
+#pragma unroll
+    for (int w = 0; w < S; ++w) raw[w] = *reinterpret_cast<const u32x4*>(src + 16 * w);
+    float top = 0.0f;
+#pragma unroll
+    for (int w = 0; w < S; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {          // the largest finite element
+        const float x = __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1));
+        top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+      }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) lmax[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < NW; ++v) top = __builtin_fmaxf(top, lmax[v]);
+    const int e = max(-100, min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23)));   // 13 - floor(log2 top)
+    const float f = __builtin_ldexpf(1.0f, e);
+#pragma unroll
+    for (int w = 0; w < S; ++w) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
+      q[w] = query_operand(x, f);
+    }
+    c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e, 24 - e), 1e-37f), 3e38f);
+  }
+
+  auto key_swizzle = [](int t) { return D == 64 ? (t >> 1) & 7 : t & 15; };   // D = 64: two rows cover the banks
+  // ---- staging: thread t carries words W (t % NW) .. of token t / NW's keys, and words W (t % 4 NW) .. of 4-token
+  // block t / (4 NW)'s values
   const int32_t* table = a.table + (int64_t)b * a.width;
   auto row_of = [&](int tok) __attribute__((always_inline)) {
     const int page = kv4::page_id(table[kv4::table_column(tok, a.log_page, a.width)], a.pages);
     return kv4::row_index(page, head, a.heads, a.log_page, tok & ((1 << a.log_page) - 1));
   };
-  uint32_t gk[PW], gv[PW], gp = 0;
-  auto copy = [&](uint32_t* dst, const uint32_t* src) __attribute__((always_inline)) {
-    if constexpr (PW == 2) {
-      *reinterpret_cast<u32x2*>(dst) = *reinterpret_cast<const u32x2*>(src);
-    } else {
+  const int kt = tid / NW, kp = tid % NW, vb = tid / (4 * NW), vp = tid % (4 * NW);
+  uint32_t gk[W], gv[W], gkp;
+  u32x4 gvp;
+  auto get = [&](uint32_t (&x)[W], const uint32_t* src) __attribute__((always_inline)) {
+    if constexpr (W >= 4) {
 #pragma unroll
-      for (int g = 0; g < PW; g += 4) *reinterpret_cast<u32x4*>(dst + g) = *reinterpret_cast<const u32x4*>(src + g);
-    }
-  };
-  auto fetch = [&](int base) __attribute__((always_inline)) {
-    const uint32_t* k = reinterpret_cast<const uint32_t*>(a.k + row_of(base + tid / 4) * (D / 2)) + (tid & 3) * PW;
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v + row_of(base + tid / 16 * 4) * (D / 2)) + (tid & 15) * PW;
+      for (int g = 0; g < W; g += 4) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(src + g);
 #pragma unroll
-    for (int g = 0; g < PW; g += PW == 2 ? 2 : 4) {
-      if constexpr (PW == 2) {
-        const u32x2 kk = *reinterpret_cast<const u32x2*>(k), vv = *reinterpret_cast<const u32x2*>(v);
-        gk[0] = kk[0], gk[1] = kk[1], gv[0] = vv[0], gv[1] = vv[1];
-      } else {
-        const u32x4 kk = *reinterpret_cast<const u32x4*>(k + g), vv = *reinterpret_cast<const u32x4*>(v + g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) gk[g + j] = kk[j], gv[g + j] = vv[j];
+        for (int j = 0; j < 4; ++j) x[g + j] = v[j];
       }
-    }
-    if (tid < 128) {
-      const int tok = base + (tid & 63);
-      gp = (tid < 64 ? a.k_par : a.v_par)[row_of(tok)];
-      if (tok >= seq.tokens) gp = 0;         // what lies behind the sequence's end is no number
+    } else if constexpr (W == 2) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(src);
+      x[0] = v[0], x[1] = v[1];
+    } else {
+      x[0] = *src;
     }
   };
-  auto store = [&](int buf) __attribute__((always_inline)) {
-    copy(reinterpret_cast<uint32_t*>(&lk[buf][(tid / 4) * kRow]) + (tid & 3) * PW, gk);
-    copy(reinterpret_cast<uint32_t*>(&lv[buf][0]) + tid * PW, gv);
-    if (tid < 128) lp[buf][tid >> 6][tid & 63] = gp;
+  // Pages of 64 tokens or more hold a whole tile: one page for all threads, its id read a tile ahead.
+  const bool whole = a.log_page >= 6;
+  auto page_of = [&](int tok) __attribute__((always_inline)) {
+    return table[kv4::table_column(tok, a.log_page, a.width)];
+  };
+  int entry = whole ? page_of(begin) : 0;
+  auto fetch = [&](int base) __attribute__((always_inline)) {
+    if (whole) {
+      const int64_t row = kv4::row_index(kv4::page_id(__builtin_amdgcn_readfirstlane(entry), a.pages), head, a.heads, a.log_page,
+                                         base & ((1 << a.log_page) - 1));
+      get(gk, reinterpret_cast<const uint32_t*>(a.k + row * (D / 2)) + (kt * (D / 8) + W * kp));
+      get(gv, reinterpret_cast<const uint32_t*>(a.v + row * (D / 2)) + (vb * (D / 2) + W * vp));
+      gkp = (a.k_par + row)[kt];
+      gvp = *reinterpret_cast<const u32x4*>(a.v_par + row + 4 * vb);
+      entry = page_of(base + kTile);
+    } else {
+      const int64_t kr = row_of(base + kt), vr = row_of(base + 4 * vb);
+      get(gk, reinterpret_cast<const uint32_t*>(a.k + kr * (D / 2)) + W * kp);
+      get(gv, reinterpret_cast<const uint32_t*>(a.v + vr * (D / 2)) + W * vp);
+      gkp = a.k_par[kr];
+      gvp = *reinterpret_cast<const u32x4*>(a.v_par + vr);
+    }
+  };
+  auto half2 = [](uint32_t w) { return __builtin_bit_cast(h2v, w); };
+  const h2v kTiny = {(_Float16)0x1p-24f, (_Float16)0x1p-24f}, k16 = {(_Float16)16.0f, (_Float16)16.0f};
+  // the pairs of halves (q - zero) 2^-24 in the two low nibbles of each half-word, the second 16 times as large
+  auto unpack = [&](uint32_t w, h2v z) __attribute__((always_inline)) {
+    return u32x2{__builtin_bit_cast(uint32_t, half2(w & 0x000F000Fu) - z),
+                 __builtin_bit_cast(uint32_t, half2(w & 0x00F000F0u) - z * k16)};
+  };
+  // Staging in steps that fill the gaps between matrix products: parameters and keys first, then the values.
+  uint8_t* const skeys = &lds[0][0][0] + kt * (D * 2);
+  uint8_t* const svals = &lds[0][1][0] + 8 * ((vb >> 1) & 1);
+  const int vchunk = 2 * (vb >> 2) + (vb & 1);           // 16-byte chunk of a channel's row that holds the block's tokens
+  h2v kz, vz[2];
+  auto stage_parameters = [&](int buf, int base) __attribute__((always_inline)) {
+    uint32_t par = gkp;
+    u32x4 vpar = gvp;
+    if (base + kTile > seq.tokens) {                     // what lies behind the sequence's end is no number
+      if (base + kt >= seq.tokens) par = 0;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (base + 4 * vb + r >= seq.tokens) vpar[r] = 0;
+    }
+    kz = half2(__builtin_amdgcn_perm(par, par, 0x01000100u)) * kTiny;
+    lf[buf][0][kt] = c1 * high_half(par);                // the same from every thread of the token
+    vz[0] = half2(__builtin_amdgcn_perm(vpar[1], vpar[0], 0x05040100u)) * kTiny;
+    vz[1] = half2(__builtin_amdgcn_perm(vpar[3], vpar[2], 0x05040100u)) * kTiny;
+    *reinterpret_cast<f32x4*>(&lf[buf][1][4 * vb]) =
+        f32x4{high_half(vpar[0]), high_half(vpar[1]), high_half(vpar[2]), high_half(vpar[3])};
+  };
+  auto stage_keys = [&](int buf, int w) __attribute__((always_inline)) {           // w < W
+    const u32x2 lo = unpack(gk[w], kz), hi = unpack(gk[w] >> 8, kz);
+    *reinterpret_cast<u32x4*>(skeys + buf * (2 * kLds) + (((W * kp + w) ^ key_swizzle(kt)) << 4)) =
+        u32x4{lo[0], lo[1], hi[0], hi[1]};
+  };
+  auto stage_values = [&](int buf, int n) __attribute__((always_inline)) {         // n < W: two channels of a quad
+    auto place = [&](int d) __attribute__((always_inline)) {
+      return svals + buf * (2 * kLds) + d * 128 + ((vchunk ^ (d & 7) ^ ((d >> 3) & 7)) << 4);
+    };
+    if constexpr (W == 1) {                              // one pair of tokens of a whole quad
+      const int pair = vp & 1, d = 4 * (vp >> 1);
+      const u32x2 lo = unpack(gv[0], pair ? vz[1] : vz[0]), hi = unpack(gv[0] >> 8, pair ? vz[1] : vz[0]);
+      const uint32_t x[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(place(d + i) + 4 * pair) = x[i];
+    } else {
+      const int g = n >> 1, i = 2 * (n & 1), d = 4 * (W / 2 * vp + g) + i;
+      const u32x2 x = unpack(gv[2 * g] >> (4 * i), vz[0]), z = unpack(gv[2 * g + 1] >> (4 * i), vz[1]);
+      *reinterpret_cast<u32x2*>(place(d)) = u32x2{x[0], z[0]};
+      *reinterpret_cast<u32x2*>(place(d + 1)) = u32x2{x[1], z[1]};
+    }
   };
 
-  f32x16 o[NT], zs = {};
+  f32x16 o[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x16{};
-  Stat st{kNegInf, 0.0f, 0.0f};
-  uint32_t top_v = 0;
-  float E = -24.0f;
+  float ref = 0.0f, l = 0.0f, E = 0.0f, most = -1.0f;    // most: the largest value scale so far
+  bool first = true;
 
+  // LDS addresses of this lane's operands in buffer 0; other buffers, halves and channels are constants further.
+  const uint8_t* const base0 = &lds[0][0][0];
+  int ka[S], va[4];
+#pragma unroll
+  for (int w = 0; w < S; ++w) ka[w] = l32 * (D * 2) + (((2 * w + h) ^ key_swizzle(l32)) << 4);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) va[x] = kLds + l32 * 128 + (((2 * x + h) ^ (l32 & 7) ^ (l32 >> 3)) << 4);
+  // key operand of slice w of half t; value operand n: 16 tokens n / NT of half t, channels 32 (n % NT) + l32
+  auto key = [&](int buf, int t, int w) __attribute__((always_inline)) {
+    return *reinterpret_cast<const h8v*>(base0 + ka[w] + (buf * 2 * kLds + t * 32 * D * 2));
+  };
+  auto value = [&](int buf, int t, int n) __attribute__((always_inline)) {
+    const int x = n / NT, i = n % NT;
+    return *reinterpret_cast<const h8v*>(base0 + va[2 * (t ^ (i & 1)) + x] + (buf * 2 * kLds + i * 4096));
+  };
+
+  float y[16];
+  h8v p[2], ring[4];
+  f32x16 s;
+  // Masks, and raises the reference where it has to be raised; base: the half tile's first token.
+  auto settle = [&](int buf, int t, int base) __attribute__((always_inline)) {
+    if (base + 32 > all) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (base + 8 * (j >> 2) + 4 * h + (j & 3) >= limit) y[j] = kNegInf;
+    }
+    float top = max3(y[0], y[1], y[2]);
+#pragma unroll
+    for (int j = 3; j < 15; j += 2) top = max3(top, y[j], y[j + 1]);
+    top = __builtin_fmaxf(top, y[15]);
+    const float u = lf[buf][1][32 * t + l32];
+    if (first || __any(top > 8.0f - E || u > most)) {
+      float dE = 0.0f, big = u;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
+      if (big > most) {                      // wave-uniform
+        const float e = (float)max(-24, (int)(__builtin_bit_cast(uint32_t, big) >> 23) - 126);   // big <= 2^e
+        dE = first ? e - E : __builtin_fmaxf(e - E, 0.0f);
+        most = __builtin_ldexpf(1.0f, (int)(E + dE));
+      }
+      const float over = join_max<false>(top) + E;                         // above m
+      const float delta = (first ? (over == kNegInf ? 0.0f : over) : __builtin_fmaxf(over, 0.0f)) + dE;
+      const float f = first ? 0.0f : exp2_fast(-delta);
+      ref += delta;
+      E += dE;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) o[i] *= f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) y[j] -= delta;
+      first = false;
+    }
+  };
+  auto scale4 = [&](const f32x4& f, int g) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) y[4 * g + r] = __builtin_fmaf(s[4 * g + r], f[r], -ref);
+  };
+  // Scores of (buf, t) on the matrix cores while the vector ALUs turn y into the weights of (wbuf, wt).  Every product is a
+  // scheduling region of its own with its share of the rest, operands are read four products ahead; the last reads
+  // are the first operands of the product with the values that follows.
+  f32x4 u[4];
+  // The first reads of scores_and_weights, made before the masks and the reference of the half tile in front (D = 256
+  // has no registers for that).
+  auto read = [&](int buf, int t, int wbuf, int wt) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) ring[w] = key(buf, t, w);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) u[g] = *reinterpret_cast<const f32x4*>(&lf[0][0][0] + (2 * wbuf + 1) * kTile + 32 * wt + 8 * g + 4 * h);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto read_ahead = [&](int buf, int t, int wbuf, int wt) __attribute__((always_inline)) {
+    if (D < 256) read(buf, t, wbuf, wt);
+  };
+  auto scores_and_weights = [&](int buf, int t, int wbuf, int wt) __attribute__((always_inline)) {
+    if (D == 256) read(buf, t, wbuf, wt);
+    s = f32x16{};
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int w = 0; w < S; ++w) {
+      s = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[w & 3], q[w], s, 0, 0, 0);
+      ring[w & 3] = w + 4 < S ? key(buf, t, w + 4 < S ? w + 4 : 0) : value(wbuf, wt, w + 4 - S < 0 ? 0 : w + 4 - S);
+#pragma unroll
+      for (int j = 16 * w / S; j < 16 * (w + 1) / S; ++j) {
+        const float e = exp2_fast(y[j]);
+        l += e;
+        p[j >> 3][j & 7] = (_Float16)(e * u[j >> 2][j & 3]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // The product of the weights with the values of (wbuf, wt) while s is scaled (factors of (buf, t)) and `fill(n)` runs.
+  auto product_and_scale = [&](int wbuf, int wt, int buf, int t, auto fill) __attribute__((always_inline)) {
+    f32x4 f[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) f[g] = *reinterpret_cast<const f32x4*>(&lf[0][0][0] + 2 * buf * kTile + 32 * t + 8 * g + 4 * h);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int n = 0; n < 2 * NT; ++n) {
+      o[n % NT] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[n & 3], p[n / NT], o[n % NT], 0, 0, 0);
+      if (n + 4 < 2 * NT) ring[n & 3] = value(wbuf, wt, n + 4 < 2 * NT ? n + 4 : 0);
+      fill(n);
+      if (n >= 2 * NT - 4) scale4(f[n - (2 * NT - 4)], n - (2 * NT - 4));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // Half tiles in a pipeline: while the matrix cores make the scores of one, the vector ALUs make the weights of the
+  // one before; while its product with the values runs, the next scores are scaled and the next tile is unpacked.
   if (begin < end) {
     fetch(begin);
-    store(0);
+    stage_parameters(0, begin);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      stage_keys(0, w);
+      stage_values(0, w);
+    }
   }
   __syncthreads();
-  int buf = 0;
-  for (int base = begin; base < end; base += kTile, buf ^= 1) {
-    if (base + kTile < end) fetch(base + kTile);
-    if (base < any) {
-      const uint32_t word = lp[buf][1][lane];
-      const bool raise_v = __any(word > (top_v | 0xFFFFu));
-      if (raise_v) {
-        uint32_t w = word;
+  if (begin + kTile < end) fetch(begin + kTile);
+  if (begin < end) {
+    s = f32x16{};
 #pragma unroll
-        for (int d = 32; d; d >>= 1) w = max(w, (uint32_t)__shfl_xor((int)w, d));
-        top_v = max(top_v, w);
-      }
-      const float newE = raise_v ? exponent_of(top_v) : E;
-      float y[32];
+    for (int w = 0; w < S; ++w) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(key(0, 0, w), q[w], s, 0, 0, 0);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x16 s = {};
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(&lk[buf][(32 * t + l32) * kRow]) + h * S;
+    for (int g = 0; g < 4; ++g) scale4(*reinterpret_cast<const f32x4*>(&lf[0][0][8 * g + 4 * h]), g);
+    read_ahead(0, 1, 0, 0);
+    settle(0, 0, begin);
+  }
+  // One tile in buffer B.  What is staged or multiplied behind the last tile repeats what is there and is not used.
+  auto step = [&](auto which, int base) __attribute__((always_inline)) {
+    constexpr int B = decltype(which)::value;
+    scores_and_weights(B, 1, B, 0);
+    product_and_scale(B, 0, B, 1, [&](int n) __attribute__((always_inline)) {
+      if (n == 0) stage_parameters(B ^ 1, base + kTile);
 #pragma unroll
-        for (int w = 0; w < S; w += 4) {
-          const u32x4 kk = *reinterpret_cast<const u32x4*>(k + w);
+      for (int w = 0; w < W; ++w)
+        if (n == w * NT / W + (W <= NT ? 1 : 0)) stage_keys(B ^ 1, w);
+    });
+    __syncthreads();                         // the next tile's keys are there
+    read_ahead(B ^ 1, 0, B, 1);
+    settle(B, 1, base + 32);
+    scores_and_weights(B ^ 1, 0, B, 1);
+    product_and_scale(B, 1, B ^ 1, 0, [&](int n) __attribute__((always_inline)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(unpack_keys(kk[j]), q[w + j], s, 0, 0, 0);
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const u32x4 par = *reinterpret_cast<const u32x4*>(&lp[buf][0][32 * t + 8 * g + 4 * h]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            y[16 * t + 4 * g + r] = __builtin_fmaf(-low_half(par[r]), qs, s[4 * g + r]) * high_half(par[r]);
-        }
-      }
-      if (base + kTile > all) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (base + 32 * (j >> 4) + 8 * ((j >> 2) & 3) + 4 * h + (j & 3) >= limit) y[j] = kNegInf;
-      }
-      float top = kNegInf;
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) top = max3(top, y[j], y[j + 1]);
-      if (__any(top > st.m) || raise_v) {
-        const float m = __builtin_fmaxf(st.m, join_max<false>(top));
-        const float ref = m == kNegInf ? 0.0f : __builtin_fmaf(c1, m, newE);
-        const float f = st.m == kNegInf ? 0.0f : exp2_fast(st.ref - ref);
-        st.m = m;
-        st.ref = ref;
-        st.l *= f;
-        zs *= f;
-#pragma unroll
-        for (int i = 0; i < NT; ++i) o[i] *= f;
-      }
-      E = newE;
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {        // 16 tokens: blocks 4 x + h and 4 x + 2 + h of the 32
-          h8v p;
-          u32x4 zp;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const u32x4 par = *reinterpret_cast<const u32x4*>(&lp[buf][1][32 * t + 16 * x + 8 * g + 4 * h]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const float e = exp2_fast(__builtin_fmaf(y[16 * t + 8 * x + 4 * g + r], c1, -st.ref));
-              st.l += e;
-              p[4 * g + r] = (_Float16)(e * high_half(par[r]));
-            }
-            zp[2 * g] = __builtin_amdgcn_perm(par[1], par[0], 0x05040100u);
-            zp[2 * g + 1] = __builtin_amdgcn_perm(par[3], par[2], 0x05040100u);
-          }
-          zs = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, zp), p, zs, 0, 0, 0);
-          const uint8_t* b0 = &lv[buf][(8 * t + 4 * x + h) * 2 * D];
-          const uint8_t* b1 = b0 + 4 * D;
-          if constexpr (D == 64) {           // half a quad a lane: channels 2 l32, 2 l32 + 1
-            const u32x2 v0 = *reinterpret_cast<const u32x2*>(b0 + 8 * (l32 >> 1));
-            const u32x2 v1 = *reinterpret_cast<const u32x2*>(b1 + 8 * (l32 >> 1));
-            const u32x4 w = u32x4{v0[0], v0[1], v1[0], v1[1]} >> (8 * (l32 & 1));
-            o[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, w & 0x000F000Fu), p, o[0], 0, 0, 0);
-            o[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, w & 0x00F000F0u), p, o[1], 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int u = 0; u < NT / 4; ++u) {
-              const u32x2 v0 = *reinterpret_cast<const u32x2*>(b0 + 8 * ((NT / 4) * l32 + u));
-              const u32x2 v1 = *reinterpret_cast<const u32x2*>(b1 + 8 * ((NT / 4) * l32 + u));
-              const u32x4 lo = {v0[0], v0[1], v1[0], v1[1]}, hi = lo >> 8;
-              const u32x4 op[4] = {lo & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                o[4 * u + i] =
-                    __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8v, op[i]), p, o[4 * u + i], 0, 0, 0);
-            }
-          }
-        }
-    }
-    if (base + kTile < end) store(buf ^ 1);
-    __syncthreads();
+      for (int w = 0; w < W; ++w)
+        if (n == w * NT / W + (W <= NT ? 1 : 0)) stage_values(B ^ 1, w);
+    });
+    read_ahead(B ^ 1, 1, B ^ 1, 0);
+    if (base + kTile < end) settle(B ^ 1, 0, base + kTile);
+    if (base + 2 * kTile < end) fetch(base + 2 * kTile);
+    __syncthreads();                         // its values too, and every wave has read this tile
+  };
+  for (int base = begin; base < end; base += 2 * kTile) {
+    step(Half<0>{}, base);
+    if (base + kTile < end) step(Half<1>{}, base + kTile);
   }
 
-  const float l = join_sum<false>(st.l);
-  if (row >= rows) return;
+  // Register 4 g + r of o[i]: channel 32 i + 8 g + 4 h + r, its codes 16 times too large for odd r.
+  l = join_sum<false>(l);
+  const int64_t id = (int64_t)(seq.first + qi) * a.q_heads + head * a.group + row - qi * a.group;
   const int64_t all_rows = (int64_t)a.total_q * a.q_heads;
-  if (a.chunks > 1 && h == 0) {
-    float* ml = a.part + a.chunks * all_rows * D + (chunk * all_rows + id) * 2;
-    ml[0] = st.m == kNegInf ? kNegInf : st.ref;
-    ml[1] = l;
+  const bool live = r0 + 32 * wave + l32 < rows;
+  if (a.chunks > 1) {
+    if (!live) return;
+    if (h == 0) {
+      float* ml = a.part + a.chunks * all_rows * D + (chunk * all_rows + id) * 2;
+      ml[0] = l > 0.0f || l != l ? ref : kNegInf;
+      ml[1] = l;
+    }
+    float* dst = a.part + (chunk * all_rows + id) * D;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(dst + 32 * i + 8 * g + 4 * h) =
+            f32x4{o[i][4 * g] * 0x1p24f, o[i][4 * g + 1] * 0x1p20f, o[i][4 * g + 2] * 0x1p24f, o[i][4 * g + 3] * 0x1p20f};
+    return;
   }
-  const float inv = a.chunks > 1 ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+  // Out through LDS, a wave's rows in a part of its own, so that rows leave whole (eight-byte pieces of 32 rows a
+  // multiple of 4 KB apart would all go to one channel of the L2).  Piece of 16 bytes c of row r at c ^ (r & 7).
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint8_t* own = lds[0][0] + wave * (32 * D * 2);
+  static_assert(NW * 32 * D * 2 <= sizeof(lds), "the output rows fit the tile buffers");
 #pragma unroll
-  for (int g = 0; g < 16; ++g) {             // register g: channels NT * (8 (g / 4) + 4 h + g % 4) .. + NT - 1
-    const int d = NT * (8 * (g >> 2) + 4 * h + (g & 3));
-    float x[NT];
+  for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int i = 0; i < NT; ++i) x[i] = inv * __builtin_fmaf(o[i][g], i & 1 ? 0x1p20f : 0x1p24f, -zs[0]);
-    if (a.chunks > 1) {
-      float* dst = a.part + (chunk * all_rows + id) * D + d;
-#pragma unroll
-      for (int i = 0; i < NT; i += 2) *reinterpret_cast<float2*>(dst + i) = float2{x[i], x[i + 1]};
-    } else {
-#pragma unroll
-      for (int i = 0; i < NT; i += 2) *reinterpret_cast<uint32_t*>(a.out + id * D + d + i) = pack2<T>(x[i], x[i + 1]);
+    for (int g = 0; g < 4; ++g) {
+      const float e = inv * 0x1p24f, f = inv * 0x1p20f;
+      *reinterpret_cast<u32x2*>(own + l32 * (D * 2) + (((4 * i + g) ^ (l32 & 7)) << 4) + 8 * h) =
+          u32x2{pack2<T>(o[i][4 * g] * e, o[i][4 * g + 1] * f), pack2<T>(o[i][4 * g + 2] * e, o[i][4 * g + 3] * f)};
+    }
+  constexpr int kLanes = D / 8;              // lanes of a row
+  for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
+    const int gr = r0 + 32 * wave + r;
+    if (gr < rows) {
+      const int i = gr / a.group;
+      const int64_t rid = (int64_t)(seq.first + i) * a.q_heads + head * a.group + gr - i * a.group;
+      *reinterpret_cast<u32x4*>(a.out + rid * D + 8 * (lane % kLanes)) =
+          *reinterpret_cast<const u32x4*>(own + r * (D * 2) + (((lane % kLanes) ^ (r & 7)) << 4));
     }
   }
 }
 
 // ------------------------------------------------------------------ joining the chunks of a divided sequence
-// One wave per query row: the chunks' sums, each scaled to the largest reference, in chunk order.
+// One workgroup per query row: the chunks' sums, each scaled to the largest reference.  Wave v adds chunks v, v + 4,
+// ... in order, then the waves' sums are added in order.  Sums are read beside the statistics, eight in flight, also of
+// chunks that hold no token of the row (whatever is there, left out below): one memory latency less.
 template <class T, int D>
 __global__ __launch_bounds__(256) void join_kernel(Args a) {
   constexpr int C = D / 64;
-  const int lane = threadIdx.x & 63;
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  __shared__ float part[4][D];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int most = a.max_q * a.group;
-  const int bh = (int)(w / most), r = (int)(w - (int64_t)bh * most);
-  if (bh >= a.batch * a.heads) return;
+  const int bh = blockIdx.x / most, r = blockIdx.x - bh * most;
   const int b = bh / a.heads, head = bh - b * a.heads;
   const kv4::Sequence seq = kv4::sequence(a.q_start[b], a.q_start[b + 1], a.lens[b], a.total_q, a.max_q, a.max_len,
                                           a.width << a.log_page);
@@ -612,11 +766,18 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
   const int64_t all_rows = (int64_t)a.total_q * a.q_heads;
   const int chunks = (n + a.chunk_tokens - 1) / a.chunk_tokens;          // those that hold a token of this row
   const float* ml = a.part + a.chunks * all_rows * D + id * 2;
-  float M = kNegInf, l = 0.0f;
-  if (lane < chunks) {
-    M = ml[lane * all_rows * 2];
-    l = ml[lane * all_rows * 2 + 1];
-  }
+  const float* src = a.part + id * D + lane * C;
+  float x[8][C];
+  auto load = [&](int c0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int j = 0; j < C; ++j) x[k][j] = src[min(c0 + 4 * k, a.chunks - 1) * all_rows * D + j];
+  };
+  load(wave);
+  const float2 st = *reinterpret_cast<const float2*>(ml + min(lane, a.chunks - 1) * all_rows * 2);
+  const float M = lane < chunks ? st.x : kNegInf;
+  float l = lane < chunks ? st.y : 0.0f;
   float top = M;
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
@@ -624,53 +785,71 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
   l *= f;
 #pragma unroll
   for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
-  float x[C] = {};
-  for (int c = 0; c < chunks; ++c) {
-    const float g = __shfl(f, c);
-    const float* src = a.part + (c * all_rows + id) * D + lane * C;
+  float sum[C] = {};
+  for (int c0 = wave; c0 < chunks; c0 += 32) {
+    if (c0 > wave) load(c0);
 #pragma unroll
-    for (int j = 0; j < C; ++j) x[j] += g * src[j];
+    for (int k = 0; k < 8; ++k) {
+      const float g = __shfl(f, min(c0 + 4 * k, 63));
+      if (c0 + 4 * k < chunks)
+#pragma unroll
+        for (int j = 0; j < C; ++j) sum[j] += g * x[k][j];
+    }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
-  for (int j = 0; j < C; ++j) a.out[id * D + lane * C + j] = T::store(x[j] * inv);
+  for (int j = 0; j < C; ++j) part[wave][lane * C + j] = sum[j];
+  __syncthreads();
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  if (threadIdx.x < D) {
+    const int d = threadIdx.x;
+    a.out[id * D + d] = T::store((part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+  }
 }
 
+enum Kind { kFour = 1, kEight = 2, kPrompt = 3 };
 constexpr int kMaxChunks = 64;               // one lane of the joining wave each
 
 template <class T, int D>
 void launch(const Args& a, int kind, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.row_tiles * a.chunks));
-  if (kind == 1)
-    hipLaunchKernelGGL((decode_kernel<T, D, 1>), grid, dim3(256), 0, st, a);
-  else if (kind == 2)
-    hipLaunchKernelGGL((decode_kernel<T, D, 2>), grid, dim3(256), 0, st, a);
+  if (kind == kFour)
+    hipLaunchKernelGGL((decode_kernel<T, D, 4>), grid, dim3(256), 0, st, a);
+  else if (kind == kEight)
+    hipLaunchKernelGGL((decode_kernel<T, D, 8>), grid, dim3(512), 0, st, a);
   else
     hipLaunchKernelGGL((prompt_kernel<T, D>), grid, dim3(256), 0, st, a);
   if (a.chunks > 1) {
-    const int64_t waves = (int64_t)a.batch * a.heads * a.max_q * a.group;
-    hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, st, a);
+    const int64_t rows = (int64_t)a.batch * a.heads * a.max_q * a.group;
+    hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)rows), dim3(256), 0, st, a);
   }
 }
 
 }  // namespace
 
-// kind 1, 2: decode_kernel with one or two tiles of 16 rows; 3: prompt_kernel.
+// How a call is run.
+//   kPrompt: prompt_kernel, 128 query rows a workgroup, for more than 64 rows a sequence and kv head.
+//   kFour / kEight: decode_kernel, 16 rows a workgroup of four or eight waves.
+// A sequence is divided into chunks (joined by a second kernel, about 7 us in all) until the grid has `want`
+// workgroups, but not below 256 tokens a chunk, and not at all up to 1024 tokens, which eight waves walk through in
+// four steps.  Measured (one call, 256 compute units): 16 sequences of up to 2048 tokens, 32 kv heads: 23.7 us whole in four
+// waves, 24.5 in eight, 30 divided in two; 4 of up to 32768, 8 kv heads: 32.5 in 8 chunks, 38 in 24 or more; 16 of 4096
+// with 16 heads of 64 channels: 21.2 whole in eight waves, 27 in four; one of 700: 8.0 whole, 8.9 divided; 8 of up to 4001 with 40
+// rows: 23.6 in 16-row tiles and 6 chunks, 34 in prompt_kernel.
 Kv4Plan kv4_plan(int total_q, int q_heads, int heads, int dim, int batch, int max_q, int max_len) {
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
   Kv4Plan p;
-  p.kind = rows <= 16 ? 1 : rows <= 32 ? 2 : 3;
-  const int per = p.kind == 3 ? 128 : 16 * p.kind;
+  p.kind = rows > 64 ? kPrompt : rows > 16 ? kFour : kEight;
+  const int per = p.kind == kPrompt ? 128 : 16;
   p.row_tiles = (int)((rows + per - 1) / per);
-  // workgroups without division, against four (two) a compute unit
   const int64_t groups = (int64_t)batch * heads * p.row_tiles;
-  const int64_t want = p.kind == 3 ? 512 : 1024;
-  const int step = 128;
+  if (p.kind == kEight && groups >= 512) p.kind = kFour;
+  const int64_t want = p.kind == kPrompt ? 512 : p.kind == kEight ? 256 : rows > 16 ? 768 : 1;
   int64_t chunks = (want + groups - 1) / groups;
-  chunks = chunks < 1 ? 1 : chunks > kMaxChunks ? kMaxChunks : chunks;
+  chunks = chunks > kMaxChunks ? kMaxChunks : chunks;
+  if (p.kind != kPrompt && max_len <= 1024) chunks = 1;
   const int64_t tokens = (max_len + chunks - 1) / chunks;
-  p.chunk_tokens = (int)((tokens + step - 1) / step * step);
-  p.chunks = max_len < 1 ? 1 : (max_len + p.chunk_tokens - 1) / p.chunk_tokens;
+  p.chunk_tokens = (int)((tokens + 255) / 256 * 256);
+  p.chunks = (max_len + p.chunk_tokens - 1) / p.chunk_tokens;
   return p;
 }
 
