@@ -36,14 +36,13 @@ __device__ __forceinline__ float elem(uint32_t w, int i) { return T::load(i ? w 
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) { return (uint32_t)T::store(a) | (uint32_t)T::store(b) << 16; }
 
-// fl32(x / s), r = fl32(1 / s) from an IEEE divide: the product x r is within two ulps, one
-// corrected step makes it faithful, and a second one (exact remainder, correctly rounded
-// reciprocal) makes it the correctly rounded quotient (P. Markstein's theorem).  Needs s and x / s away
-// from the ends of the fp32 range: s >= 2^-100; x / s near a rounding border of the codes is.
+// A quotient with the nearest integer of fl32(x / s): the product with the correctly rounded reciprocal r, corrected once.
+// For 8- and 11-bit x against the scales of both quantizers (fl32(max / 127); any fp16 value) this was walked over every pair of
+// significands (tests/test_serve_arith.py): fl32(x / s) lies exactly on a border between two codes for common x, such
+// as max / 2, and an uncorrected product falls on either side of it.  s = 0: r = 0, and 0 for x = 0.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float q0 = x * r;
-  const float q1 = __builtin_fmaf(__builtin_fmaf(-q0, s, x), r, q0);
-  return __builtin_fmaf(__builtin_fmaf(-q1, s, x), r, q1);
+  const float q = x * r;
+  return __builtin_fmaf(__builtin_fmaf(-q, s, x), r, q);
 }
 
 // ---- W8A8

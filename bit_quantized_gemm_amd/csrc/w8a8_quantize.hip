@@ -5,15 +5,17 @@
 // code, so a row is read once into registers by the threads that share it, its maximum is joined
 // (in a wave by DPP-free shuffles, across waves through LDS) and the codes are made from the registers.
 // The threads of a row follow its length: a wave for short rows (four rows a workgroup, no
-// barrier), 256 threads up to 16384 elements, 1024 beyond.  Rows whose elements no
-// 16-byte load fits (odd K or stride, shifted views) are read element by element.
+// barrier), 256 threads up to 16384 elements, 1024 beyond.  Rows whose elements no aligned 16-byte load fits
+// (odd K or stride, shifted views) are read by unaligned ones, the last few elements one by one.
 //
-// The codes must be those of an IEEE divide: x / s lands exactly between two codes whenever x is
-// max / 2 (a common value in bf16), and the nearest fp32 quotient decides.  See quotient().
+// The codes are those of an IEEE divide, without its dozen instructions an element: see quotient().
 #include "serve_internal.h"
 
 namespace atom {
 namespace {
+
+// 16 bytes at any address of a 16-bit element: gfx950 loads them in one instruction (two cache lines at most).
+typedef u32x4 Unaligned __attribute__((aligned(2)));
 
 template <class T, int THREADS, int CH, bool VEC>
 __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx,
@@ -35,6 +37,10 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel
     if (VEC) {
       u32x4 v = {0, 0, 0, 0};
       if (8 * c < K) v = *reinterpret_cast<const u32x4*>(x + 8 * c);   // VEC: K % 8 == 0
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i][j] = v[j];
+    } else if (8 * c + 8 <= K) {
+      const u32x4 v = *reinterpret_cast<const Unaligned*>(x + 8 * c);
 #pragma unroll
       for (int j = 0; j < 4; ++j) w[i][j] = v[j];
     } else {
@@ -76,11 +82,12 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float v = elem<T>(w[i][2 * half + j / 2], j & 1);
-        float u = tiny ? (s > 0.0f ? v / s : 0.0f) : quotient(v, s, r);
-        u = __builtin_fminf(__builtin_fmaxf(__builtin_rintf(u), -127.0f), 127.0f);
-        b[j] = (uint32_t)(int)u & 0xFFu;
+        // |v| is at most the row's maximum, so the code is within +-127 by itself; next to fp32's smallest numbers the
+        // scale's own rounding can carry it further
+        float u = tiny ? __builtin_fminf(__builtin_fmaxf(s > 0.0f ? v / s : 0.0f, -127.0f), 127.0f) : quotient(v, s, r);
+        b[j] = __builtin_bit_cast(uint32_t, u + 12582912.0f);     // 1.5 * 2^23: the integer (ties to even) in the low byte
       }
-      o[half] = b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24;
+      o[half] = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
     }
     *reinterpret_cast<u32x2*>(q + 8 * c) = u32x2{o[0], o[1]};
   }
