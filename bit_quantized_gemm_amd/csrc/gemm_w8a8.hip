@@ -21,8 +21,8 @@
 //     waves divide K, and each wave loads its operands straight into registers, a batch of
 //     16-byte loads in flight at once; the waves' integer sums meet in LDS.
 #include "lds_ring.h"
-#include "serve_internal.h"
 #include "atom_internal.h"
+#include "w8a8_row.h"
 
 namespace atom {
 namespace {
@@ -334,16 +334,101 @@ __global__ void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __r
   }
 }
 
+// The layer for at most MR <= 4 tokens in one launch: every workgroup quantizes the tokens for itself, into LDS, while its
+// first weights are on their way; then as above.  Each wave's weights are read as in gemm_rows_kernel.
+template <class T, int MR, int CH>
+__global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                           const int8_t* __restrict__ Wq, const float* __restrict__ sw,
+                                                           const uint16_t* __restrict__ bias, int M, int N, int K, int Kp,
+                                                           uint16_t* __restrict__ Y) {
+  constexpr int kBatch = 4;
+  extern __shared__ __attribute__((aligned(16))) int32_t shared[];   // sums [waves][16 tokens][16 columns], then the codes
+  __shared__ uint32_t wave_max[MR][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
+  const int units = Kp / 128;
+  const int ua = units * wave / waves, ub = units * (wave + 1) / waves;
+  const int8_t* w = Wq + (size_t)min(n0 + l16, N - 1) * Kp + 16 * q;
+  i32x4 b[kBatch][2];
+  auto load = [&](int u) __attribute__((always_inline)) {      // past the range's end: the last unit again, not multiplied
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) b[k][t] = *reinterpret_cast<const i32x4*>(w + min(u + k, max(ub, 1) - 1) * 128 + 64 * t);
+  };
+  load(ua);
+  __builtin_amdgcn_sched_barrier(0);
+
+  int8_t* codes = reinterpret_cast<int8_t*>(shared + waves * 256);
+  u32x4 x[MR][CH];
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      x[m][i] = w8a8::load8<false>(X + (int64_t)min(m, M - 1) * ldx, threadIdx.x + i * blockDim.x, K);
+      top = w8a8::max8(x[m][i], top);
+    }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+    if (lane == 0) wave_max[m][wave] = top;
+  }
+  __syncthreads();
+  float s[MR];
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    uint32_t top = 0;
+    for (int v = 0; v < waves; ++v) top = max(top, wave_max[m][v]);
+    s[m] = T::load(top) / 127.0f;
+    const float r = s[m] > 0.0f ? 1.0f / s[m] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      if (8 * c < Kp) *reinterpret_cast<u32x2*>(codes + m * Kp + 8 * c) = w8a8::codes8<T>(x[m][i], s[m], r);
+    }
+  }
+  __syncthreads();
+
+  const int8_t* row = codes + min(l16, MR - 1) * Kp + 16 * q;
+  i32x4 acc = {};
+  for (int u = ua; u < ub; u += kBatch) {
+    if (u > ua) load(u);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (u + k < ub) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              b[k][t], *reinterpret_cast<const i32x4*>(row + (u + k) * 128 + 64 * t), acc, 0, 0, 0);
+      }
+    }
+  }
+  *reinterpret_cast<i32x4*>(shared + (wave * 16 + l16) * 16 + 4 * q) = acc;
+  __syncthreads();
+  const int m = threadIdx.x >> 4, n = n0 + (threadIdx.x & 15);
+  if (m < M && n < N) {
+    int sum = 0;
+    for (int v = 0; v < waves; ++v) sum += shared[v * 256 + threadIdx.x];
+    float sx = s[0];
+#pragma unroll
+    for (int i = 1; i < MR; ++i) sx = m == i ? s[i] : sx;
+    Y[(size_t)m * N + n] = T::store(scaled(sum, sx, sw[n], bias ? T::load(bias[n]) : 0.0f));
+  }
+}
+
 // The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
 constexpr int kKinds = 5;
 constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
+
+// Waves of a workgroup that divide units of 128 bytes of K, at least four units each.
+int rows_waves(int Kp) { return min(16, max(4, (Kp / 128 + 3) / 4)); }
 
 template <class T>
 void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const uint16_t* bias, int M, int N,
             int K, uint16_t* Y, int32_t* part, const W8Plan& p, hipStream_t st) {
   const int Kp = (K + 127) / 128 * 128;
   if (p.kind == 0) {
-    const int waves = min(16, max(4, (Kp / 128 + 3) / 4));
+    const int waves = rows_waves(Kp);
     if (M <= 16)
       hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
                          bias, M, N, Kp, Y);
@@ -366,6 +451,22 @@ void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw
   ATOM_TILE(3, 256, 128, 3, 1)
   ATOM_TILE(4, 256, 256, 2, 1)
 #undef ATOM_TILE
+}
+
+template <class T, int MR>
+void launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const float* sw, const uint16_t* bias, int M,
+                        int N, int K, uint16_t* Y, hipStream_t st) {
+  const int Kp = (K + 127) / 128 * 128, waves = rows_waves(Kp), chunks = (Kp / 8 + 64 * waves - 1) / (64 * waves);
+  const dim3 grid((N + 15) / 16), block(64 * waves);
+  const size_t lds = waves * 1024 + (size_t)MR * Kp;
+#define ATOM_ROWS(CH)                                                                                                   \
+  if (chunks <= CH) {                                                                                                  \
+    hipLaunchKernelGGL((linear_rows_kernel<T, MR, CH>), grid, block, lds, st, X, ldx, Wq, sw, bias, M, N, K, Kp, Y);   \
+    return;                                                                                                            \
+  }
+  ATOM_ROWS(1)
+  ATOM_ROWS(2)
+#undef ATOM_ROWS
 }
 
 }  // namespace
@@ -416,6 +517,22 @@ hipError_t launch_gemm_w8a8(const int8_t* Xq, const float* sx, const int8_t* Wq,
     launch<Bf16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
   else
     launch<Fp16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
+  return hipGetLastError();
+}
+
+bool linear_rows_fits(int M, int N, int K) {
+  const int64_t work = (int64_t)M * K * (((N + 15) / 16 + compute_units() - 1) / compute_units());
+  return M <= 4 && work <= 16384;
+}
+
+hipError_t launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const float* sw, const uint16_t* bias,
+                              int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream) {
+  if (bf16)
+    M == 1 ? launch_linear_rows<Bf16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+           : launch_linear_rows<Bf16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
+  else
+    M == 1 ? launch_linear_rows<Fp16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+           : launch_linear_rows<Fp16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
   return hipGetLastError();
 }
 

@@ -154,6 +154,10 @@ int atom_linear_w8a8(const void* X, int64_t ldx, int32_t dtype, const void* Wq, 
   const Range out[2] = {range_of(Y, (uint64_t)M * N * 2), range_of(workspace, (uint64_t)need)};
   if (int s = check_overlap(in, bias ? 4 : 3, out, 2)) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (atom::linear_rows_fits(M, N, K))
+    return hip_status(atom::launch_linear_rows(static_cast<const uint16_t*>(X), ldx, static_cast<const int8_t*>(Wq), sw,
+                                               static_cast<const uint16_t*>(bias), M, N, K, dtype == ATOM_BF16,
+                                               static_cast<uint16_t*>(Y), st));
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* sx = reinterpret_cast<float*>(xq + (uint64_t)M * row_bytes8(K));
   int32_t* part = reinterpret_cast<int32_t*>(reinterpret_cast<uint8_t*>(sx) + up16((uint64_t)M * 4));

@@ -61,6 +61,11 @@ hipError_t launch_gemm_w8a8(const int8_t* Xq, const float* sx, const int8_t* Wq,
                             int M, int N, int K, bool bf16, uint16_t* Y, int32_t* part, const W8Plan& plan,
                             hipStream_t stream);
 
+// The whole layer in one launch, for so few tokens that every workgroup may quantize them for itself.
+bool linear_rows_fits(int M, int N, int K);
+hipError_t launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const float* sw, const uint16_t* bias,
+                              int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream);
+
 // ---- KV cache
 hipError_t launch_kv4_append(const uint16_t* K, int64_t k_stride, const uint16_t* V, int64_t v_stride,
                              const int64_t* slots, int tokens, bool bf16, const atom_kv4_cache& c, hipStream_t stream);

@@ -9,13 +9,10 @@
 // (odd K or stride, shifted views) are read by unaligned ones, the last few elements one by one.
 //
 // The codes are those of an IEEE divide, without its dozen instructions an element: see quotient().
-#include "serve_internal.h"
+#include "w8a8_row.h"
 
 namespace atom {
 namespace {
-
-// 16 bytes at any address of a 16-bit element: gfx950 loads them in one instruction (two cache lines at most).
-typedef u32x4 Unaligned __attribute__((aligned(2)));
 
 template <class T, int THREADS, int CH, bool VEC>
 __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx,
@@ -29,34 +26,12 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel
   if (kRows > 1 && row >= rows) return;                 // whole waves: no barrier follows
   const uint16_t* x = X + (size_t)row * ldx;
 
-  // chunk c = t + i * THREADS: elements 8 c .. 8 c + 7, zeros behind K
-  uint32_t w[CH][4];
+  u32x4 w[CH];                                          // chunk c = t + i * THREADS: elements 8 c .. 8 c + 7
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int c = t + i * THREADS;
-    if (VEC) {
-      u32x4 v = {0, 0, 0, 0};
-      if (8 * c < K) v = *reinterpret_cast<const u32x4*>(x + 8 * c);   // VEC: K % 8 == 0
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[i][j] = v[j];
-    } else if (8 * c + 8 <= K) {
-      const u32x4 v = *reinterpret_cast<const Unaligned*>(x + 8 * c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[i][j] = v[j];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = 8 * c + 2 * j;
-        w[i][j] = (e < K ? (uint32_t)x[e] : 0u) | (e + 1 < K ? (uint32_t)x[e + 1] << 16 : 0u);
-      }
-    }
-  }
-  // |x| as integers: the order of the bits is the order of the values
+  for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(x, t + i * THREADS, K);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < CH; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(w[i][j] & 0x7FFFu, (w[i][j] >> 16) & 0x7FFFu));
+  for (int i = 0; i < CH; ++i) m = w8a8::max8(w[i], m);
 #pragma unroll
   for (int d = 32; d; d >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
   if constexpr (THREADS > 64) {
@@ -69,27 +44,11 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel
   const float s = T::load(m) / 127.0f;
   if (t == 0) sx[row] = s;
   const float r = s > 0.0f ? 1.0f / s : 0.0f;
-  const bool tiny = s < 0x1p-100f;                      // bf16 rows next to zero: the plain divide
   int8_t* q = Xq + (size_t)row * Kp;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = t + i * THREADS;
-    if (8 * c >= Kp) continue;
-    uint32_t o[2];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t b[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float v = elem<T>(w[i][2 * half + j / 2], j & 1);
-        // |v| is at most the row's maximum, so the code is within +-127 by itself; next to fp32's smallest numbers the
-        // scale's own rounding can carry it further
-        float u = tiny ? __builtin_fminf(__builtin_fmaxf(s > 0.0f ? v / s : 0.0f, -127.0f), 127.0f) : quotient(v, s, r);
-        b[j] = __builtin_bit_cast(uint32_t, u + 12582912.0f);     // 1.5 * 2^23: the integer (ties to even) in the low byte
-      }
-      o[half] = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u) | __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
-    }
-    *reinterpret_cast<u32x2*>(q + 8 * c) = u32x2{o[0], o[1]};
+    if (8 * c < Kp) *reinterpret_cast<u32x2*>(q + 8 * c) = w8a8::codes8<T>(w[i], s, r);
   }
 }
 
