@@ -280,13 +280,14 @@ __global__ __launch_bounds__(256) void finish_kernel(const int32_t* __restrict__
   }
 }
 
-// At most 16 RT tokens.  Lane l of a K = 64 slice supplies row l & 15, bytes 16 (l >> 4) .. + 15 of
-// both operands; the accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
+// At most 16 RT tokens against 16 columns a workgroup.  Lane l of a K = 64 slice supplies row l & 15, bytes
+// 16 (l >> 4) .. + 15 of both operands; an accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
+constexpr int kBatch = 4;        // units of 128 bytes of K whose loads a wave has in flight
 template <class T, int RT>
-__global__ void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
-                                 const int8_t* __restrict__ Wq, const float* __restrict__ sw,
-                                 const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y) {
-  constexpr int kBatch = 4;      // units of 128 bytes of K whose loads a wave has in flight
+__global__ __launch_bounds__(1024) void gemm_rows_kernel(const int8_t* __restrict__ Xq, const float* __restrict__ sx,
+                                                         const int8_t* __restrict__ Wq, const float* __restrict__ sw,
+                                                         const uint16_t* __restrict__ bias, int M, int N, int Kp,
+                                                         uint16_t* __restrict__ Y) {
   extern __shared__ __attribute__((aligned(16))) int32_t sums[];   // [waves][RT][16 tokens][16 columns]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
@@ -341,7 +342,6 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
                                                            const int8_t* __restrict__ Wq, const float* __restrict__ sw,
                                                            const uint16_t* __restrict__ bias, int M, int N, int K, int Kp,
                                                            uint16_t* __restrict__ Y) {
-  constexpr int kBatch = 4;
   extern __shared__ __attribute__((aligned(16))) int32_t shared[];   // sums [waves][16 tokens][16 columns], then the codes
   __shared__ uint32_t wave_max[MR][16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -471,8 +471,10 @@ void launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const 
 
 }  // namespace
 
-// The plan of a shape.  Up to 32 tokens: the few-rows kernel (32 x 4096 x 4096: 8 us against 12 us in 64 x 128 tiles).
-// Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
+// The plan of a shape.  Up to 32 tokens: the few-rows kernel, unless the weights are so many that the tiles' wider reads
+// make up for their start (us, few rows against 64 x 128 tiles: 16 x 4096 x 4096 6.5 and 12.3, 16 x 28672 x 8192 58 and 51, 32 x 4096 x
+// 4096 8.2 and 12.6, 32 x 11008 x 4096 18.7 and 13.6; each token row costs the few-rows kernel another read of its codes for every 16
+// columns).  Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
 // epilogue) and `full` ns for each element of K when every compute unit holds `slots` workgroups, `one` ns when it holds
 // one (fitted to 1024 x 11008 x 4096, 2048 x 4096 x 11008, 4096 x 28672 x 8192, 512 x 4096 x 4096 and 1500 x 6000 x 700 on
 // 256 units).  A grid that leaves half the units idle over a long K, or most of them over a shorter one, has K
@@ -482,7 +484,12 @@ W8Plan w8_plan(int M, int N, int K) {
   auto tiles = [&](int kind) {
     return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
   };
-  if (M <= 32) return W8Plan{0, (N + 15) / 16, 1};
+  const double weights = (double)N * K;
+  if (M <= 32) {
+    const double rows = 3.5 + weights * (M <= 4 ? 0.15e-6 : M <= 16 ? 0.21e-6 : 0.33e-6);
+    const double tile = 1.0 + (weights / 4.6e6 > 3e-3 * K ? weights / 4.6e6 : 3e-3 * K);
+    if (rows <= tile) return W8Plan{0, (N + 15) / 16, 1};
+  }
   struct Cost {
     int slots;
     double full, one, fixed;
