@@ -223,17 +223,19 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
       for (int t = 0; t < 2; ++t) s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(unpack_keys(k[t][w]), q[w], s[t], 0, 0, 0);
     load_keys(next);
     uint32_t word = 0;
-    if (base + 32 > seq.tokens) {            // what lies behind the sequence's end is no number
+    if (base + 32 > all) {                   // a row's masked tokens leave its E alone, whatever their scales
+      const int there = seq.tokens - base - 4 * h, seen = limit - base - 4 * h;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (base + 16 * t + 4 * h + r >= seq.tokens) kp[t][r] = vp[t][r] = 0;
+        for (int r = 0; r < 4; ++r) {
+          if (16 * t + r >= there) kp[t][r] = vp[t][r] = 0;   // what lies behind the sequence's end is no number
+          word = max(word, 16 * t + r < seen ? vp[t][r] : 0);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) word = max(word, vp[j >> 2][j & 3]);
     }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) word = max(word, vp[t][r]);
     const bool raise_v = __any(word > (top_v | 0xFFFFu));
     if (raise_v) {
       word = max(word, (uint32_t)__shfl_xor((int)word, 16));
@@ -250,9 +252,10 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
     }
     load_key_parameters(next);
     if (base + 32 > all) {
+      const int seen = limit - base - 4 * h;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (base + 16 * (j >> 2) + 4 * h + (j & 3) >= limit) y[j] = kNegInf;
+        if (16 * (j >> 2) + (j & 3) >= seen) y[j] = kNegInf;
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) top = max3(top, y[j], y[j + 1]);
@@ -562,23 +565,37 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   float y[16];
   h8v p[2], ring[4];
   f32x16 s;
+  f32x4 u[4];                                // value scales of the half tile whose weights come next (see read)
   // Masks, and raises the reference where it has to be raised; base: the half tile's first token.
   auto settle = [&](int buf, int t, int base) __attribute__((always_inline)) {
-    if (base + 32 > all) {
+    const bool edge = base + 32 > all;
+    float big;                               // a value scale: of any token, or the largest that the row sees
+    if (edge) {
+      big = 0.0f;
+      const int seen = limit - base - 4 * h;
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        if (base + 8 * (j >> 2) + 4 * h + (j & 3) >= limit) y[j] = kNegInf;
+      for (int j = 0; j < 16; ++j) {
+        const int i = 8 * (j >> 2) + (j & 3);
+        if (i >= seen)
+          y[j] = kNegInf;
+        else
+          big = __builtin_fmaxf(big, D < 256 ? u[j >> 2][j & 3] : lf[buf][1][32 * t + 4 * h + i]);
+      }
+      big = join_max<false>(big);
+    } else {
+      big = lf[buf][1][32 * t + l32];
     }
     float top = max3(y[0], y[1], y[2]);
 #pragma unroll
     for (int j = 3; j < 15; j += 2) top = max3(top, y[j], y[j + 1]);
     top = __builtin_fmaxf(top, y[15]);
-    const float u = lf[buf][1][32 * t + l32];
-    if (first || __any(top > 8.0f - E || u > most)) {
-      float dE = 0.0f, big = u;
+    if (first || __any(top > 8.0f - E || big > most)) {
+      float dE = 0.0f;
+      if (!edge) {
 #pragma unroll
-      for (int d = 16; d; d >>= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
-      if (big > most) {                      // wave-uniform
+        for (int d = 16; d; d >>= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
+      }
+      if (big > most) {
         const float e = (float)max(-24, (int)(__builtin_bit_cast(uint32_t, big) >> 23) - 126);   // big <= 2^e
         dE = first ? e - E : __builtin_fmaxf(e - E, 0.0f);
         most = __builtin_ldexpf(1.0f, (int)(E + dE));
@@ -603,7 +620,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   // Scores of (buf, t) on the matrix cores while the vector ALUs turn y into the weights of (wbuf, wt).  Every product is a
   // scheduling region of its own with its share of the rest, operands are read four products ahead; the last reads
   // are the first operands of the product with the values that follows.
-  f32x4 u[4];
   // The first reads of scores_and_weights, made before the masks and the reference of the half tile in front (D = 256
   // has no registers for that).
   auto read = [&](int buf, int t, int wbuf, int wt) __attribute__((always_inline)) {

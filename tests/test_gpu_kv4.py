@@ -316,6 +316,31 @@ def test_attention_of_zero_and_non_finite_queries():
         assert torch.equal(bad, out)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q", [3, 40, 100])
+def test_tokens_behind_a_query_do_not_touch_it(q, D):
+    """The last two tokens are huge, infinite or NaN: only the queries that see them may notice.  The others keep their
+    result up to the weights' rounding to fp16, whose unit is set by the value scales that they see themselves.  Both runs
+    round each weight once (2^-12 of it) and the result once (2^-12 of it, or 2^-25): together at most 2^-11 of the largest
+    |value| and 2^-11 of the result; values of standard deviation 1e-3 stay below 6e-3, and the bound has twice that."""
+    n = 70 + q
+    for page in (16, 64):
+        b = Batch([n, 50], [q, min(q, 50)], 2, 1, D, page, seed=11, v_gain=1e-3)
+        plain = b.run()
+        b.check(plain)
+        at = torch.arange(n - 2, n, device="cuda")
+        slots = b.table[0].long()[at // page] * page + at % page
+        before = plain[:q - 2].clone()
+        for fill in (60000.0, float("inf"), -float("inf"), float("nan")):
+            say(f"[kv4 behind] q={q} D={D} page={page} {fill}")
+            x = torch.full((2, 1, D), fill, dtype=torch.float16, device="cuda")
+            x[1, 0, ::2] = 1.0
+            bq.atom_kv4_append(x, x, slots, b.cache)
+            got = b.run()
+            assert torch.equal(got[q:], plain[q:])           # the other sequence
+            torch.testing.assert_close(got[:q - 2], before, rtol=2.0**-10, atol=2.0**-10 * 6e-3)
+
+
 def test_attention_strided_queries_and_tight_bounds():
     b = Batch([100, 60, 30], [6, 4, 2], 4, 2, 128, 16, seed=6)
     wide = torch.zeros(b.total, 3 * 4 * 128, dtype=torch.float16, device="cuda")
