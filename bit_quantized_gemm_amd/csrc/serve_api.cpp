@@ -75,11 +75,11 @@ bool valid_attention(int32_t total_q, int32_t q_heads, int32_t heads, int32_t di
   if (!valid_rows(total_q) || q_heads > 16384 || batch < 1 || batch > (1 << 20) || max_q < 1 || max_q > ATOM_MAX_ROWS)
     return false;
   if (max_len < 1 || max_len > (1 << 30)) return false;
-  // query rows of one sequence and kv head, and the workgroups of a launch, in 31 bits
-  const uint64_t rows = (uint64_t)max_q * (uint64_t)(q_heads / heads);
+  const uint64_t rows = (uint64_t)max_q * (uint64_t)(q_heads / heads);   // of one sequence and kv head
   if (rows >= ((uint64_t)1 << 30)) return false;
-  return (uint64_t)batch * (uint64_t)heads * ((rows + 15) / 16) * 64 < ((uint64_t)1 << 37) &&
-         (uint64_t)batch * (uint64_t)heads * ((rows + 127) / 128) < ((uint64_t)1 << 30);
+  // a launch has less than 2^32 threads
+  const atom::Kv4Plan p = atom::kv4_plan(total_q, q_heads, heads, dim, batch, max_q, max_len);
+  return (uint64_t)batch * (uint64_t)heads * (uint64_t)p.row_tiles < ((uint64_t)1 << 24);
 }
 
 }  // namespace

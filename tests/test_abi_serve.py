@@ -159,6 +159,8 @@ def test_attention_validation(lib):
     assert call(ws=(10 << 36) + 4, nws=need, **more) == E_ALIGN
     assert call(ws=A, nws=need, **more) == E_OVERLAP
     assert lib.atom_kv4_attention_workspace_bytes(5, 3, 2, 64, 2, 1, 4096) == -E_SHAPE
+    assert lib.atom_kv4_attention_workspace_bytes(1 << 20, 64, 8, 128, 256, 1 << 20, 4096) == -E_SHAPE   # 2^27 workgroups
+    assert lib.atom_kv4_attention_workspace_bytes(1 << 20, 64, 8, 128, 256, 1 << 12, 4096) >= 0
     assert lib.atom_kv4_attention_workspace_bytes(1, 2, 2, 64, 1, 1, 100) == 0
     with pytest.raises(bq.AtomError):
         bq.atom_kv4_attention_workspace_bytes(5, 3, 2, 64, 2, 1, 4096)
