@@ -393,6 +393,55 @@ def test_two_calls_at_once_on_two_streams():
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
 
 
+def test_prompt_parts_against_long_contexts():
+    """A part of a prompt against a long context, divided among workgroups, in pages of every size, with pages that end inside
+    a tile, a sequence shorter than the others and one without tokens."""
+    for page, D, dtype in ((16, 128, torch.bfloat16), (32, 64, torch.float16), (128, 256, torch.float16), (64, 128, torch.float16)):
+        say(f"[kv4 prompt part] page={page} D={D}")
+        b = Batch([2111, 130, 0, 700], [70, 66, 5, 1], 4, 2, D, page, dtype, seed=page, spare_rows=1)
+        assert bq.atom_kv4_attention_workspace_bytes(b.total + 1, 4, 2, D, 4, 70, 2111) > 0
+        out = torch.full_like(b.q, 7.0)
+        b.run(out=out, max_q=70, max_len=2111)
+        b.check(out)
+        assert torch.all(out[b.total:] == 7)
+        b.check(b.run(max_q=70, max_len=2111, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")), what="undivided")
+
+
+def test_shared_and_repeated_pages():
+    """Two sequences whose tables name the same pages (a common prefix), one of them the same page twice."""
+    b = Batch([64, 48, 60], [1, 1, 1], 4, 2, 64, 16, seed=13)
+    b.table[1] = b.table[0]
+    b.table[2, 1] = b.table[2, 0]
+    b.check(b.run())
+    b.check(b.run(max_q=1, max_len=64))
+
+
+def test_two_graphs_of_divided_sequences():
+    """Two captured graphs and eager calls in turn, on streams of their own: each call has its own workspace."""
+    bs = [Batch([3000, 900], [1, 1], 8, 2, 128, 64, seed=1), Batch([2500, 1700], [40, 3], 8, 2, 128, 64, seed=2)]
+    for b in bs:
+        b.run()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for g, b in zip(graphs, bs):
+        with torch.cuda.graph(g):
+            outs.append(b.run())
+    for i in range(4):
+        for b in bs:
+            b.q.copy_(randn(*b.q.shape, seed=50 + i))
+        for g in graphs:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [b.run() for b in bs]
+        torch.cuda.synchronize()
+        for o, e in zip(outs, eager):
+            assert torch.equal(o, e)
+    for b, o in zip(bs, outs):
+        b.check(o)
+
+
 # ------------------------------------------------------------------ a layer as it would be used
 def _layer(Hq, H, D, hidden, dtype):
     W = [bq.atom_quantize_w8a8(randn(n, k, seed=20 + i, dtype=dtype, gain=k ** -0.5))

@@ -130,6 +130,55 @@ def test_linear(M, N, K, dtype, bias):
         torch.testing.assert_close(bq.atom_gemm_w8a8(Xq, sx, Wq, sw, K, bias=b, dtype=t, workspace=work), Y, rtol=0, atol=0)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 33, 16384), (2, 20, 8192), (3, 48, 5461), (4, 65, 4096), (4, 16, 4097), (1, 70, 16385), (2, 5, 1),
+                                   (4, 1, 129), (3, 4096, 513)])
+def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
+    """Quantized and multiplied in one launch, at the ends of what that takes: the bits of the two steps, also from rows
+    that lie apart and start at odd elements."""
+    say(f"[w8a8 one launch] {M}x{N}x{K} {dtype}")
+    t = TYPES[dtype]
+    Wq, sw = bq.atom_quantize_w8a8(make(N, K, t, 1, 0.02))
+    wide = make(M, K + 9, t, 2)
+    wide[M - 1, 3:] = 0                              # a row of zeros
+    wide[0, K // 2] = 1000                           # and one with an outlier
+    for first in (0, 1, 3, 8):
+        x = wide[:, first:first + K]
+        Y = bq.linear_w8a8(x, Wq, sw)
+        torch.testing.assert_close(Y, bq.atom_gemm_w8a8(*bq.atom_quantize_w8a8(x), Wq, sw, K, dtype=t), rtol=0, atol=0)
+        torch.testing.assert_close(Y, bq.linear_w8a8(x.contiguous(), Wq, sw), rtol=0, atol=0)
+    keep = wide.clone()
+    odd = torch.full((M, K + 9), float("nan"), dtype=t, device="cuda")       # what lies around the rows is not read into them
+    odd[:, 5:5 + K] = keep[:, 5:5 + K]
+    torch.testing.assert_close(bq.linear_w8a8(odd[:, 5:5 + K], Wq, sw), bq.linear_w8a8(keep[:, 5:5 + K].contiguous(), Wq, sw),
+                               rtol=0, atol=0)
+
+
+def test_two_graphs_and_eager_calls_between():
+    """Two captured graphs of the same shapes and eager calls in turn: none reads another's workspace."""
+    for M, N, K in ((2, 300, 1000), (64, 128, 4096)):
+        Wq, sw = bq.atom_quantize_w8a8(make(N, K, torch.float16, 1, 0.02))
+        xs = [make(M, K, torch.float16, 2 + i) for i in range(2)]
+        bq.linear_w8a8(xs[0], Wq, sw)
+        torch.cuda.synchronize()
+        graphs, ys = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+        for g, x in zip(graphs, xs):
+            with torch.cuda.graph(g):
+                ys.append(bq.linear_w8a8(x, Wq, sw))
+        for i in range(4):
+            for x in xs:
+                x.copy_(make(M, K, torch.float16, 20 + i + x.data_ptr() % 7))
+            streams = torch.cuda.Stream(), torch.cuda.Stream()
+            for g, s in zip(graphs, streams):
+                s.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(s):
+                    g.replay()
+            eager = [bq.linear_w8a8(x, Wq, sw) for x in xs]
+            torch.cuda.synchronize()
+            for y, e, x in zip(ys, eager, xs):
+                torch.testing.assert_close(y, e, rtol=0, atol=0)
+
+
 def test_extreme_sums():
     """The largest sums: every code +-127 over the longest K, exactly -+127^2 * 65536."""
     K = bq.MAX_K
