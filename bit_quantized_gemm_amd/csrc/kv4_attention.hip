@@ -406,40 +406,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   // the tokens that all of this wave's rows see
   const int all = min(kv4::visible(seq, min(r0 + 32 * wave, rows - 1) / a.group), seq.tokens);
 
-  // ---- queries: lane half h holds words 2 s + h of its row
-  h8v q[S];
-  float c1;
-  {
-    const uint16_t* src = a.q + (int64_t)(seq.first + qi) * a.q_stride + (int64_t)(head * a.group + row - qi * a.group) * D + 8 * h;
-    u32x4 raw[S];
-#pragma unroll
-    for (int w = 0; w < S; ++w) raw[w] = *reinterpret_cast<const u32x4*>(src + 16 * w);
-    float top = 0.0f;
-#pragma unroll
-    for (int w = 0; w < S; ++w)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {          // the largest finite element
-        const float x = __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1));
-        top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
-      }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) lmax[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < NW; ++v) top = __builtin_fmaxf(top, lmax[v]);
-    const int e = max(-100, min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23)));   // 13 - floor(log2 top)
-    const float f = __builtin_ldexpf(1.0f, e);
-#pragma unroll
-    for (int w = 0; w < S; ++w) {
-      float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
-      q[w] = query_operand(x, f);
-    }
-    c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e, 24 - e), 1e-37f), 3e38f);
-  }
-
   auto key_swizzle = [](int t) { return D == 64 ? (t >> 1) & 7 : t & 15; };   // D = 64: two rows cover the banks
   // ---- staging: thread t carries words W (t % NW) .. of token t / NW's keys, and words W (t % 4 NW) .. of 4-token
   // block t / (4 NW)'s values
@@ -489,6 +455,42 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       gvp = *reinterpret_cast<const u32x4*>(a.v_par + vr);
     }
   };
+  if (begin < end) fetch(begin);             // on its way while the queries are read and scaled
+
+  // ---- queries: lane half h holds words 2 s + h of its row
+  h8v q[S];
+  float c1;
+  {
+    const uint16_t* src = a.q + (int64_t)(seq.first + qi) * a.q_stride + (int64_t)(head * a.group + row - qi * a.group) * D + 8 * h;
+    u32x4 raw[S];
+#pragma unroll
+    for (int w = 0; w < S; ++w) raw[w] = *reinterpret_cast<const u32x4*>(src + 16 * w);
+    float top = 0.0f;
+#pragma unroll
+    for (int w = 0; w < S; ++w)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {          // the largest finite element
+        const float x = __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1));
+        top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
+      }
+#pragma unroll
+    for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) lmax[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < NW; ++v) top = __builtin_fmaxf(top, lmax[v]);
+    const int e = max(-100, min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23)));   // 13 - floor(log2 top)
+    const float f = __builtin_ldexpf(1.0f, e);
+#pragma unroll
+    for (int w = 0; w < S; ++w) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
+      q[w] = query_operand(x, f);
+    }
+    c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e, 24 - e), 1e-37f), 3e38f);
+  }
+
   auto half2 = [](uint32_t w) { return __builtin_bit_cast(h2v, w); };
   const h2v kTiny = {(_Float16)0x1p-24f, (_Float16)0x1p-24f}, k16 = {(_Float16)16.0f, (_Float16)16.0f};
   // the pairs of halves (q - zero) 2^-24 in the two low nibbles of each half-word, the second 16 times as large
@@ -668,7 +670,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   // Half tiles in a pipeline: while the matrix cores make the scores of one, the vector ALUs make the weights of the
   // one before; while its product with the values runs, the next scores are scaled and the next tile is unpacked.
   if (begin < end) {
-    fetch(begin);
     stage_parameters(0, begin);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
