@@ -17,7 +17,7 @@
 //     stages: 1000 us instead of 935).  Stage rows are unpadded, 16-byte chunks at swizzled positions: the 16 lanes of a
 //     16-byte read hit distinct bank groups.  A stage is four K slices; a wave multiplies one slice while the next one's
 //     operands are read, one read or copy between two products.
-//   gemm_rows_kernel (few tokens): bound by reading the weights.  A workgroup owns 16 columns, its
+//   gemm_rows_kernel (few tokens, or few outputs): bound by reading the weights.  A workgroup owns 16 columns, its
 //     waves divide K, and each wave loads its operands straight into registers, a batch of
 //     16-byte loads in flight at once; the waves' integer sums meet in LDS.
 #include "lds_ring.h"
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const int32_t* __restrict__
   }
 }
 
-// At most 16 RT tokens against 16 columns a workgroup.  Lane l of a K = 64 slice supplies row l & 15, bytes
+// 16 RT tokens (blockIdx.y) against 16 columns (blockIdx.x) a workgroup.  Lane l of a K = 64 slice supplies row l & 15, bytes
 // 16 (l >> 4) .. + 15 of both operands; an accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
 constexpr int kBatch = 4;        // units of 128 bytes of K whose loads a wave has in flight
 template <class T, int RT>
@@ -290,13 +290,13 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const int8_t* __restric
                                                          uint16_t* __restrict__ Y) {
   extern __shared__ __attribute__((aligned(16))) int32_t sums[];   // [waves][RT][16 tokens][16 columns]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * RT);
   const int units = Kp / 128;
   const int ua = units * wave / waves, ub = units * (wave + 1) / waves;
   const int8_t* w = Wq + (size_t)min(n0 + l16, N - 1) * Kp + 16 * q;
   const int8_t* x[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) x[i] = Xq + (size_t)min(16 * i + l16, M - 1) * Kp + 16 * q;
+  for (int i = 0; i < RT; ++i) x[i] = Xq + (size_t)min(m0 + 16 * i + l16, M - 1) * Kp + 16 * q;
   i32x4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = i32x4{};
@@ -327,7 +327,7 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const int8_t* __restric
     *reinterpret_cast<i32x4*>(sums + ((wave * RT + i) * 16 + l16) * 16 + 4 * q) = acc[i];
   __syncthreads();
   for (int e = threadIdx.x; e < RT * 256; e += blockDim.x) {
-    const int m = e >> 4, n = n0 + (e & 15);
+    const int m = m0 + (e >> 4), n = n0 + (e & 15);
     if (m >= M || n >= N) continue;
     int s = 0;
     for (int v = 0; v < waves; ++v) s += sums[v * RT * 256 + e];
@@ -433,7 +433,7 @@ void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw
       hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
                          bias, M, N, Kp, Y);
     else
-      hipLaunchKernelGGL((gemm_rows_kernel<T, 2>), dim3(p.tiles), dim3(64 * waves), waves * 2048, st, Xq, sx, Wq, sw,
+      hipLaunchKernelGGL((gemm_rows_kernel<T, 2>), dim3(p.tiles, (M + 31) / 32), dim3(64 * waves), waves * 2048, st, Xq, sx, Wq, sw,
                          bias, M, N, Kp, Y);
     return;
   }
@@ -474,7 +474,9 @@ void launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const 
 // The plan of a shape.  Up to 32 tokens: the few-rows kernel, unless the weights are so many that the tiles' wider reads
 // make up for their start (us, few rows against 64 x 128 tiles: 16 x 4096 x 4096 6.5 and 12.3, 16 x 28672 x 8192 58 and 51, 32 x 4096 x
 // 4096 8.2 and 12.6, 32 x 11008 x 4096 18.7 and 13.6; each token row costs the few-rows kernel another read of its codes for every 16
-// columns).  Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
+// columns).  More tokens take it too, 32 to a workgroup, while there is at most one workgroup for a compute unit and K is not
+// long (us, tiles and few rows: 128 x 1000 x 300 5.2 and 3.8, 64 x 1536 x 2048 7.8 and 5.3, 128 x 1024 x 4096 10.0 and 7.6, 96 x 1280 x 5120
+// 10.1 and 8.9, 64 x 1024 x 8192 10.5 and 12.7; with two workgroups a unit 64 x 4096 x 1024 6.3 and 8.0).  Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
 // epilogue) and `full` ns for each element of K when every compute unit holds `slots` workgroups, `one` ns when it holds
 // one (fitted to 1024 x 11008 x 4096, 2048 x 4096 x 11008, 4096 x 28672 x 8192, 512 x 4096 x 4096 and 1500 x 6000 x 700 on
 // 256 units).  A grid that leaves half the units idle over a long K, or most of them over a shorter one, has K
@@ -490,12 +492,13 @@ W8Plan w8_plan(int M, int N, int K) {
     const double tile = 1.0 + (weights / 4.6e6 > 3e-3 * K ? weights / 4.6e6 : 3e-3 * K);
     if (rows <= tile) return W8Plan{0, (N + 15) / 16, 1};
   }
+  const int cus = compute_units();
+  if (M > 32 && K <= 6144 && (int64_t)((N + 15) / 16) * ((M + 31) / 32) <= cus) return W8Plan{0, (N + 15) / 16, 1};
   struct Cost {
     int slots;
     double full, one, fixed;
   };
   constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.5}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
-  const int cus = compute_units();
   int best = 1;
   double least = 0.0;
   for (int kind = 1; kind < kKinds; ++kind) {

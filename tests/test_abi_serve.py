@@ -84,10 +84,10 @@ def test_gemm_w8a8_validation(lib):
         assert call(**{n: p + 4}) == E_ALIGN
     assert call(y=A + 16) == call(y=C + 512) == E_OVERLAP
     assert call(bias=F, y=F) == E_OVERLAP
-    need = bq.atom_gemm_w8a8_workspace_bytes(64, 128, 4096)
+    need = bq.atom_gemm_w8a8_workspace_bytes(64, 128, 8192)
     assert need > 0
-    assert call(m=64, n=128, k=4096, ws=F + 4, nws=need) == E_ALIGN
-    assert call(m=64, n=128, k=4096, ws=E, nws=need) == E_OVERLAP
+    assert call(m=64, n=128, k=8192, ws=F + 4, nws=need) == E_ALIGN
+    assert call(m=64, n=128, k=8192, ws=E, nws=need) == E_OVERLAP
     assert lib.atom_gemm_w8a8_workspace_bytes(0, 4, 4) == -E_SHAPE
 
 

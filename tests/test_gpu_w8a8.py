@@ -101,7 +101,7 @@ def test_quantize_survives_inf_and_nan():
 
 # every kind of kernel and its edges: few rows (one and two tiles), divided K, the three tile sizes
 SHAPES = [(1, 1, 1), (1, 17, 300), (1, 4096, 4096), (3, 130, 127), (16, 100, 11008), (17, 33, 1000), (32, 1000, 513),
-          (33, 64, 128), (33, 65, 4096), (64, 128, 2048), (65, 127, 4100), (100, 260, 65536), (128, 4096, 1024),
+          (33, 64, 128), (33, 65, 4096), (33, 65, 6145), (127, 1000, 5000), (300, 300, 300), (4000, 31, 1000), (64, 128, 2048), (65, 127, 4100), (100, 260, 65536), (128, 4096, 1024),
           (333, 777, 1155), (257, 4097, 300), (512, 8192, 256), (1024, 4100, 384), (4000, 4104, 200), (2304, 11008, 130)]
 
 
@@ -156,7 +156,7 @@ def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
 
 def test_two_graphs_and_eager_calls_between():
     """Two captured graphs of the same shapes and eager calls in turn: none reads another's workspace."""
-    for M, N, K in ((2, 300, 1000), (64, 128, 4096)):
+    for M, N, K in ((2, 300, 1000), (64, 128, 4096), (64, 128, 8192)):
         Wq, sw = bq.atom_quantize_w8a8(make(N, K, torch.float16, 1, 0.02))
         xs = [make(M, K, torch.float16, 2 + i) for i in range(2)]
         bq.linear_w8a8(xs[0], Wq, sw)
@@ -222,7 +222,7 @@ def test_given_buffers_and_streams():
     torch.testing.assert_close(other, want, rtol=0, atol=0)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (20, 300, 500), (64, 128, 4096), (300, 1000, 640)])
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (20, 300, 500), (64, 128, 4096), (64, 128, 8192), (300, 1000, 640)])
 def test_graph_replays(M, N, K):
     say(f"[w8a8 graph] {M}x{N}x{K}")
     x, w = make(M, K, torch.float16, 1), make(N, K, torch.float16, 2, 0.02)
