@@ -420,8 +420,23 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
 constexpr int kKinds = 5;
 constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
 
-// Waves of a workgroup that divide units of 128 bytes of K, at least four units each.
-int rows_waves(int Kp) { return min(16, max(4, (Kp / 128 + 3) / 4)); }
+// Waves of a workgroup that divide units of 128 bytes of K.  A wave loads whole batches, so the count (8 to 16, four
+// units each where there are fewer; at least one for 1024 bytes, which linear_rows_kernel's quantizer needs) is the
+// one that loads least behind the ranges' ends: 16 x 4096 x 11008 with 11 waves of at most 8 units 15.0 us, with 8 of 11 14.9, with 16 of
+// 6 17.6.
+int rows_waves(int Kp) {
+  const int units = Kp / 128;
+  if (units <= 32) return max(4, (units + kBatch - 1) / kBatch);
+  int best = 16, least = 1 << 30;
+  for (int w = min(16, max(8, (units + 7) / 8)); w <= 16; ++w) {
+    const int loaded = w * (((units + w - 1) / w + kBatch - 1) / kBatch * kBatch);
+    if (loaded < least) {
+      least = loaded;
+      best = w;
+    }
+  }
+  return best;
+}
 
 template <class T>
 void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw, const uint16_t* bias, int M, int N,
@@ -471,49 +486,50 @@ void launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const 
 
 }  // namespace
 
-// The plan of a shape.  Up to 32 tokens: the few-rows kernel, unless the weights are so many that the tiles' wider reads
-// make up for their start (us, few rows against 64 x 128 tiles: 16 x 4096 x 4096 6.5 and 12.3, 16 x 28672 x 8192 58 and 51, 32 x 4096 x
-// 4096 8.2 and 12.6, 32 x 11008 x 4096 18.7 and 13.6; each token row costs the few-rows kernel another read of its codes for every 16
-// columns).  More tokens take it too, 32 to a workgroup, while there is at most one workgroup for a compute unit and K is not
-// long (us, tiles and few rows: 128 x 1000 x 300 5.2 and 3.8, 64 x 1536 x 2048 7.8 and 5.3, 128 x 1024 x 4096 10.0 and 7.6, 96 x 1280 x 5120
-// 10.1 and 8.9, 64 x 1024 x 8192 10.5 and 12.7; with two workgroups a unit 64 x 4096 x 1024 6.3 and 8.0).  Otherwise the tile size whose estimated time is least: a round of the grid takes `fixed` us (first stages,
-// epilogue) and `full` ns for each element of K when every compute unit holds `slots` workgroups, `one` ns when it holds
-// one (fitted to 1024 x 11008 x 4096, 2048 x 4096 x 11008, 4096 x 28672 x 8192, 512 x 4096 x 4096 and 1500 x 6000 x 700 on
-// 256 units).  A grid that leaves half the units idle over a long K, or most of them over a shorter one, has K
-// divided up to four ways (with the second kernel 200 x 1024 x 8192: 22.5 -> 14 us, 64 x 4096 x 4096: 13 -> 11.5 us); over
-// a short one the second kernel costs more than it saves (100 x 1000 x 1000: 6.0 -> 6.9 us).
+// The plan of a shape: the kernel whose estimated time (us) is least.
+//   Few rows: a start, and for each round of a workgroup a compute unit a rate for K (up to 16 tokens a unit reads its 16
+//     columns and as much again of the tokens' codes, beyond that 32 tokens in a second tile of rows).
+//   Tiles: a round of the grid takes `fixed` us (first stages, epilogue) and `full` ns for each element of K when every
+//     unit holds `slots` workgroups, `one` ns when it holds one; reading the weights sets a floor.
+//   64 x 128 tiles with K divided two to four ways, at least eight stages each and at most one workgroup a unit: the
+//     second kernel's 2.5 us and the pieces' way through memory on top (and 4%: with weights that stay in the caches
+//     undivided tiles gain more, 256 x 4096 x 4096 18.8 and 19.1 us from HBM, 14.3 and 18 not).
+// Fitted on 256 units to weights that come from HBM, products alone.  Measured (M x N x K): few rows and undivided tiles 16 x 4096 x
+// 4096 6.8 and 17.5, 16 x 12288 x 4096 15.2 and 19.2, 16 x 28672 x 8192 62 and 58, 32 x 4096 x 4096 8.8 and 18.0, 128 x 1024 x 4096 8.3
+// and 18.4, 300 x 300 x 300 3.8 and 6.0, 64 x 4096 x 1024 8.0 and 6.3; undivided, two, three and four ways 64 x 5120 x 5120 25.7, 19.2,
+// 16.4 and 15.4, 64 x 11008 x 4096 20.6, 17.4, 23.0 and 21.8 (the last two on more than 256 workgroups).
 W8Plan w8_plan(int M, int N, int K) {
   auto tiles = [&](int kind) {
     return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
   };
-  const double weights = (double)N * K;
-  if (M <= 32) {
-    const double rows = 3.5 + weights * (M <= 4 ? 0.15e-6 : M <= 16 ? 0.21e-6 : 0.33e-6);
-    const double tile = 1.0 + (weights / 4.6e6 > 3e-3 * K ? weights / 4.6e6 : 3e-3 * K);
-    if (rows <= tile) return W8Plan{0, (N + 15) / 16, 1};
-  }
-  const int cus = compute_units();
-  if (M > 32 && K <= 6144 && (int64_t)((N + 15) / 16) * ((M + 31) / 32) <= cus) return W8Plan{0, (N + 15) / 16, 1};
   struct Cost {
     int slots;
     double full, one, fixed;
   };
-  constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.5}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
-  int best = 1;
-  double least = 0.0;
+  constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.0}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
+  const int cus = compute_units(), stages = (K + 127) / 128;
+  W8Plan best = {0, (N + 15) / 16, 1};
+  const int64_t rounds = ((int64_t)best.tiles * (M <= 16 ? 1 : (M + 31) / 32) + cus - 1) / cus;
+  double least = M <= 16 ? 2.9 + rounds * K * (M <= 4 ? 0.70e-3 : 0.97e-3) : 2.4 + rounds * (1.0 + 1.45e-3 * K);
   for (int kind = 1; kind < kKinds; ++kind) {
     const Cost& c = cost[kind];
-    const int64_t per = ((int64_t)tiles(kind) + cus - 1) / cus;     // workgroups of the busiest unit
-    const int64_t full = per / c.slots, rest = per % c.slots;
-    const double t = 1e-3 * K * (full * c.full + (rest ? c.one : 0.0)) + (full + (rest ? 1 : 0)) * c.fixed;
-    if (kind == 1 || t < least) {
-      least = t;
-      best = kind;
+    const int t = tiles(kind);
+    for (int splits = 1; splits <= (kind == 1 ? 4 : 1); ++splits) {
+      if (splits > 1 && (stages < 8 * splits || t * splits > cus)) break;
+      const int64_t per = ((int64_t)t * splits + cus - 1) / cus;    // workgroups of the busiest unit
+      const int64_t full = per / c.slots, rest = per % c.slots;
+      const double k = splits == 1 ? K : (stages + splits - 1) / splits * 128;
+      const double multiply = 1e-3 * k * (full * c.full + (rest ? c.one : 0.0));
+      const double read = (double)N * K / (splits > 1 ? 6e6 : 4.2e6);
+      double time = (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
+      if (splits > 1) time = 1.04 * (time + 2.5 + (double)t * splits * kBM[1] * kBN[1] * 8 / 3.3e6);
+      if (time < least) {
+        least = time;
+        best = W8Plan{kind, t, splits};
+      }
     }
   }
-  const int t = tiles(best), stages = (K + 127) / 128;
-  const int splits = best == 1 && (stages >= 48 ? 2 : 8) * t <= cus && stages >= 24 ? min(min(4, cus / t), stages / 12) : 1;
-  return W8Plan{best, t, splits};
+  return best;
 }
 
 int64_t w8_workspace_bytes(const W8Plan& p) {
