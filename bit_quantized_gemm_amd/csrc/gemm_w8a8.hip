@@ -9,7 +9,7 @@
 // holds its tile transposed: lane l owns token l & 31, element r is column
 // (r >> 2) * 8 + (l >> 5) * 4 + (r & 3): four runs of four columns.
 //
-// Two kernels.
+// Kernels.
 //   gemm_tile_kernel: bound by the matrix cores, and at the largest sizes by the power they draw (4096 x 28672 x 8192 at
 //     2.5 POP/s on quantized normal data, 3.0 on zeros).  The workgroup's four waves each own a quarter of a BM x BN tile.
 //     Stages of 128 bytes of K are copied from global memory straight into a ring of LDS buffers (LDS-DMA): whole
@@ -17,9 +17,14 @@
 //     stages: 1000 us instead of 935).  Stage rows are unpadded, 16-byte chunks at swizzled positions: the 16 lanes of a
 //     16-byte read hit distinct bank groups.  A stage is four K slices; a wave multiplies one slice while the next one's
 //     operands are read, one read or copy between two products.
+//     2048 x 4096 x 11008 (M x N x K) takes 86.5 us, 2.13 POP/s; the library's int8 product reaches 2.05.
 //   gemm_rows_kernel (few tokens, or few outputs): bound by reading the weights.  A workgroup owns 16 columns, its
 //     waves divide K, and each wave loads its operands straight into registers, a batch of
-//     16-byte loads in flight at once; the waves' integer sums meet in LDS.
+//     16-byte loads in flight at once; the waves' integer sums meet in LDS.  Weights from HBM: 1 x 4096 x 4096 5.9 us,
+//     1 x 28672 x 8192 43 us (5.5 TB/s), 16 x 11008 x 4096 14.3 us (3.2 TB/s, and as many bytes of codes from the L2).
+//     48 columns a workgroup (a third of those) took 13.2 us there, more elsewhere.
+//   linear_rows_kernel: the same for at most four tokens with the quantizer in front, one launch for two: 1 x 4096 x 4096
+//     6.2 us against 2.6 + 5.9.
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "w8a8_row.h"

