@@ -79,7 +79,7 @@ bool valid_attention(int32_t total_q, int32_t q_heads, int32_t heads, int32_t di
   if (rows >= ((uint64_t)1 << 30)) return false;
   // a launch has less than 2^32 threads
   const atom::Kv4Plan p = atom::kv4_plan(total_q, q_heads, heads, dim, batch, max_q, max_len);
-  return (uint64_t)batch * (uint64_t)heads * (uint64_t)p.row_tiles < ((uint64_t)1 << 24);
+  return (uint64_t)batch * (uint64_t)heads * (uint64_t)p.row_tiles * (uint64_t)p.chunks < ((uint64_t)1 << 24);
 }
 
 }  // namespace

@@ -66,8 +66,7 @@ int atom_kv4_read(const atom_kv4_cache *cache, const int64_t *slots, int32_t tok
  * sequence are left as they were.  out = softmax(scale * q . k) v with fp32 statistics and sums; scale > 0.
  * A token's weight times its value scale is rounded to fp16 with the largest value scale that the query sees as its unit.
  * max_q and max_len bound the sequences' queries and tokens on the host: queries and tokens behind them
- * are left out.  batch * H row tiles (16 rows of max_q * Hq / H, or 128 where that is above 64) must stay
- * below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage
+ * are left out.  batch * H * ceil(max_q * Hq / H / 128) must stay below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage
  * out, no fault).  What lies in the pages behind a sequence's end is never used in a result.
  * workspace: atom_kv4_attention_workspace_bytes(...) bytes (0 when none is needed) let long sequences be
  * divided among workgroups; with less (or NULL) they run undivided.  Contents on entry do not matter;

@@ -393,18 +393,51 @@ def test_two_calls_at_once_on_two_streams():
         assert torch.equal(x, want[0]) and torch.equal(y, want[1])
 
 
-def test_prompt_parts_against_long_contexts():
-    """A part of a prompt against a long context, divided among workgroups, in pages of every size, with pages that end inside
-    a tile, a sequence shorter than the others and one without tokens."""
-    for page, D, dtype in ((16, 128, torch.bfloat16), (32, 64, torch.float16), (128, 256, torch.float16), (64, 128, torch.float16)):
-        say(f"[kv4 prompt part] page={page} D={D}")
-        b = Batch([2111, 130, 0, 700], [70, 66, 5, 1], 4, 2, D, page, dtype, seed=page, spare_rows=1)
-        assert bq.atom_kv4_attention_workspace_bytes(b.total + 1, 4, 2, D, 4, 70, 2111) > 0
-        out = torch.full_like(b.q, 7.0)
-        b.run(out=out, max_q=70, max_len=2111)
-        b.check(out)
-        assert torch.all(out[b.total:] == 7)
-        b.check(b.run(max_q=70, max_len=2111, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")), what="undivided")
+# Bounds far above what the sequences hold choose the launch of a large batch: many query rows in workgroups of 128 (which
+# small batches do not take), whole, or divided against a context of up to 16384 tokens.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("page,D,G", [(16, 128, 2), (32, 64, 3), (64, 64, 1), (64, 128, 4), (128, 256, 2), (16, 256, 3)])
+def test_prompts_in_a_large_batch(page, D, G, dtype):
+    lens, count = [300, 129, 0, 97], [150, 129, 4, 1]
+    say(f"[kv4 prompts] page={page} D={D} G={G} {dtype}")
+    b = Batch(lens, count, 4 * G, 4, D, page, TYPES[dtype], seed=page + G, spare_rows=2200 - sum(count), stretch=800 // page)
+    assert bq.atom_kv4_attention_workspace_bytes(2200, 4 * G, 4, D, 4, 2200, 1100) == 0
+    out = torch.full_like(b.q, 7.0)
+    b.run(out=out, max_len=1100)
+    b.check(out)
+    assert torch.all(out[b.total:] == 7)
+    again = torch.full_like(out, 7.0)
+    b.run(out=again, max_len=1100)
+    assert torch.equal(out, again)
+    # a row of zeros, one that holds a NaN, and tokens behind the queries that are huge: none touches another row
+    b.q[1], b.q[3, 0, 0] = 0, float("nan")
+    at = torch.arange(299, 300, device="cuda")
+    slots = b.table[0].long()[at // page] * page + at % page
+    x = torch.full((1, 4, D), float("inf"), dtype=torch.float16, device="cuda")
+    bq.atom_kv4_append(x, x, slots, b.cache)
+    got = b.run(out=torch.full_like(out, 7.0), max_len=1100)
+    assert not got[3, 0].isfinite().any()
+    got[3, 0] = out[3, 0]
+    keep = [r for r in range(b.total) if r not in (1, 149)]
+    # each weight is rounded once on either side (2^-12 of it), the result once (eps / 2): values are below 6
+    torch.testing.assert_close(got[keep], out[keep], rtol=2 * torch.finfo(out.dtype).eps, atol=2.0**-11 * 6)
+
+
+@pytest.mark.parametrize("page,D,dtype", [(16, 128, "bf16"), (32, 64, "fp16"), (128, 256, "fp16"), (64, 128, "fp16")])
+def test_prompt_parts_against_long_contexts(page, D, dtype):
+    """A part of a prompt against a long context, divided among workgroups, with pages that end inside a tile, sequences
+    shorter than the others and one without tokens."""
+    say(f"[kv4 prompt part] page={page} D={D}")
+    count = [70, 66, 5, 1]
+    b = Batch([4200, 130, 0, 700], count, 8, 2, D, page, TYPES[dtype], seed=page, spare_rows=256 - sum(count),
+              stretch=(16384 - 4200) // page)
+    assert bq.atom_kv4_attention_workspace_bytes(256, 8, 2, D, 4, 256, 16384) > 0
+    out = torch.full_like(b.q, 7.0)
+    b.run(out=out, max_len=16384)
+    b.check(out)
+    assert torch.all(out[b.total:] == 7)
+    b.check(b.run(max_len=16384, workspace=torch.empty(0, dtype=torch.uint8, device="cuda")), what="undivided")
+    b.check(b.run(max_q=70, max_len=4200), what="tight bounds")
 
 
 def test_shared_and_repeated_pages():
