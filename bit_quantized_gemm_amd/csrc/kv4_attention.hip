@@ -777,16 +777,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
 }
 
 // ------------------------------------------------------------------ joining the chunks of a divided sequence
-// One workgroup per query row: the chunks' sums, each scaled to the largest reference.  Wave v adds chunks v, v + 4,
+// SPLIT waves a query row: its chunks' sums, each scaled to the largest reference.  Wave v of them adds chunks v, v + SPLIT,
 // ... in order, then the waves' sums are added in order.  Sums are read beside the statistics, eight in flight, also of
-// chunks that hold no token of the row (whatever is there, left out below): one memory latency less.
-template <class T, int D>
+// chunks that hold no token of the row (whatever is there, left out below): one memory latency less.  Four waves a row
+// are for few rows of many chunks (64 rows of 64 chunks 18.0 us in all, 19.4 with one; 8192 rows of 8: 75.8 and 65.1).
+template <class T, int D, int SPLIT>
 __global__ __launch_bounds__(256) void join_kernel(Args a) {
   constexpr int C = D / 64;
-  __shared__ float part[4][D];
+  __shared__ float part[SPLIT > 1 ? 4 : 1][D];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int most = a.max_q * a.group;
-  const int bh = blockIdx.x / most, r = blockIdx.x - bh * most;
+  const int most = a.max_q * a.group, at = SPLIT > 1 ? (int)blockIdx.x : (int)blockIdx.x * 4 + wave, v = SPLIT > 1 ? wave : 0;
+  const int bh = at / most, r = at - bh * most;
+  if (bh >= a.batch * a.heads) return;       // (SPLIT = 1: the last workgroup's waves past the rows)
   const int b = bh / a.heads, head = bh - b * a.heads;
   const kv4::Sequence seq = kv4::sequence(a.q_start[b], a.q_start[b + 1], a.lens[b], a.total_q, a.max_q, a.max_len,
                                           a.width << a.log_page);
@@ -802,9 +804,9 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
 #pragma unroll
-      for (int j = 0; j < C; ++j) x[k][j] = src[min(c0 + 4 * k, a.chunks - 1) * all_rows * D + j];
+      for (int j = 0; j < C; ++j) x[k][j] = src[min(c0 + SPLIT * k, a.chunks - 1) * all_rows * D + j];
   };
-  load(wave);
+  load(v);
   const float2 st = *reinterpret_cast<const float2*>(ml + min(lane, a.chunks - 1) * all_rows * 2);
   const float M = lane < chunks ? st.x : kNegInf;
   float l = lane < chunks ? st.y : 0.0f;
@@ -816,23 +818,28 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) l += __shfl_xor(l, d);
   float sum[C] = {};
-  for (int c0 = wave; c0 < chunks; c0 += 32) {
-    if (c0 > wave) load(c0);
+  for (int c0 = v; c0 < chunks; c0 += 8 * SPLIT) {
+    if (c0 > v) load(c0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float g = __shfl(f, min(c0 + 4 * k, 63));
-      if (c0 + 4 * k < chunks)
+      const float g = __shfl(f, min(c0 + SPLIT * k, 63));
+      if (c0 + SPLIT * k < chunks)
 #pragma unroll
         for (int j = 0; j < C; ++j) sum[j] += g * x[k][j];
     }
   }
-#pragma unroll
-  for (int j = 0; j < C; ++j) part[wave][lane * C + j] = sum[j];
-  __syncthreads();
   const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  if (threadIdx.x < D) {
-    const int d = threadIdx.x;
-    a.out[id * D + d] = T::store((part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+  if constexpr (SPLIT == 1) {
+#pragma unroll
+    for (int j = 0; j < C; ++j) a.out[id * D + lane * C + j] = T::store(sum[j] * inv);
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) part[wave][lane * C + j] = sum[j];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      const int d = threadIdx.x;
+      a.out[id * D + d] = T::store((part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
+    }
   }
 }
 
@@ -850,7 +857,10 @@ void launch(const Args& a, int kind, hipStream_t st) {
     hipLaunchKernelGGL((prompt_kernel<T, D>), grid, dim3(256), 0, st, a);
   if (a.chunks > 1) {
     const int64_t rows = (int64_t)a.batch * a.heads * a.max_q * a.group;
-    hipLaunchKernelGGL((join_kernel<T, D>), dim3((unsigned)rows), dim3(256), 0, st, a);
+    if (rows >= 1024 || a.chunks <= 8)
+      hipLaunchKernelGGL((join_kernel<T, D, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
+    else
+      hipLaunchKernelGGL((join_kernel<T, D, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
   }
 }
 
@@ -869,10 +879,10 @@ void launch(const Args& a, int kind, hipStream_t st) {
 // prompt_kernel, half as many of 256 channels):
 //   decode_kernel: 2, 5 a round, and for each 128 tokens (a unit a wave) 2.0, 1.2 or 0.85 with the units full, half or a quarter full
 //   prompt_kernel: 3.5, 5 a round, and for each 64 tokens 2.45 or 1.55 with the units full or half full; 1.55 for the longest
-//   joining: 4, 1.3 for 1000 rows, and the partial sums' way through memory.
-// Measured (us), decode_kernel and prompt_kernel whole, and the better of them in its best division: 16 sequences of 2048 tokens, 8 kv heads
-// of 128 channels, 80 rows each: 38, 60, 52; 256 rows: 74, 61, 100; one sequence of 8192, 512 rows: 57, 194, 47; prompts of 2 x 400
-// tokens, 32 heads: 24, 20, 60; 2 x 1600: 119, 76, 243; 4 x 1000, 4 kv heads of 256 channels, 400 rows: 24, 60, 44.
+//   joining: 4, 0.4 for 1000 rows, and the partial sums' way through memory.
+// Measured (us), decode_kernel and prompt_kernel whole, and the best of both divided: 16 sequences of 2048 tokens, 8 kv heads of 128
+// channels, 80 rows each: 38, 60, 40; 256 rows: 74, 62, 69; one sequence of 8192, 512 rows: 57, 194, 44; prompts of 2 x 400 tokens, 32
+// heads: 24, 21, 37; 2 x 1600: 114, 76, 153; 4 x 1000, 4 kv heads of 256 channels, 400 rows: 24, 60, 38.
 Kv4Plan kv4_plan(int total_q, int q_heads, int heads, int dim, int batch, int max_q, int max_len) {
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
   auto plan = [&](int kind, int64_t chunks) {
@@ -913,7 +923,7 @@ Kv4Plan kv4_plan(int total_q, int q_heads, int heads, int dim, int batch, int ma
         time = steps * (full * (slots == 1 ? 1.55 : 2.45) + last);
         time = 3.5 + 5.0 * (full + (rest > 0.0)) + narrow * wide * (time > most ? time : most);
       }
-      if (p.chunks > 1) time += 4.0 + 1.3e-3 * all + all * p.chunks * dim * 8 / 5e6;
+      if (p.chunks > 1) time += 4.0 + 0.4e-3 * all + all * p.chunks * dim * 8 / 5e6;
       if (least < 0.0 || time < least) {
         least = time;
         best = p;
