@@ -135,6 +135,7 @@ int atom_gemm_w8a8(const void* Xq, const float* sx, const void* Wq, const float*
 
 int64_t atom_linear_w8a8_workspace_bytes(int32_t M, int32_t N, int32_t K) {
   if (!valid_gemm8(M, N, K)) return -(int64_t)ATOM_E_SHAPE;
+  if (atom::linear_rows_fits(M, N, K)) return 0;
   return (int64_t)((uint64_t)M * row_bytes8(K) + up16((uint64_t)M * 4)) +
          atom::w8_workspace_bytes(atom::w8_plan(M, N, K));
 }
@@ -142,19 +143,20 @@ int64_t atom_linear_w8a8_workspace_bytes(int32_t M, int32_t N, int32_t K) {
 int atom_linear_w8a8(const void* X, int64_t ldx, int32_t dtype, const void* Wq, const float* sw, const void* bias,
                      int32_t M, int32_t N, int32_t K, void* Y, void* workspace, int64_t workspace_bytes,
                      void* stream) {
-  if (!X || !Wq || !sw || !Y || !workspace) return ATOM_E_NULL;
+  if (!X || !Wq || !sw || !Y) return ATOM_E_NULL;
   if (!valid_gemm8(M, N, K) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
   if (!valid_x(X, ldx, M, K)) return aligned(X, 2) ? ATOM_E_SHAPE : ATOM_E_ALIGN;
   const int64_t need = atom_linear_w8a8_workspace_bytes(M, N, K);
+  if (need > 0 && !workspace) return ATOM_E_NULL;
   if (workspace_bytes < need) return ATOM_E_SHAPE;
-  if (!aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y) || !aligned16(workspace))
+  if (!aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y) || (need > 0 && !aligned16(workspace)))
     return ATOM_E_ALIGN;
   const Range in[4] = {range_of(X, x_bytes(ldx, M, K)), range_of(Wq, (uint64_t)N * row_bytes8(K)),
                        range_of(sw, (uint64_t)N * 4), range_of(bias, bias ? (uint64_t)N * 2 : 0)};
   const Range out[2] = {range_of(Y, (uint64_t)M * N * 2), range_of(workspace, (uint64_t)need)};
-  if (int s = check_overlap(in, bias ? 4 : 3, out, 2)) return s;
+  if (int s = check_overlap(in, bias ? 4 : 3, out, need > 0 ? 2 : 1)) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (atom::linear_rows_fits(M, N, K))
+  if (need == 0)
     return hip_status(atom::launch_linear_rows(static_cast<const uint16_t*>(X), ldx, static_cast<const int8_t*>(Wq), sw,
                                                static_cast<const uint16_t*>(bias), M, N, K, dtype == ATOM_BF16,
                                                static_cast<uint16_t*>(Y), st));

@@ -185,7 +185,8 @@ def atom_gemm_w8a8(Xq, sx, Wq, sw, K, bias=None, Y=None, dtype=None, workspace=N
 def linear_w8a8(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
     """The layer: X (fp16 / bf16 [M, K]; rows may lie apart) quantized and multiplied with packed weights in
     one call.  Y has X's type.  `workspace`: 1-D uint8 of at least ``atom_linear_w8a8_workspace_bytes``
-    bytes (calls that may overlap need one each), else a torch buffer is taken for the call."""
+    bytes (calls that may overlap need one each; none for the few tokens that take one launch), else a torch buffer is
+    taken for the call when one is needed."""
     torch = _bq._torch()
     T = torch.Tensor
     if stream is None and Y is None and workspace is None and type(X) is T and type(Wq) is T and type(sw) is T:
@@ -203,10 +204,10 @@ def linear_w8a8(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
                          and bias.is_contiguous() and bias.get_device() == d)):
                 need = _linear_bytes(M, N, K)
                 Y = X.new_empty((M, N))
-                workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+                workspace = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
                 status = _bq.load_library().atom_linear_w8a8(
                     X.data_ptr(), ldx, int(t is torch.bfloat16), Wq.data_ptr(), sw.data_ptr(),
-                    None if bias is None else bias.data_ptr(), M, N, K, Y.data_ptr(), workspace.data_ptr(), need,
+                    None if bias is None else bias.data_ptr(), M, N, K, Y.data_ptr(), workspace.data_ptr() if need else None, need,
                     torch._C._cuda_getCurrentRawStream(d))
                 if status:
                     _bq._check(status, "atom_linear_w8a8")
@@ -220,7 +221,7 @@ def linear_w8a8(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
     if Y is None:
         Y = empty((M, N), X.dtype, X, stream)
     if workspace is None:
-        workspace = empty((need,), torch.uint8, X, stream)
+        workspace = empty((need,), torch.uint8, X, stream) if need else None
     elif getattr(workspace, "dim", lambda: -1)() != 1:
         raise _bq.AtomError("workspace must be a 1-D uint8 tensor")
     elif workspace.numel() < need:
@@ -232,6 +233,6 @@ def linear_w8a8(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
         raise _bq.AtomError(f"X is on {X.device}, the other operands on {Y.device}")
     with on_device(X):
         _bq._check(_bq.load_library().atom_linear_w8a8(X.data_ptr(), ldx, kind, p[1], p[2], p[3], M, N, K, p[0], p[4],
-                                                       int(workspace.numel()), _bq._stream(stream, X.device)),
+                                                       0 if workspace is None else int(workspace.numel()), _bq._stream(stream, X.device)),
                    "atom_linear_w8a8")
     return Y

@@ -56,9 +56,9 @@ int atom_gemm_w8a8(const void *Xq, const float *sx, const void *Wq, const float 
                    void *stream);
 
 /*
- * The layer in one call: quantizes X into the workspace, then Y as above.  The workspace holds at
- * least atom_linear_w8a8_workspace_bytes(M, N, K) bytes (ATOM_E_SHAPE otherwise); its contents on
- * entry do not matter, and calls that may overlap in time need one each.
+ * The layer in one call: quantizes X into the workspace, then Y as above; the few tokens that take one launch need none
+ * (0 bytes, NULL).  The workspace holds at least atom_linear_w8a8_workspace_bytes(M, N, K) bytes (ATOM_E_SHAPE
+ * otherwise); its contents on entry do not matter, and calls that may overlap in time need one each.
  */
 int64_t atom_linear_w8a8_workspace_bytes(int32_t M, int32_t N, int32_t K);
 int atom_linear_w8a8(const void *X, int64_t ldx, int32_t dtype, const void *Wq, const float *sw, const void *bias,

@@ -93,9 +93,10 @@ def test_gemm_w8a8_validation(lib):
 
 def test_linear_w8a8_validation(lib):
     g = lib.atom_linear_w8a8
-    need = bq.atom_linear_w8a8_workspace_bytes(4, 4, 256)
-    assert need >= 4 * 256 + 16
-    ok = (A, 256, 0, C, D, None, 4, 4, 256, E, F, need, S)
+    assert bq.atom_linear_w8a8_workspace_bytes(4, 4, 256) == 0               # one launch: nothing to keep
+    need = bq.atom_linear_w8a8_workspace_bytes(8, 4, 256)
+    assert need >= 8 * 256 + 32
+    ok = (A, 256, 0, C, D, None, 8, 4, 256, E, F, need, S)
 
     def call(**k):
         names = ("x", "ldx", "t", "wq", "sw", "bias", "m", "n", "k", "y", "ws", "nws", "s")
@@ -202,7 +203,7 @@ def test_binding_refusals(lib, monkeypatch):
         lambda: bq.atom_gemm_w8a8(Xq, sx, Wq, sw, 200, workspace=z((8, 8), dtype=u8)),
         lambda: bq.linear_w8a8(X, z((6, 200), dtype=i8), sw),
         lambda: bq.linear_w8a8(X, Wq, z((7,), dtype=f32)),
-        lambda: bq.linear_w8a8(X, Wq, sw, workspace=z((16,), dtype=u8)),
+        lambda: bq.linear_w8a8(z((8, 200), dtype=f16), Wq, sw, workspace=z((16,), dtype=u8)),
         lambda: bq.atom_kv4_append(K, K[:4], slots, cache),
         lambda: bq.atom_kv4_append(K, K, z((5, 1), dtype=i64), cache),
         lambda: bq.atom_kv4_append(z((5, 2, 32), dtype=f16), K, slots, cache),

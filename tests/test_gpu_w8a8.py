@@ -147,6 +147,8 @@ def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
         Y = bq.linear_w8a8(x, Wq, sw)
         torch.testing.assert_close(Y, bq.atom_gemm_w8a8(*bq.atom_quantize_w8a8(x), Wq, sw, K, dtype=t), rtol=0, atol=0)
         torch.testing.assert_close(Y, bq.linear_w8a8(x.contiguous(), Wq, sw), rtol=0, atol=0)
+        ws = torch.empty(bq.atom_linear_w8a8_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+        torch.testing.assert_close(Y, bq.linear_w8a8(x, Wq, sw, Y=torch.empty_like(Y), workspace=ws), rtol=0, atol=0)
     keep = wide.clone()
     odd = torch.full((M, K + 9), float("nan"), dtype=t, device="cuda")       # what lies around the rows is not read into them
     odd[:, 5:5 + K] = keep[:, 5:5 + K]
