@@ -126,7 +126,7 @@ __device__ __forceinline__ float exponent_of(uint32_t word) {
 // after theirs: one unit of registers, so that four waves fit a SIMD (D = 128) and hide each other's latency.
 //
 // Measured (GPU time): 16 sequences of up to 2048 tokens, 32 kv heads of 128 channels: 24 us, 4.3 TB/s of codes and parameters (a plain
-// read of as many bytes takes 17); 4 of up to 32768, 8 kv heads, 64 query heads: 29.7 us and 4 to join, 4.0 TB/s.  There the
+// read of as many bytes takes 17); 4 of up to 32768, 8 kv heads, 64 query heads: 28 us and 4 to join, 4.5 TB/s.  There the
 // vector ALUs' 300 instructions a unit take half the time and do not hide wholly behind the loads.  Two units of
 // registers (half the waves) and 16 chunks instead of 8 gained nothing.
 template <class T, int D, int WAVES>
@@ -381,7 +381,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 // Running maximum: ref = m + E with m the largest score of the row's first tile, raised only when some score of the
 // wave exceeds it by 8 (weights are at most 2^8 then) or some value scale exceeds 2^E.
 //
-// Measured: 2 prompts of up to 4096 tokens, 32 heads of 128 channels: 287-299 us (0.81-0.85 PFLOP/s of the visible half; the matrix cores' rate
+// Measured: 2 prompts of up to 4096 tokens, 32 heads of 128 channels: 279-299 us (0.81-0.87 PFLOP/s of the visible half; the matrix cores' rate
 // alone would take 177).  The vector ALUs are busy 64% of a tile's 2.4 us, the matrix cores 42%, and the clock gives way to
 // the power drawn: the same call takes 334 us on normal data of full length, 281 on zeros.  Of a workgroup's time 8 us are its
 // start, first tile and end.  64 rows a wave with one wave a SIMD (half the LDS reads and unpacking a row) took 499 us, eight waves a
