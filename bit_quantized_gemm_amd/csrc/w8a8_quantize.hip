@@ -5,13 +5,15 @@
 // code, so a row is read once into registers by the threads that share it, its maximum is joined
 // (in a wave by DPP-free shuffles, across waves through LDS) and the codes are made from the registers.
 // The threads of a row follow its length: a wave for short rows (four rows a workgroup, no
-// barrier), 256 threads up to 16384 elements, 1024 beyond.  Rows whose elements no aligned 16-byte load fits
-// (odd K or stride, shifted views) are read by unaligned ones, the last few elements one by one.
+// barrier), 256 or 512 threads up to 16384 elements, 1024 beyond; few rows, which leave units idle, take more (us, with the
+// other count: 333 x 1155 3.3 and 3.7, but 4000 x 2048 8.6 and 5.4; 600 x 8192 4.3 and 4.7, but 2048 x 8192 10.2 and 9.6).
+// Rows whose elements no aligned 16-byte load fits (odd K or stride, shifted views) are read by unaligned ones, the last few
+// elements one by one.
 //
 // The codes are those of an IEEE divide, without its dozen instructions an element: see quotient().
 //
-// Measured: 2048 x 11008 13.4 us and 4096 x 8192 21 us (5.0 and 4.8 TB/s; a copy reaches 5.1), 16 x 4096 2.6 us, of which the launch is
-// most, 333 x 1155 (unaligned rows) 4.1 us.
+// Measured: 2048 x 11008 12.8 us and 4096 x 8192 17.0 us (5.3 and 5.9 TB/s with the input in the caches, a copy of memory reaches 5.1),
+// 16 x 4096 2.9 us, of which the launch is most, 333 x 1155 (unaligned rows) 3.3 us.
 #include "w8a8_row.h"
 
 namespace atom {
@@ -70,10 +72,12 @@ void dispatch(const uint16_t* X, int64_t ldx, int rows, int K, int8_t* Xq, float
   const int Kp = (K + 127) / 128 * 128;
   const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
   if (Kp <= 512) launch<T, 64, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 2048 && rows <= 384) launch<T, 256, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
   else if (Kp <= 2048) launch<T, 64, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
   else if (Kp <= 4096) launch<T, 256, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 8192 && rows <= 1024) launch<T, 512, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
   else if (Kp <= 8192) launch<T, 256, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 16384) launch<T, 256, 8>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (Kp <= 16384) launch<T, 512, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
   else launch<T, 1024, 8>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
 }
 

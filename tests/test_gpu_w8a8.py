@@ -59,7 +59,7 @@ def check_codes(Xq, sx, x):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (5, 64), (4, 128), (9, 129), (2, 512), (7, 520), (6, 2048), (5, 2049),
                                     (3, 4096), (3, 4097), (2, 8192), (2, 11008), (3, 16384), (2, 16385), (2, 65536),
-                                    (1, 65535)])
+                                    (1, 65535), (385, 520), (390, 1155), (400, 2048), (1025, 8192), (1026, 5001)])
 def test_quantize(rows, K, dtype):
     say(f"[w8a8 quantize] {rows}x{K} {dtype}")
     x = make(rows, K, TYPES[dtype], rows + K)
