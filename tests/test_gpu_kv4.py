@@ -272,6 +272,19 @@ def test_long_sequences_divided(q, Hq, H, D):
     b.check(b.run(), what="bounds from the table")
 
 
+@pytest.mark.parametrize("lens,count,Hq,H,D", [([15000, 400], [20, 20], 32, 4, 128), ([16000, 900, 12], [100, 33, 12], 4, 1, 64),
+                                               ([16384, 5000], [1, 1], 8, 1, 64), ([16384], [40], 32, 1, 128),
+                                               ([9000, 16000], [2, 1], 2, 1, 256)])
+def test_many_chunks(lens, count, Hq, H, D):
+    """Divided 10 to 64 ways: joined by one wave a row in several batches, and by four."""
+    say(f"[kv4 many chunks] {lens} {count} heads={Hq}/{H} D={D}")
+    b = Batch(lens, count, Hq, H, D, 64, seed=D)
+    assert bq.atom_kv4_attention_workspace_bytes(sum(count), Hq, H, D, len(lens), max(count), 16384) >= 10 * sum(count) * Hq * D * 4
+    out = b.run(max_q=max(count), max_len=16384)
+    b.check(out)
+    assert torch.equal(out, b.run(max_q=max(count), max_len=16384))
+
+
 @pytest.mark.parametrize("k", [dict(q_gain=60.0), dict(q_gain=1e-4), dict(v_gain=1e-4), dict(v_gain=300.0), dict(k_gain=1e-3),
                                dict(k_gain=40.0, q_gain=0.02), dict(scale=3.0), dict(scale=1e-3)])
 @pytest.mark.parametrize("q", [1, 30])
