@@ -77,9 +77,8 @@ bool valid_attention(int32_t total_q, int32_t q_heads, int32_t heads, int32_t di
   if (max_len < 1 || max_len > (1 << 30)) return false;
   const uint64_t rows = (uint64_t)max_q * (uint64_t)(q_heads / heads);   // of one sequence and kv head
   if (rows >= ((uint64_t)1 << 30)) return false;
-  // a launch has less than 2^32 threads
-  const atom::Kv4Plan p = atom::kv4_plan(total_q, q_heads, heads, dim, batch, max_q, max_len);
-  return (uint64_t)batch * (uint64_t)heads * (uint64_t)p.row_tiles * (uint64_t)p.chunks < ((uint64_t)1 << 24);
+  const atom::Kv4Plan p = atom::kv4_plan(q_heads, heads, dim, batch, max_q, max_len);
+  return (uint64_t)batch * (uint64_t)heads * (uint64_t)p.row_tiles * (uint64_t)p.chunks < (uint64_t)kv4::kMaxGroups;
 }
 
 }  // namespace
@@ -207,7 +206,7 @@ int atom_kv4_read(const atom_kv4_cache* cache, const int64_t* slots, int32_t tok
 int64_t atom_kv4_attention_workspace_bytes(int32_t total_q, int32_t q_heads, int32_t heads, int32_t dim,
                                            int32_t batch, int32_t max_q, int32_t max_len) {
   if (!valid_attention(total_q, q_heads, heads, dim, batch, max_q, max_len)) return -(int64_t)ATOM_E_SHAPE;
-  return atom::kv4_workspace_bytes(atom::kv4_plan(total_q, q_heads, heads, dim, batch, max_q, max_len), total_q,
+  return atom::kv4_workspace_bytes(atom::kv4_plan(q_heads, heads, dim, batch, max_q, max_len), total_q,
                                    q_heads, dim);
 }
 
@@ -226,7 +225,7 @@ int atom_kv4_attention(const void* Q, int64_t q_stride, const atom_kv4_cache* ca
   if (!aligned16(Q) || (total_q > 1 && q_stride % 8) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4) ||
       !aligned16(out) || !cache_aligned(cache))
     return ATOM_E_ALIGN;
-  atom::Kv4Plan plan = atom::kv4_plan(total_q, q_heads, cache->heads, cache->dim, batch, max_q, max_len);
+  atom::Kv4Plan plan = atom::kv4_plan(q_heads, cache->heads, cache->dim, batch, max_q, max_len);
   int64_t need = atom::kv4_workspace_bytes(plan, total_q, q_heads, cache->dim);
   if (need > 0 && (!workspace || workspace_bytes < need)) {   // too little scratch: undivided
     plan.chunks = 1;

@@ -9,6 +9,7 @@
 
 #include "atom_kv4.h"
 #include "atom_w8a8.h"
+#include "kv4_plan.h"
 
 namespace atom {
 
@@ -82,12 +83,8 @@ struct Kv4Attention {
   bool bf16;
   uint16_t* out;
 };
-// How a call is run: query rows (query tokens x query heads of one kv head) per workgroup, and the
-// tokens of one chunk of a sequence; chunks > 1 need scratch.
-struct Kv4Plan {
-  int kind, row_tiles, chunks, chunk_tokens;
-};
-Kv4Plan kv4_plan(int total_q, int q_heads, int heads, int dim, int batch, int max_q, int max_len);
+using Kv4Plan = kv4::Plan;
+Kv4Plan kv4_plan(int q_heads, int heads, int dim, int batch, int max_q, int max_len);   // for this device's compute units
 int64_t kv4_workspace_bytes(const Kv4Plan& plan, int total_q, int q_heads, int dim);
 hipError_t launch_kv4_attention(const Kv4Attention& a, const Kv4Plan& plan, float* work, hipStream_t stream);
 
