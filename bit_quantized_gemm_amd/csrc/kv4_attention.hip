@@ -15,15 +15,16 @@
 // four-token blocks in the cache are the operand order of that product.
 //
 // Ranges.  The queries are scaled by a power of two so that the largest element lies in [2^13, 2^14): of a row in decode_kernel,
-// of a workgroup's rows in prompt_kernel.  fp16 then holds fp16 and bf16 queries exactly down to 2^-24 of that element.  Weights are
-// rounded to fp16 (relative 2^-12 each, as the output's own rounding) after a power of two, 2^-E >= 1 / (largest u that
-// the row has seen), keeps them in fp16's range: both the weights and the sum of p carry it, so it leaves the quotient.  The zero
-// points multiply the rounded weights too, so a rounding error acts on (v - b), not on v and b apart.  Scores, maxima and all
-// sums are fp32.
+// of a workgroup's rows in prompt_kernel.  fp16 then holds fp16 and bf16 queries exactly down to 2^-24 of that element.  The
+// weights w are rounded to fp16: 2^-11 of each, as fp16's own rounding of the output.  Sums of w (v - b) and of p carry the same power
+// of two, so it leaves the quotient; it is the row's own and follows the largest *weight* (score and value scale together): a token
+// of large values and no weight costs the others nothing.  The zero points multiply the rounded weights too, so a
+// rounding error acts on (v - b), not on v and b apart.  Scores, maxima and all sums are fp32.
 //
-// Running maximum: the reference c1 m + E is raised, and the sums rescaled, in a wave-uniform branch that random data take in
-// the first few tiles only: decode_kernel's when some score of the wave lies above its row's m or some u above its row's 2^E,
-// prompt_kernel's when a score lies 2^8 above.  m and E are a row's own, of tokens that it sees.
+// Reference: weights are 2^(score - ref) u with ref such that the largest of a row lies in [2^4, 2^15.1] from the row's first tile
+// on: fp16 then holds whatever is above 2^-18 of it to 11 bits, and the rest to steps of 2^-28.  When some weight of
+// a wave would pass 2^15, ref is raised so that the row's largest is 2^4 and the sums are rescaled, in a wave-uniform branch that
+// random data take once.  It counts tokens that the row sees, no others.
 #include "atom_internal.h"
 #include "kv4_layout.h"
 #include "serve_internal.h"
@@ -54,6 +55,11 @@ template <int B>
 struct Half {
   static constexpr int value = B;
 };
+
+// A value that all lanes hold, in a scalar register.
+__device__ __forceinline__ float uniform(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, x)));
+}
 
 // max over lanes l, l ^ 32 and (kAll) l ^ 16 of a wave
 template <bool kAll>
@@ -113,10 +119,21 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
 
 __device__ __forceinline__ float low_half(uint32_t w) { return elem<Fp16>(w, 0); }
 __device__ __forceinline__ float high_half(uint32_t w) { return elem<Fp16>(w, 1); }
-// E for a word whose high half is the largest scale: scale <= 2^E
-__device__ __forceinline__ float exponent_of(uint32_t word) {
-  const float s = high_half(word);
-  return (float)max(-24, (int)(__builtin_bit_cast(uint32_t, s) >> 23) - 126);
+
+constexpr float kTarget = 4.0f, kLimit = 15.0f;   // log2 of a row's largest weight: after ref is raised, and at most
+
+// How far ref rises for a row whose largest weight is 2^top: at the row's first tokens wherever that is, later only upwards.
+__device__ __forceinline__ float rise(float top, bool first) {
+  if (first) return top == kNegInf ? 0.0f : top - kTarget;
+  return __builtin_fmaxf(top - kTarget, 0.0f);
+}
+
+// 47 + log2 of the scale in the high half of a parameter word, to 0.09 below: fp16's exponent and mantissa bits, read as a
+// fraction of 32 (the fifteen bits times 2^-10), and up to 2^-10 of the zero point's.  Scales below 2^-14, zero among them, count as
+// 2^-15 to 2^-14.
+constexpr float kLogBias = 47.0f;
+__device__ __forceinline__ float log_scale(uint32_t word) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_alignbit(0x42u, word, 8));
 }
 
 // ------------------------------------------------------------------ few query rows: bound by the cache's bytes
@@ -215,9 +232,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
   const int limit = kv4::visible(seq, qi);
 
   f32x4 o[NT], zs = {};
-  float m = kNegInf, ref = 0.0f, l = 0.0f;   // the largest y = score / c1 so far; c1 m + E; this lane's part of sum p 2^-E
-  uint32_t top_v = 0;                        // parameter word of the largest value scale so far (E of its high half)
-  float E = -24.0f;
+  float ref = 0.0f, l = 0.0f;                // l: this lane's part of sum 2^(score - ref)
+  bool first = true;
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x4{};
 
@@ -229,33 +245,20 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 #pragma unroll
       for (int t = 0; t < 2; ++t) s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(unpack_keys(k[t][w]), q[w], s[t], 0, 0, 0);
     load_keys(next);
-    uint32_t word = 0;
-    if (base + 32 > all) {                   // a row's masked tokens leave its E alone, whatever their scales
-      const int there = seq.tokens - base - 4 * h, seen = limit - base - 4 * h;
+    if (base + 32 > all) {                   // what lies behind the sequence's end is no number
+      const int there = seq.tokens - base - 4 * h;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          if (16 * t + r >= there) kp[t][r] = vp[t][r] = 0;   // what lies behind the sequence's end is no number
-          word = max(word, 16 * t + r < seen ? vp[t][r] : 0);
-        }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) word = max(word, vp[j >> 2][j & 3]);
+        for (int r = 0; r < 4; ++r)
+          if (16 * t + r >= there) kp[t][r] = vp[t][r] = 0;
     }
-    const bool raise_v = __any(word > (top_v | 0xFFFFu));
-    if (raise_v) {
-      word = max(word, (uint32_t)__shfl_xor((int)word, 16));
-      word = max(word, (uint32_t)__shfl_xor((int)word, 32));
-      top_v = max(top_v, word);
-    }
-    const float newE = raise_v ? exponent_of(top_v) : E;
 
-    float y[8], top = kNegInf;
+    float y[8], top = kNegInf;               // score - ref
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t par = kp[j >> 2][j & 3];
-      y[j] = __builtin_fmaf(-low_half(par), qs, s[j >> 2][j & 3]) * high_half(par);
+      y[j] = __builtin_fmaf(__builtin_fmaf(-low_half(par), qs, s[j >> 2][j & 3]) * high_half(par), c1, -ref);
     }
     load_key_parameters(next);
     if (base + 32 > all) {
@@ -265,26 +268,26 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
         if (16 * (j >> 2) + (j & 3) >= seen) y[j] = kNegInf;
     }
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) top = max3(top, y[j], y[j + 1]);
-    if (__any(top > m) || raise_v) {
-      const float new_m = __builtin_fmaxf(m, join_max<true>(top));
-      const float new_ref = new_m == kNegInf ? 0.0f : __builtin_fmaf(c1, new_m, newE);
-      const float f = m == kNegInf ? 0.0f : exp2_fast(ref - new_ref);
-      m = new_m;
-      ref = new_ref;
+    for (int j = 0; j < 8; j += 2)
+      top = max3(top, y[j] + log_scale(vp[j >> 2][j & 3]), y[j + 1] + log_scale(vp[j >> 2][(j & 3) + 1]));
+    if (first || __any(top > kLimit + kLogBias)) {
+      const float delta = rise(join_max<true>(top) - kLogBias, first), f = first ? 0.0f : exp2_fast(-delta);
+      first = false;
+      ref += delta;
       l *= f;
       zs *= f;
 #pragma unroll
       for (int i = 0; i < NT; ++i) o[i] *= f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] -= delta;
     }
     h8v p;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float e = exp2_fast(__builtin_fmaf(y[j], c1, -ref));
+      const float e = exp2_fast(y[j]);
       l += e;
       p[j] = (_Float16)(e * high_half(vp[j >> 2][j & 3]));
     }
-    E = newE;
 
     // zero points: rows of the first operand all alike, so every register of zs holds the same sum
     u32x4 zp;
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
   // Join the waves: everything to the largest reference (log2), then a tree over the sums.
   l = join_sum<true>(l);
   if (h == 0) {
-    sm[wave][l16] = m == kNegInf ? kNegInf : ref;
+    sm[wave][l16] = l > 0.0f || l != l ? ref : kNegInf;
     sl[wave][l16] = l;
   }
   __syncthreads();
@@ -378,8 +381,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 // The scale of the queries (a power of two) is one for the workgroup, so that a token's factor c1 * s can be made when it
 // is staged.  Rows far smaller than the largest one keep an absolute error of 2^-31 of the largest row's scores.
 //
-// Running maximum: ref = m + E with m the largest score of the row's first tile, raised only when some score of the
-// wave exceeds it by 8 (weights are at most 2^8 then) or some value scale exceeds 2^E.
+// Reference: a half tile's largest score and the largest value scale of the wave so far bound its weights; only where that bound
+// passes 2^15 are the weights themselves looked at.
 //
 // Measured: 2 prompts of up to 4096 tokens, 32 heads of 128 channels: 279-299 us (0.81-0.87 PFLOP/s of the visible half; the matrix cores' rate
 // alone would take 177).  The vector ALUs are busy 64% of a tile's 2.4 us, the matrix cores 42%, and the clock gives way to
@@ -462,8 +465,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       entry = page_of(base + kTile);
     } else {
       const int64_t kr = row_of(base + kt), vr = row_of(base + 4 * vb);
-      get(gk, reinterpret_cast<const uint32_t*>(a.k + kr * (D / 2)) + W * kp);
-      get(gv, reinterpret_cast<const uint32_t*>(a.v + vr * (D / 2)) + W * vp);
+      int wk = W * kp, wv = W * vp;          // kept from being added to the arrays' addresses ahead of the loop: no registers for that
+      asm("" : "+v"(wk), "+v"(wv));
+      get(gk, reinterpret_cast<const uint32_t*>(a.k + kr * (D / 2)) + wk);
+      get(gv, reinterpret_cast<const uint32_t*>(a.v + vr * (D / 2)) + wv);
       gkp = a.k_par[kr];
       gvp = *reinterpret_cast<const u32x4*>(a.v_par + vr);
     }
@@ -558,7 +563,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   f32x16 o[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) o[i] = f32x16{};
-  float ref = 0.0f, l = 0.0f, E = 0.0f, most = -1.0f;    // most: the largest value scale so far
+  float ref = 0.0f, l = 0.0f;
+  float most = 0x1p-40f, room = kLimit + 40.0f;          // a power of two that no value scale so far exceeds, kLimit - log2 of it
   bool first = true;
 
   // LDS addresses of this lane's operands in buffer 0; other buffers, halves and channels are constants further.
@@ -583,49 +589,37 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   f32x4 u[4];                                // value scales of the half tile whose weights come next (see read)
   // Masks, and raises the reference where it has to be raised; base: the half tile's first token.
   auto settle = [&](int buf, int t, int base) __attribute__((always_inline)) {
-    const bool edge = base + 32 > all;
-    float big;                               // a value scale: of any token, or the largest that the row sees
-    if (edge) {
-      big = 0.0f;
+    if (base + 32 > all) {
       const int seen = limit - base - 4 * h;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int i = 8 * (j >> 2) + (j & 3);
-        if (i >= seen)
-          y[j] = kNegInf;
-        else
-          big = __builtin_fmaxf(big, D < 256 ? u[j >> 2][j & 3] : lf[buf][1][32 * t + 4 * h + i]);
-      }
-      big = join_max<false>(big);
-    } else {
-      big = lf[buf][1][32 * t + l32];
+      for (int j = 0; j < 16; ++j)
+        if (8 * (j >> 2) + (j & 3) >= seen) y[j] = kNegInf;
     }
+    float big = lf[buf][1][32 * t + l32];    // a value scale: of any token
     float top = max3(y[0], y[1], y[2]);
 #pragma unroll
     for (int j = 3; j < 15; j += 2) top = max3(top, y[j], y[j + 1]);
     top = __builtin_fmaxf(top, y[15]);
-    if (first || __any(top > 8.0f - E || big > most)) {
-      float dE = 0.0f;
-      if (!edge) {
+    if (first || __any(top > room || big > most)) {
 #pragma unroll
-        for (int d = 16; d; d >>= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
+      for (int d = 16; d; d >>= 1) big = __builtin_fmaxf(big, __shfl_xor(big, d));
+      most = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, __builtin_fmaxf(big, most)) + 0x7FFFFFu) & 0x7F800000u);
+      room = uniform(kLimit + 127.0f - (float)(__builtin_bit_cast(uint32_t, most) >> 23));
+      most = uniform(most);
+      top = kNegInf;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {         // a scale of zero counts as 2^-40: its p stays in fp32's range
+        const float v = lf[buf][1][32 * t + 4 * h + 8 * (j >> 2) + (j & 3)];
+        top = __builtin_fmaxf(top, y[j] + __builtin_amdgcn_logf(__builtin_fmaxf(v, 0x1p-40f)));
       }
-      if (big > most) {
-        const float e = (float)max(-24, (int)(__builtin_bit_cast(uint32_t, big) >> 23) - 126);   // big <= 2^e
-        dE = first ? e - E : __builtin_fmaxf(e - E, 0.0f);
-        most = __builtin_ldexpf(1.0f, (int)(E + dE));
-      }
-      const float over = join_max<false>(top) + E;                         // above m
-      const float delta = (first ? (over == kNegInf ? 0.0f : over) : __builtin_fmaxf(over, 0.0f)) + dE;
-      const float f = first ? 0.0f : exp2_fast(-delta);
+      const float delta = rise(join_max<false>(top), first), f = first ? 0.0f : exp2_fast(-delta);
+      first = false;
       ref += delta;
-      E += dE;
       l *= f;
 #pragma unroll
       for (int i = 0; i < NT; ++i) o[i] *= f;
 #pragma unroll
       for (int j = 0; j < 16; ++j) y[j] -= delta;
-      first = false;
     }
   };
   auto scale4 = [&](const f32x4& f, int g) __attribute__((always_inline)) {

@@ -64,7 +64,9 @@ int atom_kv4_read(const atom_kv4_cache *cache, const int64_t *slots, int32_t tok
  *   out     : fp16 / bf16 [total_q, Hq, D] contiguous                         (output)
  * Query i of n sees the tokens 0 .. lens[b] - n + i; one that sees none gets zeros.  Rows outside every
  * sequence are left as they were.  out = softmax(scale * q . k) v with fp32 statistics and sums; scale > 0.
- * A token's weight times its value scale is rounded to fp16 with the largest value scale that the query sees as its unit.
+ * A token's weight times its value scale is rounded to fp16 with the largest such product that the query sees as its unit
+ * (2^-11 of it; products below 2^-18 of the largest: to steps of 2^-28 of the largest; a scale below 2^-14 counts as 2^-14
+ * in that unit).
  * max_q and max_len bound the sequences' queries and tokens on the host: queries and tokens behind them
  * are left out.  batch * H * ceil(max_q * Hq / H / 128) must stay below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage
  * out, no fault).  What lies in the pages behind a sequence's end is never used in a result.

@@ -1,0 +1,162 @@
+"""Attention over the 4-bit KV cache where queries, values and scores of very different size meet (needs an MI355X).
+
+Bound of |out - out64| for one query and channel, over the n tokens that it sees, with their exact weights w_t (sum 1), value
+scales u_t and key scales s_t:
+* weight t is off by a factor within 1 +- eta_t, eta_t = (D + 8) 2^-24 scale sum|q| 15 s_t + 100 * 2^-22: the fp32 roundings of a
+  sum of D + 2 products of codes and zero points below 16, and of its exponent (tokens further than 100 below the largest
+  score weigh nothing); likewise their sum;
+* w_t u_t is rounded to fp16: 2^-11 of it, or half of fp16's smallest step, 2^-25, where the largest w u that the query sees is at
+  least 2^4 (2^3.9 with the exponent's own error): 15 codes times 2^-28.9 max(w u) a token;
+* sums over tokens, waves and chunks are fp32: (n + 80) 2^-24 of sum w u (code + zero), which is at most 30 sum w u, and as much of
+  |out| through the weights' sum;
+* the result's own half step (fp16: at least 2^-25).
+No term holds a value or scale of a token that weighs nothing.
+"""
+import numpy as np
+import pytest
+
+from oracle import serve_oracle as S
+from test_gpu_kv4 import TYPES, Batch, f32, host, randn, say
+
+torch = pytest.importorskip("torch")
+import bit_quantized_gemm_amd as bq  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# Rows of Q and longest context that the launch is planned for: up to 16 rows a kv head take the kernel of 16 rows, the other
+# bounds the kernel of 128, whole and divided (pinned in test_kv4_plan.py).
+MODES = {"decode": (0, 300), "divided": (0, 4096), "prompt": (20000, 300), "parts": (4400, 16384)}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no ROCm GPU visible")
+    bq.load_library()
+
+
+def batch(mode, lens, count, Hq, H, D, page=16, **k):
+    total, longest = MODES[mode]
+    b = Batch(lens, count, Hq, H, D, page, spare_rows=max(0, total - sum(count)), stretch=longest // page - -(-max(lens) // page), **k)
+    most = max(total, max(count))
+    b.run_it = lambda: b.run(max_len=longest, max_q=most)[:b.total]
+    return b
+
+
+def put(b, i, tokens, key, value):
+    """Replaces tokens of sequence i."""
+    t = torch.as_tensor(tokens, device="cuda")
+    bq.atom_kv4_append(key, value, b.table[i].long()[t // b.page] * b.page + t % b.page, b.cache)
+
+
+def check(b, out, what=""):
+    """Every row against the oracle.  Where scores are so large that their error says nothing about a weight, the row has to be
+    the value of its largest score, if that is further ahead than the error; returns (rows so checked, rows left out)."""
+    D, Hq = b.q.shape[2], b.q.shape[1]
+    cache, q, got, first = host(b.cache), f32(b.q[:b.total]).astype(np.float64), f32(out).astype(np.float64), 0
+    H = cache[0].shape[1]
+    scale, eps = D ** -0.5, torch.finfo(out.dtype).eps / 2
+    low = 2.0**-25 if out.dtype == torch.float16 else 0.0
+    ahead = unsure = 0
+    for i, (n, c) in enumerate(zip(b.lens, b.count)):
+        t = np.arange(n)
+        slots = b.table[i].cpu().numpy().astype(np.int64)[t // b.page] * b.page + t % b.page
+        key, value = S.kv4_read(cache, b.page, slots, 0), S.kv4_read(cache, b.page, slots, 1)
+        par = [x[slots // b.page, :, slots % b.page, 1].astype(np.float64) for x in (cache[1], cache[3])]      # [n, H]
+        for r in range(c):
+            seen = n - c + r + 1
+            for j in range(Hq):
+                o = got[first + r, j]
+                where = f"{what} sequence {i}, query {r}, head {j}"
+                if seen <= 0:
+                    assert not o.any(), where
+                    continue
+                h = j // (Hq // H)
+                v, s, u = value[:seen, h], par[0][:seen, h], par[1][:seen, h]
+                x = scale * (key[:seen, h] @ q[first + r, j])
+                eta = (D + 8) * 2.0**-24 * scale * np.abs(q[first + r, j]).sum() * 15 * s + 100 * 2.0**-22
+                top = x.argmax()
+                if eta[x + eta > x[top] - eta[top] - 100].max() > 0.05:
+                    rest = np.delete(x + eta, top)
+                    if seen > 1 and x[top] - eta[top] - 40 < rest.max():
+                        unsure += 1
+                        continue
+                    ahead += 1
+                    want = v[top]
+                    tol = (2.0**-11 + 2.0**-20 + eps) * np.abs(want) + low
+                else:
+                    w = np.exp(x - x[top])
+                    w /= w.sum()
+                    want = w @ v
+                    wu = w * u
+                    tol = ((w * (2.0**-11 + eta)) @ np.abs(v) + (w @ eta) * np.abs(want) + seen * 15 * 2.0**-28.9 * wu.max()
+                           + (seen + 80) * 2.0**-24 * (30 * wu.sum() + np.abs(want)) + eps * np.abs(want) + low)
+                err = np.abs(o - want)
+                assert np.all(err <= tol), f"{where}: worst {np.max(err / np.maximum(tol, 1e-300)):.3g} of the bound, error {err.max():.3g}"
+        first += c
+    return ahead, unsure
+
+
+COUNTS = {"decode": ([250, 90], [7, 2]), "divided": ([3000, 90], [7, 1]), "prompt": ([250, 90], [70, 40]),
+          "parts": ([7000, 90], [20, 3])}
+
+
+# ------------------------------------------------------------------ values
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("ratio", [1e3, 1e6])
+def test_a_large_value_of_no_weight(ratio, mode, D, dtype):
+    """A token in sight whose value is `ratio` times the others' but whose score is some forty below theirs: nobody's bits."""
+    say(f"[kv4 large value] ratio={ratio} {mode} D={D} {dtype}")
+    lens, count = COUNTS[mode]
+    gain = 1.0 if ratio < 1e4 else 1e-2
+    b = batch(mode, lens, count, 4, 2, D, dtype=TYPES[dtype], seed=21, v_gain=gain)
+    b.q[:, :, 0] = 8.0
+    for at in (5, lens[0] // 2):                             # in the first tile, and behind tiles without it
+        key = torch.zeros(1, 2, D, dtype=torch.float16, device="cuda")
+        key[..., 0] = -5.0 * D ** 0.5
+        put(b, 0, [at], key, randn(1, 2, D, seed=at, gain=gain * ratio))
+        out = b.run_it()
+        check(b, out, f"token {at}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+def test_value_scales_over_the_whole_range(mode, D):
+    """Scales from fp16's smallest normal numbers to its largest, in any order, one value in ten all zero."""
+    say(f"[kv4 scales] {mode} D={D}")
+    lens, count = COUNTS[mode]
+    b = batch(mode, lens, count, 4, 2, D, seed=22)
+    g = torch.Generator().manual_seed(5)
+    for i, n in enumerate(lens):
+        v = (torch.rand(n, 2, D, generator=g) * 2 - 1) * torch.exp2(torch.rand(n, 2, 1, generator=g) * 25 - 10)
+        v *= torch.rand(n, 2, 1, generator=g) > 0.1
+        put(b, i, range(n), randn(n, 2, D, seed=i + 30, gain=3.0), v.half().cuda())
+    check(b, b.run_it())
+    zero = torch.zeros(lens[0], 2, D, dtype=torch.float16, device="cuda")
+    put(b, 0, range(lens[0]), randn(lens[0], 2, D, seed=3), zero)
+    out = b.run_it()
+    assert not out[:count[0]].any()
+    check(b, out)
+
+
+# ------------------------------------------------------------------ scores that rise late
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+def test_scores_that_rise_along_the_sequence(mode, D):
+    """Scores that climb by several powers of two from tile to tile, and fall again, for some of the rows of a tile; value
+    scales that climb with them, or against them."""
+    say(f"[kv4 rising] {mode} D={D}")
+    lens, count = COUNTS[mode]
+    for up in (1, -1):
+        b = batch(mode, lens, count, 4, 2, D, seed=23)
+        b.q[:, :, 0] = 0.0
+        b.q[::3, :, 0] = 6.0                                 # every third row sees the climb
+        for i, n in enumerate(lens):
+            t = torch.arange(n)
+            key, value = randn(n, 2, D, seed=40 + i).cpu(), randn(n, 2, D, seed=50 + i).cpu().float()
+            key[:, :, 0] = ((100 - (t - n // 2).abs()) * D ** 0.5 / 12).half()[:, None]       # half a unit of score a token
+            value *= torch.exp2(up * ((t - n / 2) / 20).clamp(-11, 11))[:, None, None]
+            put(b, i, range(n), key.cuda(), value.half().cuda())
+        check(b, b.run_it(), f"up={up}")

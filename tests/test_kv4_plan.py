@@ -73,3 +73,15 @@ def test_calls_below_the_documented_limit_are_accepted(total_q, q_heads, heads, 
     if not os.path.exists(bq.lib_path()):
         pytest.skip("libatom.so not built (python -m bit_quantized_gemm_amd.build)")
     assert bq.atom_kv4_attention_workspace_bytes(total_q, q_heads, heads, dim, batch, max_q, max_len) >= 0
+
+
+def test_ranges_reach_every_kernel(plans):
+    """The bounds of test_gpu_kv4_range.py: the kernel of 16 rows whole and divided, the kernel of 128 likewise."""
+    pytest.importorskip("torch")
+    import test_gpu_kv4_range as R
+    want = {"decode": (EIGHT, False), "divided": (EIGHT, True), "prompt": (PROMPT, False), "parts": (PROMPT, True)}
+    for mode, (total, longest) in R.MODES.items():
+        most = max(total, max(R.COUNTS[mode][1]))
+        calls = [(4, 2, dim, 2, most, longest // 16 * 16) for dim in (64, 128, 256)]
+        for kind, _, chunks, _ in plans(calls):
+            assert (kind, chunks > 1) == want[mode], mode
