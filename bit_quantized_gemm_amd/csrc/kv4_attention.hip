@@ -87,6 +87,17 @@ __device__ __forceinline__ h8v query_operand(const float (&x)[8], float f) {
              (_Float16)(x[2] * f), (_Float16)(x[6] * f), (_Float16)(x[3] * g), (_Float16)(x[7] * g)};
 }
 
+// The exponent that brings a row whose largest element has these bits to [2^13, 2^14): 2^-114 for bf16's largest, at most 2^100.
+__device__ __forceinline__ int query_exponent(float top) {
+  return min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23));
+}
+// c1 of queries scaled by 2^e.  Positive, and at most 2^100: scores / c1 are whole multiples of 2^-72 (codes and queries 2^-24
+// each, a scale 2^-24 at least), so beyond that the largest score alone has weight either way, and no product of it with a
+// scale and a sum overflows.
+__device__ __forceinline__ float score_factor(float scale, int e) {
+  return __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(scale * kLog2e, 24 - e), 1e-37f), 0x1p100f);
+}
+
 // A query row spread over the lanes that share column l: its operands, and the constants of its scores.
 template <class T, int WORDS>
 __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v (&op)[WORDS], float& sum, float& c1) {
@@ -99,8 +110,7 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = __builtin_fmaxf(top, __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1)));
   top = join_max<true>(top);
-  const int ex = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // floor(log2 top); -127 for 0, 128 for inf
-  const int e = max(-100, min(100, ex == 128 ? 0 : 13 - ex));
+  const int e = top == __builtin_inff() ? 0 : query_exponent(top);
   const float f = __builtin_ldexpf(1.0f, e);
   float s = 0.0f;
 #pragma unroll
@@ -113,8 +123,7 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
     for (int i = 0; i < 8; ++i) s += x[i] * f;
   }
   sum = join_sum<true>(s) * 0x1p-24f;
-  // positive and finite, so that it keeps the scores' order and -inf stays -inf
-  c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(scale * kLog2e, 24 - e), 1e-37f), 3e38f);
+  c1 = score_factor(scale, e);
 }
 
 __device__ __forceinline__ float low_half(uint32_t w) { return elem<Fp16>(w, 0); }
@@ -123,9 +132,12 @@ __device__ __forceinline__ float high_half(uint32_t w) { return elem<Fp16>(w, 1)
 constexpr float kTarget = 4.0f, kLimit = 15.0f;   // log2 of a row's largest weight: after ref is raised, and at most
 
 // How far ref rises for a row whose largest weight is 2^top: at the row's first tokens wherever that is, later only upwards.
+// Beyond 2^22, where the scores' own steps come near the target, to that weight's score itself, so that no weight is left above
+// its value scale.
 __device__ __forceinline__ float rise(float top, bool first) {
-  if (first) return top == kNegInf ? 0.0f : top - kTarget;
-  return __builtin_fmaxf(top - kTarget, 0.0f);
+  const float to = __builtin_fabsf(top) < 0x1p22f ? top - kTarget : top;
+  if (first) return top == kNegInf ? 0.0f : to;
+  return __builtin_fmaxf(to, 0.0f);
 }
 
 // 47 + log2 of the scale in the high half of a parameter word, to 0.09 below: fp16's exponent and mantissa bits, read as a
@@ -497,7 +509,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < NW; ++v) top = __builtin_fmaxf(top, lmax[v]);
-    const int e = max(-100, min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23)));   // 13 - floor(log2 top)
+    const int e = query_exponent(top);
     const float f = __builtin_ldexpf(1.0f, e);
 #pragma unroll
     for (int w = 0; w < S; ++w) {
@@ -506,7 +518,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
       q[w] = query_operand(x, f);
     }
-    c1 = __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(a.scale * kLog2e, 24 - e), 1e-37f), 3e38f);
+    c1 = score_factor(a.scale, e);
   }
 
   auto half2 = [](uint32_t w) { return __builtin_bit_cast(h2v, w); };

@@ -160,3 +160,19 @@ def test_scores_that_rise_along_the_sequence(mode, D):
             value *= torch.exp2(up * ((t - n / 2) / 20).clamp(-11, 11))[:, None, None]
             put(b, i, range(n), key.cuda(), value.half().cuda())
         check(b, b.run_it(), f"up={up}")
+
+
+# ------------------------------------------------------------------ queries
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("power", [26, 60, 99, 118])
+def test_huge_queries(power, mode, D):
+    """bf16 queries up to the type's largest: finite results, the value of the largest score."""
+    say(f"[kv4 huge queries] 2^{power} {mode} D={D}")
+    lens, count = COUNTS[mode]
+    b = batch(mode, lens, count, 4, 2, D, dtype=torch.bfloat16, seed=24)
+    b.q.mul_(2.0**power)
+    out = b.run_it()
+    assert out.isfinite().all()
+    ahead, unsure = check(b, out)
+    assert ahead > 9 * unsure
