@@ -14,8 +14,8 @@
 // weights feed the second product from the registers the first one left them in.  The values'
 // four-token blocks in the cache are the operand order of that product.
 //
-// Ranges.  The queries are scaled by a power of two so that the largest element lies in [2^13, 2^14): of a row in decode_kernel,
-// of a workgroup's rows in prompt_kernel.  fp16 then holds fp16 and bf16 queries exactly down to 2^-24 of that element.  The
+// Ranges.  The queries are scaled by a power of two so that the largest element lies in [2^13, 2^14): of a row, or in prompt_kernel
+// of a workgroup's rows while the rows' own largest elements are within 2^12 of each other.  fp16 then holds fp16 and bf16 queries exactly down to 2^-24 of that element.  The
 // weights w are rounded to fp16: 2^-11 of each, as fp16's own rounding of the output.  Sums of w (v - b) and of p carry the same power
 // of two, so it leaves the quotient; it is the row's own and follows the largest *weight* (score and value scale together): a token
 // of large values and no weight costs the others nothing.  The zero points multiply the rounded weights too, so a
@@ -391,7 +391,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 // lanes 0-31, 4-7, 12-15 for the others); chunk c at position c ^ (d & 7) ^ (d / 8 & 7).  Sixteen lanes of a 16-byte read hit all banks.
 //
 // The scale of the queries (a power of two) is one for the workgroup, so that a token's factor c1 * s can be made when it
-// is staged.  Rows far smaller than the largest one keep an absolute error of 2^-31 of the largest row's scores.
+// is staged.  A row 2^12 below the largest one then still has its queries to 2^-25 of its own largest element.  Where rows lie further
+// apart (or one is far out), each has a scale of its own, c1 stands for one half way between the ends, and each row's sums are
+// multiplied by its own factor over that one before they are scaled: 16 products a half tile in a branch of the whole workgroup.
 //
 // Reference: a half tile's largest score and the largest value scale of the wave so far bound its weights; only where that bound
 // passes 2^15 are the weights themselves looked at.
@@ -411,7 +413,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   constexpr int kLds = kTile * D * 2;        // bytes of a tile's keys, or values, in LDS
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][kLds];
   __shared__ __attribute__((aligned(16))) float lf[2][2][kTile];           // c1 * key scale, value scale
-  __shared__ float lmax[NW];
+  __shared__ int lexp[2][NW];                // a wave's least and largest exponent of a row
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, h = lane >> 5;
@@ -489,7 +491,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
 
   // ---- queries: lane half h holds words 2 s + h of its row
   h8v q[S];
-  float c1;
+  float c1, rel;                             // rel: this row's factor over c1
+  bool apart;
   {
     const uint16_t* src = a.q + (int64_t)(seq.first + qi) * a.q_stride + (int64_t)(head * a.group + row - qi * a.group) * D + 8 * h;
     u32x4 raw[S];
@@ -499,17 +502,29 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
 #pragma unroll
     for (int w = 0; w < S; ++w)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {          // the largest finite element
+      for (int i = 0; i < 8; ++i) {          // the row's largest finite element
         const float x = __builtin_fabsf(elem<T>(raw[w][i / 2], i & 1));
         top = x < __builtin_inff() ? __builtin_fmaxf(top, x) : top;
       }
+    top = join_max<false>(top);
+    const int own = query_exponent(top);
+    int least = own, most = top > 0.0f ? own : -114;     // a row of zeros keeps no distance
 #pragma unroll
-    for (int d = 32; d; d >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) lmax[wave] = top;
+    for (int d = 16; d; d >>= 1) {
+      least = min(least, __shfl_xor(least, d));
+      most = max(most, __shfl_xor(most, d));
+    }
+    if (lane == 0) lexp[0][wave] = least, lexp[1][wave] = most;
     __syncthreads();
 #pragma unroll
-    for (int v = 0; v < NW; ++v) top = __builtin_fmaxf(top, lmax[v]);
-    const int e = query_exponent(top);
+    for (int v = 0; v < NW; ++v) {
+      least = min(least, lexp[0][v]);
+      most = max(most, lexp[1][v]);
+    }
+    least = __builtin_amdgcn_readfirstlane(least);
+    most = __builtin_amdgcn_readfirstlane(most);
+    apart = most - least > 12;
+    const int e = apart ? own : least;
     const float f = __builtin_ldexpf(1.0f, e);
 #pragma unroll
     for (int w = 0; w < S; ++w) {
@@ -518,7 +533,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
       q[w] = query_operand(x, f);
     }
-    c1 = score_factor(a.scale, e);
+    c1 = score_factor(a.scale, apart ? (least + most) >> 1 : least);
+    rel = score_factor(a.scale, e) / c1;
   }
 
   auto half2 = [](uint32_t w) { return __builtin_bit_cast(h2v, w); };
@@ -634,6 +650,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       for (int j = 0; j < 16; ++j) y[j] -= delta;
     }
   };
+  auto weigh = [&]() __attribute__((always_inline)) {      // s of rows with scales of their own
+    if (apart) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[j] *= rel;
+    }
+  };
   auto scale4 = [&](const f32x4& f, int g) __attribute__((always_inline)) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) y[4 * g + r] = __builtin_fmaf(s[4 * g + r], f[r], -ref);
@@ -672,6 +694,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   };
   // The product of the weights with the values of (wbuf, wt) while s is scaled (factors of (buf, t)) and `fill(n)` runs.
   auto product_and_scale = [&](int wbuf, int wt, int buf, int t, auto fill) __attribute__((always_inline)) {
+    weigh();
     f32x4 f[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) f[g] = *reinterpret_cast<const f32x4*>(&lf[0][0][0] + 2 * buf * kTile + 32 * t + 8 * g + 4 * h);
@@ -702,6 +725,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
     s = f32x16{};
 #pragma unroll
     for (int w = 0; w < S; ++w) s = __builtin_amdgcn_mfma_f32_32x32x16_f16(key(0, 0, w), q[w], s, 0, 0, 0);
+    weigh();
 #pragma unroll
     for (int g = 0; g < 4; ++g) scale4(*reinterpret_cast<const f32x4*>(&lf[0][0][8 * g + 4 * h]), g);
     read_ahead(0, 1, 0, 0);

@@ -176,3 +176,46 @@ def test_huge_queries(power, mode, D):
     assert out.isfinite().all()
     ahead, unsure = check(b, out)
     assert ahead > 9 * unsure
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("power", [0, 26, 118])
+def test_elements_next_to_the_types_end(power, mode, D):
+    """Two rows whose largest element is next to bf16's largest number, among others of 2^power."""
+    say(f"[kv4 end of the type] 2^{power} {mode} D={D}")
+    lens, count = COUNTS[mode]
+    b = batch(mode, lens, count, 4, 2, D, dtype=torch.bfloat16, seed=26)
+    b.q.mul_(2.0**power)
+    b.q[0, 0, :2], b.q[1, 1, 0] = 3.3e38, -3.3e38
+    out = b.run_it()
+    assert out.isfinite().all()
+    check(b, out)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype,other", [("bf16", 2.0**100), ("bf16", 2.0**40), ("bf16", 2.0**27), ("fp16", 2.0**13), ("bf16", 2.0**-100)])
+def test_rows_of_different_size(dtype, other, mode, D):
+    """A row of far larger, or smaller, queries among ordinary ones: each keeps its own bits."""
+    say(f"[kv4 rows] {other:.3g} {mode} D={D} {dtype}")
+    lens, count = COUNTS[mode]
+    b = batch(mode, lens, count, 4, 2, D, dtype=TYPES[dtype], seed=25)
+    plain = b.run_it()
+    check(b, plain)
+    b.q[1, 2] *= other
+    b.q[3, 0] *= other
+    b.q[5, 1] = 0
+    if dtype == "fp16":
+        b.q[4] *= 2.0**-10                                   # to fp16's smallest
+    out = b.run_it()
+    assert out.isfinite().all()
+    check(b, out)
+    b.q[1, 2, 3] = float("inf")
+    b.q[3, 0, 3] = float("nan")
+    bad = b.run_it()
+    for r, h in ((1, 2), (3, 0)):
+        assert not bad[r, h].isfinite().any()
+        bad[r, h] = 0
+        out[r, h] = 0
+    torch.testing.assert_close(bad, out, rtol=2 * torch.finfo(out.dtype).eps, atol=2.0**-11 * 6)
