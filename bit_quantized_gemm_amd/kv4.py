@@ -139,8 +139,8 @@ def atom_kv4_append(K, V, slots, cache, stream=None):
     if stream is None and type(K) is T and type(V) is T and type(slots) is T and K.is_cuda and K.dim() == 3:
         d, t = fast_device(K), K.dtype
         c = _fast_cache(cache, d) if d >= 0 and (t is torch.float16 or t is torch.bfloat16) else None
-        if (c is not None and K.shape == V.shape == (slots.shape[0], c.heads, c.dim) and slots.dtype is torch.int64
-                and slots.dim() == 1 and slots.is_contiguous() and slots.get_device() == d):
+        if (c is not None and slots.dim() == 1 and K.shape == V.shape == (slots.shape[0], c.heads, c.dim)
+                and slots.dtype is torch.int64 and slots.is_contiguous() and slots.get_device() == d):
             ks, vs = _fast_rows(K, c.heads, c.dim, t, d), _fast_rows(V, c.heads, c.dim, t, d)
             if ks and vs:
                 status = _bq.load_library().atom_kv4_append(K.data_ptr(), ks, V.data_ptr(), vs, slots.data_ptr(), K.shape[0],
