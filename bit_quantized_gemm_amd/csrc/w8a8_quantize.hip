@@ -15,16 +15,17 @@
 // Measured: 2048 x 11008 12.8 us and 4096 x 8192 17.0 us (5.3 and 5.9 TB/s with the input in the caches, a copy of memory reaches 5.1),
 // 16 x 4096 2.9 us, of which the launch is most, 333 x 1155 (unaligned rows) 3.3 us.
 #include "w8a8_row.h"
+#include "w8a8_rows.h"
 
 namespace atom {
 namespace {
 
 template <class T, int THREADS, int CH, bool VEC>
-__global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+__global__ __launch_bounds__(w8a8::block_threads(THREADS)) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                                                int rows, int K, int Kp,
                                                                                int8_t* __restrict__ Xq,
                                                                                float* __restrict__ sx) {
-  constexpr int kBlock = THREADS <= 64 ? 256 : THREADS;
+  constexpr int kBlock = w8a8::block_threads(THREADS);
   constexpr int kRows = kBlock / THREADS;               // rows of one workgroup
   const int t = threadIdx.x % THREADS;
   const int row = blockIdx.x * kRows + threadIdx.x / THREADS;
@@ -59,25 +60,31 @@ __global__ __launch_bounds__(THREADS <= 64 ? 256 : THREADS) void quantize_kernel
 
 template <class T, int THREADS, int CH>
 void launch(const uint16_t* X, int64_t ldx, bool vec, int rows, int K, int Kp, int8_t* Xq, float* sx, hipStream_t st) {
-  constexpr int kBlock = THREADS <= 64 ? 256 : THREADS;
-  const dim3 grid((rows + kBlock / THREADS - 1) / (kBlock / THREADS));
-  if (vec)
-    hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, true>), grid, dim3(kBlock), 0, st, X, ldx, rows, K, Kp, Xq, sx);
-  else
-    hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, false>), grid, dim3(kBlock), 0, st, X, ldx, rows, K, Kp, Xq, sx);
+  constexpr int kBlock = w8a8::block_threads(THREADS), kRows = kBlock / THREADS;
+  for (int64_t r = 0; r < rows; r += w8a8::launch_rows(THREADS)) {
+    const int n = (int)(rows - r < w8a8::launch_rows(THREADS) ? rows - r : w8a8::launch_rows(THREADS));
+    const dim3 grid((n + kRows - 1) / kRows);
+    if (vec)
+      hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, true>), grid, dim3(kBlock), 0, st, X + r * ldx, ldx, n, K, Kp,
+                         Xq + r * Kp, sx + r);
+    else
+      hipLaunchKernelGGL((quantize_kernel<T, THREADS, CH, false>), grid, dim3(kBlock), 0, st, X + r * ldx, ldx, n, K, Kp,
+                         Xq + r * Kp, sx + r);
+  }
 }
 
 template <class T>
 void dispatch(const uint16_t* X, int64_t ldx, int rows, int K, int8_t* Xq, float* sx, hipStream_t st) {
   const int Kp = (K + 127) / 128 * 128;
   const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
-  if (Kp <= 512) launch<T, 64, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 2048 && rows <= 384) launch<T, 256, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 2048) launch<T, 64, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 4096) launch<T, 256, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 8192 && rows <= 1024) launch<T, 512, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 8192) launch<T, 256, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
-  else if (Kp <= 16384) launch<T, 512, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  const w8a8::RowShape s = w8a8::row_shape(rows, Kp);
+  if (s.threads == 64 && s.chunks == 1) launch<T, 64, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 64) launch<T, 64, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 256 && s.chunks == 1) launch<T, 256, 1>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 256 && s.chunks == 2) launch<T, 256, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 256) launch<T, 256, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 512 && s.chunks == 2) launch<T, 512, 2>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
+  else if (s.threads == 512) launch<T, 512, 4>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
   else launch<T, 1024, 8>(X, ldx, vec, rows, K, Kp, Xq, sx, st);
 }
 

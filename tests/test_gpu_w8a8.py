@@ -250,3 +250,26 @@ def test_output_past_32_bits():
     Y = bq.linear_w8a8(x, Wq, sw)
     for rows in (slice(0, 40), slice(70000, 70040), slice(M - 40, M)):
         torch.testing.assert_close(Y[rows], bq.linear_w8a8(x[rows], Wq, sw), rtol=0, atol=0)
+
+
+def test_quantize_more_rows_than_a_launch():
+    """2^24 rows of 2049 elements (69 GB): 256 threads each are 2^32, one more than a launch takes.  Zero rows but a few."""
+    rows, K = 1 << 24, 2049
+    rb = bq.atom_w8a8_row_bytes(K)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < rows * (2 * K + rb) + (8 << 30):
+        pytest.skip("needs 114 GB of device memory")
+    say(f"[w8a8 quantize] {rows}x{K}")
+    try:
+        x = torch.zeros(rows, K, dtype=torch.float16, device="cuda")
+        Xq, sx = torch.full((rows, rb), 0x55, dtype=torch.int8, device="cuda"), torch.full((rows,), -1.0, device="cuda")
+        at = torch.tensor([0, 5, (1 << 23) + 1, rows - 257, rows - 2, rows - 1], device="cuda")
+        x[at] = make(len(at), K, torch.float16, 7)
+        bq.atom_quantize_w8a8(x, Xq=Xq, sx=sx)
+        check_codes(Xq[at], sx[at], x[at])
+        Xq[at], sx[at] = 0, 0
+        assert not sx.any()
+        assert all(not part.view(torch.int64).any() for part in Xq.split(1 << 20))
+    finally:
+        x = Xq = sx = None
+        torch.cuda.empty_cache()
