@@ -34,7 +34,8 @@ class _CCache(ctypes.Structure):
 
 
 class KV4Cache(NamedTuple):
-    """The cache's arrays; any four tensors of these shapes will do wherever a cache is taken."""
+    """The cache's arrays; any four tensors of these shapes will do wherever a cache is taken, as long as the zero points are
+    whole numbers from 0 to 15 and the scales finite and not negative where sequences lie, as the append writes them."""
     k: object        # uint8 [pages, heads, page, dim / 2]
     k_par: object    # fp16  [pages, heads, page, 2]: (zero point, scale)
     v: object        # uint8 [pages, heads, page / 4, dim / 4, 8]

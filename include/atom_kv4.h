@@ -12,6 +12,8 @@
  *   lo = min(min x, 0), hi = max(max x, 0), scale = fp16_rne(fl32(min((hi - lo) / 15, 65504))),
  *   zero = clamp(rint_even(fl32(-lo / scale)), 0, 15), q = clamp(rint_even(fl32(x / scale)) + zero, 0, 15),
  *   and all three are 0 where scale = 0.
+ * Whoever fills the arrays without the append below keeps to that: zero points are whole numbers from 0 to 15, scales finite
+ * and not negative.  Attention's results for other parameters are unspecified (no fault).
  *
  * Shapes: D is 64, 128 or 256; page is a power of two from 16 to 256; 1 <= H <= 1024;
  * 1 <= pages < 2^31 / page; fp16 or bf16 keys, values and queries (`dtype`, as in atom_w8a8.h).  The
