@@ -217,8 +217,8 @@ def atom_kv4_attention(Q, cache, table, lens, q_start, scale=None, max_len=None,
     which lie in the pages table[b] (int32 [batch, width]).  Query i of n sees tokens 0 .. lens[b] - n + i;
     one that sees none gets zeros, rows outside every sequence are left as they were.  `scale` defaults
     to dim ** -0.5.  `max_len` and `max_q` bound the lengths and query counts on the host (by default what
-    the table and Q can hold; tighter bounds choose a better launch): tokens and queries behind them are
-    left out.  `workspace`: 1-D uint8 of ``atom_kv4_attention_workspace_bytes`` bytes (calls that may overlap
+    the table and Q can hold; tighter bounds choose a better launch): queries behind max_q are left out, a length
+    above max_len is taken as max_len.  `workspace`: 1-D uint8 of ``atom_kv4_attention_workspace_bytes`` bytes (calls that may overlap
     need one each), else a torch buffer is taken for the call when one is needed."""
     torch = _bq._torch()
     T = torch.Tensor

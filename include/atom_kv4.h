@@ -69,9 +69,11 @@ int atom_kv4_read(const atom_kv4_cache *cache, const int64_t *slots, int32_t tok
  * A token's weight times its value scale is rounded to fp16 with the largest such product that the query sees as its unit
  * (2^-11 of it; products below 2^-18 of the largest: to steps of 2^-28 of the largest; a scale below 2^-14 counts as 2^-14
  * in that unit).
- * max_q and max_len bound the sequences' queries and tokens on the host: queries and tokens behind them
- * are left out.  batch * H * ceil(max_q * Hq / H / 128) must stay below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage
- * out, no fault).  What lies in the pages behind a sequence's end is never used in a result.
+ * max_q and max_len bound the sequences' queries and tokens on the host.  Queries behind max_q are left out (their rows
+ * stay as they were; the others see what they would).  A length above max_len, or above what `width` pages hold, is taken as
+ * that: the sequence ends there, and its last query sees its last token.  batch * H * ceil(max_q * Hq / H / 128) must stay
+ * below 2^24, the largest launch.  Entries of lens, q_start and table outside their ranges are clamped into them (garbage out,
+ * no fault).  What lies in the pages behind a sequence's end is never used in a result.
  * workspace: atom_kv4_attention_workspace_bytes(...) bytes (0 when none is needed) let long sequences be
  * divided among workgroups; with less (or NULL) they run undivided.  Contents on entry do not matter;
  * calls that may overlap in time need one each.
