@@ -85,3 +85,32 @@ def test_ranges_reach_every_kernel(plans):
         calls = [(4, 2, dim, 2, most, longest // 16 * 16) for dim in (64, 128, 256)]
         for kind, _, chunks, _ in plans(calls):
             assert (kind, chunks > 1) == want[mode], mode
+
+
+def test_prompt_tests_reach_the_prompt_kernel(plans):
+    """test_gpu_kv4_prompt.py, and the two tests of large batches in test_gpu_kv4.py, whole and divided."""
+    pytest.importorskip("torch")
+    import test_gpu_kv4 as T
+    import test_gpu_kv4_prompt as P
+    shapes = [(c[0], c[2], c[3], c[4], c[5]) for c in T.CASES]
+    shapes += [(lens, Hq, H, D, page) for D in (64, 128, 256) for page in (16, 32, 64) for lens, Hq, H in (
+        ([200, 70], 4, 2), ([190, 130], 4, 2), ([73, 50], 2, 1), ([170, 50], 2, 1), ([280, 90], 2, 1))]
+    calls = []
+    for lens, Hq, H, D, page in shapes:
+        total, longest = P.bounds(lens, Hq, H)
+        calls.append((Hq, H, D, len(lens), total, min(longest, max(longest // page, -(-max(lens) // page)) * page)))
+    calls += [(4 * G, 4, D, 4, 2200, 1100) for D, G in ((128, 2), (64, 3), (64, 1), (128, 4), (256, 2), (256, 3))]
+    for c, (kind, _, chunks, _) in zip(calls, plans(calls)):
+        assert (kind, chunks) == (PROMPT, 1), c
+    calls = [(8, 2, D, 4, 256, 16384) for D in (64, 128, 256)]
+    for c, (kind, _, chunks, _) in zip(calls, plans(calls)):
+        assert kind == PROMPT and chunks > 1, c
+
+
+def test_small_batches_take_the_kernel_of_16_rows(plans):
+    """The shapes of test_gpu_kv4.py with their own bounds: eight waves up to 16 rows, four beyond."""
+    pytest.importorskip("torch")
+    import test_gpu_kv4 as T
+    calls = [(Hq, H, D, len(lens), max(count), max(lens)) for lens, count, Hq, H, D, _ in T.CASES]
+    for c, (kind, _, chunks, _) in zip(calls, plans(calls)):
+        assert kind == (EIGHT if c[4] * c[0] // c[1] <= 16 else FOUR) and chunks == 1, c
