@@ -77,9 +77,9 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// BM x BN output tile of four waves (2 x 2), RING stage buffers.  splits > 1: piece p of tile t is workgroup
-// p * tiles + t and writes its int32 tile to part[(p * tiles + t) * BM * BN].
-template <class T, int BM, int BN, int RING, int WAVES>
+// BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
+// workgroup p * tiles + t and writes its int32 tile to part[(p * tiles + t) * BM * BN].
+template <class T, int BM, int BN, int RING, int WAVES, bool kDivided>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
     const int8_t* __restrict__ Xq, const float* __restrict__ sx, const int8_t* __restrict__ Wq,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int Kp, uint16_t* __restrict__ Y,
@@ -98,7 +98,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
   const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
   int lin = (int)blockIdx.x, piece = 0;
-  if (splits > 1) {
+  if (kDivided && splits > 1) {
     piece = lin / tiles;
     lin -= piece * tiles;
   } else {
@@ -110,7 +110,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   const int2 tc = tile_coords(lin, tiles_m, tiles_n);
   const int m0 = tc.x * BM, n0 = tc.y * BN;
   const int stages = Kp / kStage;
-  const int sa = (int)((int64_t)stages * piece / splits), sb = (int)((int64_t)stages * (piece + 1) / splits);
+  const int sa = kDivided ? (int)((int64_t)stages * piece / splits) : 0;
+  const int sb = kDivided ? (int)((int64_t)stages * (piece + 1) / splits) : stages;
 
   // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 8 rows an
   // instruction: lane i lands at row i / 8, position i % 8, and loads the chunk that lies there.
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   }
   __builtin_amdgcn_s_waitcnt(0);                          // no copy into LDS outlives the workgroup
 
-  if (splits > 1) {
+  if (kDivided && splits > 1) {
     int32_t* tile = part + ((size_t)piece * tiles + lin) * (BM * BN);
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -423,6 +424,7 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
 
 // The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
 constexpr int kKinds = 5;
+constexpr int kDividedKind = 1;  // the tile size whose plans may divide K
 constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
 
 // Waves of a workgroup that divide units of 128 bytes of K.  A wave loads whole batches, so the count (8 to 16, four
@@ -459,18 +461,18 @@ void launch(const int8_t* Xq, const float* sx, const int8_t* Wq, const float* sw
   }
   const dim3 grid(p.tiles * p.splits);
 #define ATOM_TILE(KIND, BM, BN, RING, W)                                                                             \
-  if (p.kind == KIND) {                                                                                              \
-    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W>), grid, dim3(256), 0, st, Xq, sx, Wq, sw, bias, M, N,   \
-                       Kp, Y, p.tiles, p.splits, part);                                                              \
-    if (p.splits > 1)                                                                                                \
-      hipLaunchKernelGGL((finish_kernel<T, BM, BN>), dim3(p.tiles * (BM * BN / 1024)), dim3(256), 0, st, part, sx,   \
-                         sw, bias, M, N, Y, p.tiles, p.splits);                                                      \
-  }
+  if (p.kind == KIND)                                                                                                \
+    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind>), grid, dim3(256), 0, st, Xq, sx, \
+                       Wq, sw, bias, M, N, Kp, Y, p.tiles, p.splits, part);
   ATOM_TILE(1, 64, 128, 3, 2)
   ATOM_TILE(2, 128, 128, 2, 2)
   ATOM_TILE(3, 256, 128, 3, 1)
   ATOM_TILE(4, 256, 256, 2, 1)
 #undef ATOM_TILE
+  if (p.splits > 1)
+    hipLaunchKernelGGL((finish_kernel<T, kBM[kDividedKind], kBN[kDividedKind]>),
+                       dim3(p.tiles * (kBM[kDividedKind] * kBN[kDividedKind] / 1024)), dim3(256), 0, st, part, sx, sw, bias, M,
+                       N, Y, p.tiles, p.splits);
 }
 
 template <class T, int MR>
@@ -519,7 +521,7 @@ W8Plan w8_plan(int M, int N, int K) {
   for (int kind = 1; kind < kKinds; ++kind) {
     const Cost& c = cost[kind];
     const int t = tiles(kind);
-    for (int splits = 1; splits <= (kind == 1 ? 4 : 1); ++splits) {
+    for (int splits = 1; splits <= (kind == kDividedKind ? 4 : 1); ++splits) {
       if (splits > 1 && (stages < 8 * splits || t * splits > cus)) break;
       const int64_t per = ((int64_t)t * splits + cus - 1) / cus;    // workgroups of the busiest unit
       const int64_t full = per / c.slots, rest = per % c.slots;
@@ -527,7 +529,7 @@ W8Plan w8_plan(int M, int N, int K) {
       const double multiply = 1e-3 * k * (full * c.full + (rest ? c.one : 0.0));
       const double read = (double)N * K / (splits > 1 ? 6e6 : 4.2e6);
       double time = (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
-      if (splits > 1) time = 1.04 * (time + 2.5 + (double)t * splits * kBM[1] * kBN[1] * 8 / 3.3e6);
+      if (splits > 1) time = 1.04 * (time + 2.5 + (double)t * splits * kBM[kind] * kBN[kind] * 8 / 3.3e6);
       if (time < least) {
         least = time;
         best = W8Plan{kind, t, splits};

@@ -409,7 +409,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   constexpr int S = D / 16;                  // K = 16 slices of the key product
   constexpr int NT = D / 32;                 // 32-channel tiles of the output
   constexpr int kTile = 64;
-  constexpr int W = D / (8 * NW);            // words of key codes, and of value codes, that a thread stages
+  constexpr int W = D / (8 * NW);            // words of key codes, and of value codes, that a thread stages: 2, 4 or 8
   constexpr int kLds = kTile * D * 2;        // bytes of a tile's keys, or values, in LDS
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][kLds];
   __shared__ __attribute__((aligned(16))) float lf[2][2][kTile];           // c1 * key scale, value scale
@@ -455,11 +455,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[g + j] = v[j];
       }
-    } else if constexpr (W == 2) {
+    } else {
       const u32x2 v = *reinterpret_cast<const u32x2*>(src);
       x[0] = v[0], x[1] = v[1];
-    } else {
-      x[0] = *src;
     }
   };
   // Pages of 64 tokens or more hold a whole tile: one page for all threads, its id read a tile ahead.
@@ -574,18 +572,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
     auto place = [&](int d) __attribute__((always_inline)) {
       return svals + buf * (2 * kLds) + d * 128 + ((vchunk ^ (d & 7) ^ ((d >> 3) & 7)) << 4);
     };
-    if constexpr (W == 1) {                              // one pair of tokens of a whole quad
-      const int pair = vp & 1, d = 4 * (vp >> 1);
-      const u32x2 lo = unpack(gv[0], pair ? vz[1] : vz[0]), hi = unpack(gv[0] >> 8, pair ? vz[1] : vz[0]);
-      const uint32_t x[4] = {lo[0], lo[1], hi[0], hi[1]};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(place(d + i) + 4 * pair) = x[i];
-    } else {
-      const int g = n >> 1, i = 2 * (n & 1), d = 4 * (W / 2 * vp + g) + i;
-      const u32x2 x = unpack(gv[2 * g] >> (4 * i), vz[0]), z = unpack(gv[2 * g + 1] >> (4 * i), vz[1]);
-      *reinterpret_cast<u32x2*>(place(d)) = u32x2{x[0], z[0]};
-      *reinterpret_cast<u32x2*>(place(d + 1)) = u32x2{x[1], z[1]};
-    }
+    const int g = n >> 1, i = 2 * (n & 1), d = 4 * (W / 2 * vp + g) + i;
+    const u32x2 x = unpack(gv[2 * g] >> (4 * i), vz[0]), z = unpack(gv[2 * g + 1] >> (4 * i), vz[1]);
+    *reinterpret_cast<u32x2*>(place(d)) = u32x2{x[0], z[0]};
+    *reinterpret_cast<u32x2*>(place(d + 1)) = u32x2{x[1], z[1]};
   };
 
   f32x16 o[NT];
@@ -739,7 +729,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       if (n == 0) stage_parameters(B ^ 1, base + kTile);
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if (n == w * NT / W + (W <= NT ? 1 : 0)) stage_keys(B ^ 1, w);
+        if (n == w + 1) stage_keys(B ^ 1, w);
     });
     __syncthreads();                         // the next tile's keys are there
     read_ahead(B ^ 1, 0, B, 1);
@@ -748,7 +738,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
     product_and_scale(B, 1, B ^ 1, 0, [&](int n) __attribute__((always_inline)) {
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        if (n == w * NT / W + (W <= NT ? 1 : 0)) stage_values(B ^ 1, w);
+        if (n == w + 1) stage_values(B ^ 1, w);
     });
     read_ahead(B ^ 1, 1, B ^ 1, 0);
     if (base + kTile < end) settle(B ^ 1, 0, base + kTile);
