@@ -141,6 +141,19 @@ def test_value_scales_over_the_whole_range(mode, D):
     check(b, out)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+def test_one_token(mode, D):
+    """A token alone in sight: its weight is not rounded, so the result is its value, rounded once (fp16: half a step, 2^-11 of it, and
+    2^-18 for the fp32 steps and the reference's own rounding)."""
+    say(f"[kv4 one token] {mode} D={D}")
+    b = batch(mode, [1] * 40, [1] * 40, 4, 2, D, seed=27, q_gain=2.0)
+    out = b.run_it().double()
+    slots = b.table[:, 0].long() * b.page
+    want = torch.from_numpy(S.kv4_read(host(b.cache), b.page, slots.tolist(), 1)).cuda().repeat_interleave(2, 1)
+    assert torch.all((out - want).abs() <= (2.0**-11 + 2.0**-18) * want.abs() + 2.0**-25)
+
+
 # ------------------------------------------------------------------ scores that rise late
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("mode", MODES)
