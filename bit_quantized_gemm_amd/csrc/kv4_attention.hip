@@ -136,8 +136,8 @@ __device__ __forceinline__ float high_half(uint32_t w) { return elem<Fp16>(w, 1)
 constexpr float kTarget = 4.0f, kLimit = 15.0f;   // log2 of a row's largest weight: after ref is raised (at least), and at most
 
 // How far ref rises for a row whose largest weight is 2^top (its scale's exponent alone): at the row's first tokens wherever that
-// is, later only upwards.  Beyond 2^22, where the scores' own steps come near the target, to that weight's score itself, so that no weight is left above
-// its value scale.
+// is, later only upwards.  Beyond 2^22, where the scores' own steps come near the target, to that weight's score itself, so that
+// no weight is left above its value scale.
 __device__ __forceinline__ float rise(float top, bool first) {
   const float to = __builtin_fabsf(top) < 0x1p22f ? top - kTarget : top;
   if (first) return top == kNegInf ? 0.0f : to;
@@ -161,9 +161,9 @@ __device__ __forceinline__ float exponent(uint32_t word) {
 // through LDS.  A unit's keys are replaced by the next unit's as soon as the score product has read them, its values
 // after theirs: one unit of registers, so that four waves fit a SIMD (D = 128) and hide each other's latency.
 //
-// Measured (GPU time): 16 sequences of up to 2048 tokens, 32 kv heads of 128 channels: 24 us, 4.3 TB/s of codes and parameters (a plain
-// read of as many bytes takes 17); 4 of up to 32768, 8 kv heads, 64 query heads: 28 us and 4 to join, 4.5 TB/s.  There the
-// vector ALUs' 300 instructions a unit take half the time and do not hide wholly behind the loads.  Two units of
+// Measured (GPU time): 16 sequences of up to 2048 tokens, 32 kv heads of 128 channels: 21.7 us, 4.7 TB/s of codes and parameters (a
+// plain read of as many bytes takes 17); 4 of up to 32768, 8 kv heads, 64 query heads: 26.5 us and 4 to join, 4.8 TB/s.  There the
+// vector ALUs' 200 or so instructions a unit take half the time and do not hide wholly behind the loads.  Two units of
 // registers (half the waves) and 16 chunks instead of 8 gained nothing.
 template <class T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 2 : 4))) void decode_kernel(Args a) {
@@ -409,9 +409,9 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 // passes 2^15 are the weights themselves looked at.
 //
 // Measured: 2 prompts of up to 4096 tokens, 32 heads of 128 channels: 279-299 us (0.81-0.87 PFLOP/s of the visible half; the matrix cores' rate
-// alone would take 177).  The vector ALUs are busy 64% of a tile's 2.4 us, the matrix cores 42%, and the clock gives way to
-// the power drawn: the same call takes 334 us on normal data of full length, 281 on zeros.  Of a workgroup's time 8 us are its
-// start, first tile and end.  64 rows a wave with one wave a SIMD (half the LDS reads and unpacking a row) took 499 us, eight waves a
+// alone would take 177).  The vector ALUs are busy 60% of the time (counters), the matrix cores 40%, and the clock gives way to
+// the power drawn: the same call takes 334 us on normal data of full length, 281 on zeros.  Rows with scales of their own 296 us
+// where one scale takes 282.  Of a workgroup's time 8 us are its start, first tile and end.  64 rows a wave with one wave a SIMD (half the LDS reads and unpacking a row) took 499 us, eight waves a
 // workgroup no less than four, and a schedule pinned to the products 4% more.
 template <class T, int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void prompt_kernel(Args a) {

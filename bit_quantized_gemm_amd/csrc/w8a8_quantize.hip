@@ -6,13 +6,15 @@
 // (in a wave by DPP-free shuffles, across waves through LDS) and the codes are made from the registers.
 // The threads of a row follow its length: a wave for short rows (four rows a workgroup, no
 // barrier), 256 or 512 threads up to 16384 elements, 1024 beyond; few rows, which leave units idle, take more (us, with the
-// other count: 333 x 1155 3.3 and 3.7, but 4000 x 2048 8.6 and 5.4; 600 x 8192 4.3 and 4.7, but 2048 x 8192 10.2 and 9.6).
+// other count: 256 x 2048 2.7 and 3.3, 1024 x 2048 3.8 and 3.5, 4096 x 2048 8.7 and 5.3; 512 x 8192 3.7 and 4.1, 1024 x 8192 5.3
+// and 5.3, 2048 x 8192 10.1 and 9.4).  The counts cross at 250 rows of 1024 elements and 700 of 2048, at 700 of 5120 and 1000 of
+// 8192; the borders, 384 and 1024, lie between and cost at most 10% next to them.
 // Rows whose elements no aligned 16-byte load fits (odd K or stride, shifted views) are read by unaligned ones, the last few
 // elements one by one.
 //
 // The codes are those of an IEEE divide, without its dozen instructions an element: see quotient().
 //
-// Measured: 2048 x 11008 12.8 us and 4096 x 8192 17.0 us (5.3 and 5.9 TB/s with the input in the caches, a copy of memory reaches 5.1),
+// Measured: 2048 x 11008 12.8 us and 4096 x 8192 16.7 us (5.3 and 5.9 TB/s with the input in the caches, a copy of memory reaches 5.1),
 // 16 x 4096 2.9 us, of which the launch is most, 333 x 1155 (unaligned rows) 3.3 us.
 #include "w8a8_row.h"
 #include "w8a8_rows.h"
