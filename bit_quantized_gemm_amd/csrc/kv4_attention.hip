@@ -4,10 +4,14 @@
 //   score = c * s * (sum_d q_d k_d - a * sum_d q_d),      c = scale * log2(e)
 //   out_d = sum_t w_t (v_td - b_t) / sum_t p_t,           p = 2^(score - max), w = p * u,
 // so the matrix cores multiply the codes themselves and the scales meet one score or one weight a
-// token.  A code goes into the fp16 operand as the bits it has: the half-precision number with
-// mantissa q is q * 2^-24 exactly (a subnormal, which the gfx950 matrix cores keep), and with the
-// nibble one place up 16 q * 2^-24.  Unpacking eight codes is one shift and four ands; the factor 16 of every
-// other nibble is taken out of the query (keys) or the result (values), exactly.
+// token.  A code goes into the fp16 operand as the bits it has: a half-precision number whose low eleven bits are b is b 2^-24
+// exactly (below 2^-14 a subnormal, which the gfx950 matrix cores keep).  Shifted by three, a half-word's nibbles stand there as 8 q and
+// 128 q: unpacking eight codes is two shifts and four ands, and the factor 16 of every other nibble is taken out of the query (keys) or the
+// result (values), exactly.  The place matters: the matrix cores line up the products of a sum by their operands' exponent
+// fields, which for every subnormal is that of 2^-14, and drop what lies some 2^-24 below the largest.  With q and 16 q (one shift less)
+// sums of 32 products were off by up to 2^-11.5 codes of the largest factor, always downwards; with 8 q it is 2^-14.5, with
+// prompt_kernel's normal numbers 2^-18.  (Error against 64 bits of 16 x 2048 tokens, fp16, queries 64 times as large: 2.09e-4 of the norm
+// with q, 1.87e-4 with 8 q or all 128 q, 1.86e-4 in 32 bits; all 128 q, four shifts, takes 3% more time.)
 //
 // Both products have the tokens (keys) or channels (values) as rows and the queries as columns: a
 // lane's scores belong to one query, and as the contraction over tokens may run in any order, the
@@ -77,16 +81,16 @@ __device__ __forceinline__ float join_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// Eight codes of a word -> fp16 operand, halves (n0, n4, 16 n1, 16 n5, n2, n6, 16 n3, 16 n7) * 2^-24.
+// Eight codes of a word -> fp16 operand, halves (n0, n4, 16 n1, 16 n5, n2, n6, 16 n3, 16 n7) * 2^-21.
+constexpr int kCodeBits = 21;
 __device__ __forceinline__ h8v unpack_keys(uint32_t w) {
-  const uint32_t v = w >> 8;
-  const u32x4 o = {w & 0x000F000Fu, w & 0x00F000F0u, v & 0x000F000Fu, v & 0x00F000F0u};
+  const uint32_t x = w << 3, y = w >> 5;
+  const u32x4 o = {x & 0x00780078u, x & 0x07800780u, y & 0x00780078u, y & 0x07800780u};
   return __builtin_bit_cast(h8v, o);
 }
 
-// The query operand of the same word: the row's eight channels in that order, the odd ones / 16.
-__device__ __forceinline__ h8v query_operand(const float (&x)[8], float f) {
-  const float g = f * 0.0625f;
+// The query operand of the same word: the row's eight channels in that order, the odd ones times g, the others times f.
+__device__ __forceinline__ h8v query_operand(const float (&x)[8], float f, float g) {
   return h8v{(_Float16)(x[0] * f), (_Float16)(x[4] * f), (_Float16)(x[1] * g), (_Float16)(x[5] * g),
              (_Float16)(x[2] * f), (_Float16)(x[6] * f), (_Float16)(x[3] * g), (_Float16)(x[7] * g)};
 }
@@ -95,11 +99,11 @@ __device__ __forceinline__ h8v query_operand(const float (&x)[8], float f) {
 __device__ __forceinline__ int query_exponent(float top) {
   return min(100, 140 - (int)(__builtin_bit_cast(uint32_t, top) >> 23));
 }
-// c1 of queries scaled by 2^e.  Positive, and at most 2^100: scores / c1 are whole multiples of 2^-72 (codes and queries 2^-24
-// each, a scale 2^-24 at least), so beyond that the largest score alone has weight either way, and no product of it with a
-// scale and a sum overflows.
-__device__ __forceinline__ float score_factor(float scale, int e) {
-  return __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(scale * kLog2e, 24 - e), 1e-37f), 0x1p100f);
+// c1 of queries scaled by 2^e and codes scaled by 2^-bits.  Positive, and at most 2^90: scores / c1 are whole multiples of 2^-69
+// (codes 2^-21, queries 2^-24, a scale 2^-24 at least), so beyond that the largest score alone has weight either way, and
+// no product of it with a scale and a sum overflows.
+__device__ __forceinline__ float score_factor(float scale, int e, int bits) {
+  return __builtin_fminf(__builtin_fmaxf(__builtin_ldexpf(scale * kLog2e, bits - e), 1e-37f), 0x1p90f);
 }
 
 // A query row spread over the lanes that share column l: its operands, and the constants of its scores.
@@ -122,12 +126,12 @@ __device__ __forceinline__ void load_query(const uint16_t* src, float scale, h8v
     float x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
-    op[w] = query_operand(x, f);
+    op[w] = query_operand(x, f, f * 0.0625f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) s += x[i] * f;
   }
-  sum = join_sum<true>(s) * 0x1p-24f;
-  c1 = score_factor(scale, e);
+  sum = join_sum<true>(s) * 0x1p-21f;
+  c1 = score_factor(scale, e, kCodeBits);
 }
 
 __device__ __forceinline__ float low_half(uint32_t w) { return elem<Fp16>(w, 0); }
@@ -322,8 +326,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 #pragma unroll
     for (int u = 0; u < W / 2; ++u) {
       const u32x4 lo = {v[0][2 * u], v[0][2 * u + 1], v[1][2 * u], v[1][2 * u + 1]};
-      const u32x4 hi = lo >> 8;
-      const u32x4 op[4] = {lo & 0x000F000Fu, lo & 0x00F000F0u, hi & 0x000F000Fu, hi & 0x00F000F0u};
+      const u32x4 x = lo << 3, z = lo >> 5;
+      const u32x4 op[4] = {x & 0x00780078u, x & 0x07800780u, z & 0x00780078u, z & 0x07800780u};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         o[4 * u + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8v, op[i]), p, o[4 * u + i], 0, 0, 0);
@@ -349,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) o[i][r] = f * __builtin_fmaf(o[i][r], i & 1 ? 0x1p20f : 0x1p24f, -zs[0]);
+    for (int r = 0; r < 4; ++r) o[i][r] = f * __builtin_fmaf(o[i][r], i & 1 ? 0x1p17f : 0x1p21f, -zs[0]);
   for (int half = WAVES / 2; half; half >>= 1) {
     if (half < WAVES / 2) __syncthreads();   // the step before has read its buffers
     if (wave >= half && wave < 2 * half) {
@@ -392,7 +396,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 // ------------------------------------------------------------------ many query rows: bound by the vector ALUs and matrix cores
 // One workgroup of four waves: 128 query rows of one sequence and kv head, 32 a wave, against a chunk of the tokens in
 // tiles of 64.  A tile is unpacked once for all waves on its way into LDS, as fp16 operands with the zero point already
-// taken off (q - zero is a small integer: its multiple of 2^-24 is exact), two buffers, the next tile's loads in registers
+// taken off (q 2^-24 or 16 q 2^-24, as the bits lie, times a power of two less the zero point, in one instruction for two codes: a small
+// integer's multiple of 2^-9, a normal number), two buffers, the next tile's loads in registers
 // meanwhile.  That leaves a wave per score one fma (scale and running maximum), half a maximum, the exponential, the
 // sum, the value scale and half a conversion.
 //
@@ -419,6 +424,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   constexpr int S = D / 16;                  // K = 16 slices of the key product
   constexpr int NT = D / 32;                 // 32-channel tiles of the output
   constexpr int kTile = 64;
+  constexpr int kStageBits = 9;              // codes in LDS are multiples of 2^-9
   constexpr int W = D / (8 * NW);            // words of key codes, and of value codes, that a thread stages: 2, 4 or 8
   constexpr int kLds = kTile * D * 2;        // bytes of a tile's keys, or values, in LDS
   __shared__ __attribute__((aligned(16))) uint8_t lds[2][2][kLds];
@@ -539,18 +545,19 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = elem<T>(raw[w][i / 2], i & 1);
-      q[w] = query_operand(x, f);
+      q[w] = query_operand(x, f, f);
     }
-    c1 = score_factor(a.scale, apart ? (least + most) >> 1 : least);
-    rel = score_factor(a.scale, e) / c1;
+    c1 = score_factor(a.scale, apart ? (least + most) >> 1 : least, kStageBits);
+    rel = score_factor(a.scale, e, kStageBits) / c1;
   }
 
   auto half2 = [](uint32_t w) { return __builtin_bit_cast(h2v, w); };
-  const h2v kTiny = {(_Float16)0x1p-24f, (_Float16)0x1p-24f}, k16 = {(_Float16)16.0f, (_Float16)16.0f};
-  // the pairs of halves (q - zero) 2^-24 in the two low nibbles of each half-word, the second 16 times as large
+  const h2v kUnit = {(_Float16)0x1p-9f, (_Float16)0x1p-9f}, kLow = {(_Float16)0x1p15f, (_Float16)0x1p15f},
+            kHigh = {(_Float16)0x1p11f, (_Float16)0x1p11f};
+  // the pairs of halves (q - zero) 2^-9 of the codes in the two low nibbles of each half-word
   auto unpack = [&](uint32_t w, h2v z) __attribute__((always_inline)) {
-    return u32x2{__builtin_bit_cast(uint32_t, half2(w & 0x000F000Fu) - z),
-                 __builtin_bit_cast(uint32_t, half2(w & 0x00F000F0u) - z * k16)};
+    return u32x2{__builtin_bit_cast(uint32_t, __builtin_elementwise_fma(half2(w & 0x000F000Fu), kLow, -z)),
+                 __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(half2(w & 0x00F000F0u), kHigh, -z))};
   };
   // Staging in steps that fill the gaps between matrix products: parameters and keys first, then the values.
   uint8_t* const skeys = &lds[0][0][0] + kt * (D * 2);
@@ -566,10 +573,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
       for (int r = 0; r < 4; ++r)
         if (base + 4 * vb + r >= seq.tokens) vpar[r] = 0;
     }
-    kz = half2(__builtin_amdgcn_perm(par, par, 0x01000100u)) * kTiny;
+    kz = half2(__builtin_amdgcn_perm(par, par, 0x01000100u)) * kUnit;
     lf[buf][0][kt] = c1 * high_half(par);                // the same from every thread of the token
-    vz[0] = half2(__builtin_amdgcn_perm(vpar[1], vpar[0], 0x05040100u)) * kTiny;
-    vz[1] = half2(__builtin_amdgcn_perm(vpar[3], vpar[2], 0x05040100u)) * kTiny;
+    vz[0] = half2(__builtin_amdgcn_perm(vpar[1], vpar[0], 0x05040100u)) * kUnit;
+    vz[1] = half2(__builtin_amdgcn_perm(vpar[3], vpar[2], 0x05040100u)) * kUnit;
     *reinterpret_cast<f32x4*>(&lf[buf][1][4 * vb]) =
         f32x4{high_half(vpar[0]), high_half(vpar[1]), high_half(vpar[2]), high_half(vpar[3])};
   };
@@ -760,7 +767,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
     if (base + kTile < end) step(Half<1>{}, base + kTile);
   }
 
-  // Register 4 g + r of o[i]: channel 32 i + 8 g + 4 h + r, its codes 16 times too large for odd r.
+  // Register 4 g + r of o[i]: channel 32 i + 8 g + 4 h + r.
   l = join_sum<false>(l);
   const int64_t id = (int64_t)(seq.first + qi) * a.q_heads + head * a.group + row - qi * a.group;
   const int64_t all_rows = (int64_t)a.total_q * a.q_heads;
@@ -778,7 +785,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
 #pragma unroll
       for (int g = 0; g < 4; ++g)
         *reinterpret_cast<f32x4*>(dst + 32 * i + 8 * g + 4 * h) =
-            f32x4{o[i][4 * g] * 0x1p24f, o[i][4 * g + 1] * 0x1p20f, o[i][4 * g + 2] * 0x1p24f, o[i][4 * g + 3] * 0x1p20f};
+            f32x4{o[i][4 * g] * 0x1p9f, o[i][4 * g + 1] * 0x1p9f, o[i][4 * g + 2] * 0x1p9f, o[i][4 * g + 3] * 0x1p9f};
     return;
   }
   // Out through LDS, a wave's rows in a part of its own, so that rows leave whole (eight-byte pieces of 32 rows a
@@ -790,9 +797,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      const float e = inv * 0x1p24f, f = inv * 0x1p20f;
+      const float e = inv * 0x1p9f;
       *reinterpret_cast<u32x2*>(own + l32 * (D * 2) + (((4 * i + g) ^ (l32 & 7)) << 4) + 8 * h) =
-          u32x2{pack2<T>(o[i][4 * g] * e, o[i][4 * g + 1] * f), pack2<T>(o[i][4 * g + 2] * e, o[i][4 * g + 3] * f)};
+          u32x2{pack2<T>(o[i][4 * g] * e, o[i][4 * g + 1] * e), pack2<T>(o[i][4 * g + 2] * e, o[i][4 * g + 3] * e)};
     }
   constexpr int kLanes = D / 8;              // lanes of a row
   for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {

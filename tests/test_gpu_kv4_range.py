@@ -82,8 +82,8 @@ def check(b, out, what=""):
                         unsure += 1
                         continue
                     ahead += 1
-                    want = v[top]
-                    tol = (2.0**-11 + 2.0**-20 + eps) * np.abs(want) + low
+                    want = v[top]                            # the others weigh at most e^-40 each
+                    tol = (2.0**-11 + 2.0**-20 + eps) * np.abs(want) + low + seen * np.exp(-40) * np.abs(v).max()
                 else:
                     w = np.exp(x - x[top])
                     w /= w.sum()
@@ -152,6 +152,67 @@ def test_one_token(mode, D):
     slots = b.table[:, 0].long() * b.page
     want = torch.from_numpy(S.kv4_read(host(b.cache), b.page, slots.tolist(), 1)).cuda().repeat_interleave(2, 1)
     assert torch.all((out - want).abs() <= (2.0**-11 + 2.0**-18) * want.abs() + 2.0**-25)
+
+
+# ------------------------------------------------------------------ sums
+# The matrix cores line up the products of a sum by their operands' exponent fields and drop what lies 2^-24 below the largest.
+# An fp16 code q * 2^-21 below 2^-14 has the field of 2^-14, which stands for 128 codes: a product loses at most 2^-24 * 128 = 2^-17
+# codes of the largest factor beside it.  (Codes of 2^-24 would lose 2^-14.)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+def test_small_weights_beside_a_heavy_one(mode, D):
+    """One token holds nearly all the weight and is zero in most channels; what the others add there, some 2^-13 of a code each, is
+    kept."""
+    say(f"[kv4 heavy token] {mode} D={D}")
+    n = 31
+    b = batch(mode, [n, 9], [1, 1], 4, 2, D, seed=28)
+    b.q[0] = 0
+    b.q[0, :, 0] = 11.75
+    key, value = torch.zeros(n, 2, D, dtype=torch.float16, device="cuda"), torch.zeros(n, 2, D, dtype=torch.float16, device="cuda")
+    key[4, :, 0] = D ** 0.5                                  # scores of 11.75 and 0
+    value[:] = 8.0                                           # a scale of 1, zero point 7, codes 0, 7 and 15
+    value[4] = 0
+    value[:, :, 1], value[4, :, 3] = -7.0, 8.0
+    put(b, 0, range(n), key, value)
+    out = b.run_it()[0].double()
+    w = 1 / (n - 1 + np.exp(11.75))
+    want = (n - 1) * w * 8
+    eta = 2 * ((D + 8) * 2.0**-24 * 11.75 * 15 / 15 + 100 * 2.0**-22)
+    tol = want * (2.0**-11 + eta + 2.0**-11) + n * 2.0**-17
+    for c in (0, 2, slice(4, None)):
+        assert torch.all((out[:, c] - want).abs() <= tol), (c, want, tol, out[:, c].min().item(), out[:, c].max().item())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("mode", MODES)
+def test_small_products_beside_a_large_query_element(mode, D):
+    """A query's largest element meets keys that are zero there; the scores are what the small ones make.  Two tokens, so the
+    result's place between their values is their scores' difference: off by at most 2 (D 2^-17 + 20 * 15 * 2^-24) scale max|q| s."""
+    say(f"[kv4 large element] {mode} D={D}")
+    many = 40
+    b = batch(mode, [2] * many, [1] * many, 4, 2, D, seed=29)
+    g = torch.Generator().manual_seed(9)
+    q = torch.randn(many, 4, D, generator=g)
+    big = 4096.0
+    q[:, :, 0] = big
+    b.q[:many] = q.half().cuda()
+    for i in range(many):
+        key, value = torch.randn(2, 2, D, generator=g), torch.zeros(2, 2, D)
+        key[:, :, 0] = 0
+        key[:, :, 1], key[:, :, 2] = -3.5, 4.0               # a scale of 1/2, zero point 7
+        value[1] = 1.0
+        put(b, i, range(2), key.clamp(-3.5, 4.0).half().cuda(), value.half().cuda())
+    out = b.run_it().double().cpu().numpy()
+    scale, qd, cache = D ** -0.5, f32(b.q[:many]).astype(np.float64), host(b.cache)
+    for i in range(many):
+        slots = b.table[i, 0].item() * b.page + np.arange(2)
+        k = S.kv4_read(cache, b.page, slots, 0)
+        for j in range(4):
+            x = scale * (k[:, j // 2] @ qd[i, j])
+            p = 1 / (1 + np.exp(x[0] - x[1]))
+            off = 2 * (D * 2.0**-17 + 20 * 15 * 2.0**-24) * scale * big * 0.5
+            tol = p * (1 - p) * np.expm1(off) + p * 2.0**-10 + 2.0**-24
+            assert np.all(np.abs(out[i, j] - p) <= tol), (i, j, p, out[i, j, 0], tol)
 
 
 # ------------------------------------------------------------------ scores that rise late
