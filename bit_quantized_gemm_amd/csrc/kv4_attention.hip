@@ -23,7 +23,7 @@
 // weights w are rounded to fp16: 2^-11 of each, as fp16's own rounding of the output.  Sums of w (v - b) and of p carry the same power
 // of two, so it leaves the quotient; it is the row's own and follows the largest *weight* (score and value scale together): a token
 // of large values and no weight costs the others nothing.  The zero points multiply the rounded weights too, so a
-// rounding error acts on (v - b), not on v and b apart.  Scores, maxima and all sums are fp32.
+// rounding error acts on (v - b), not on v and b apart.  Scores, maxima and all sums are held in fp32.
 //
 // Reference: weights are 2^(score - ref) u with ref such that the largest of a row lies in [2^4, 2^15.1] from the row's first tile
 // on: fp16 then holds whatever is above 2^-18 of it to 11 bits, and the rest to steps of 2^-28.  When some weight of
@@ -31,8 +31,8 @@
 // largest is 2^4 to 2^5 and the sums are rescaled, in a wave-uniform branch that random data take in the first tiles only.  ref counts
 // tokens that the row sees, no others, and goes by their scales' exponents: the score that sets it is then a whole power of two and
 // its weight, a fp16 number times that, not rounded at all.  (Error against 64 bits of a decode step over 2048 tokens of 128 channels,
-// fp16: 2.8e-4 of the norm, 3.0e-4 with a reference that is not whole, 2.1e-4 with weights in 32 bits, the output's rounding alone;
-// raised at every new largest weight it is 2.7e-4 and takes 22.2 us instead of 21.6.)
+// fp16: 2.7e-4 of the norm, 3.0e-4 with a reference that is not whole, 2.1e-4 with weights in 32 bits, the output's rounding alone;
+// raised at every new largest weight it is no less and takes 3% more time.)
 #include "atom_internal.h"
 #include "kv4_layout.h"
 #include "serve_internal.h"
@@ -165,9 +165,9 @@ __device__ __forceinline__ float exponent(uint32_t word) {
 // through LDS.  A unit's keys are replaced by the next unit's as soon as the score product has read them, its values
 // after theirs: one unit of registers, so that four waves fit a SIMD (D = 128) and hide each other's latency.
 //
-// Measured (GPU time): 16 sequences of up to 2048 tokens, 32 kv heads of 128 channels: 21.7 us, 4.7 TB/s of codes and parameters (a
+// Measured (GPU time): 16 sequences of up to 2048 tokens, 32 kv heads of 128 channels: 21.8 us, 4.7 TB/s of codes and parameters (a
 // plain read of as many bytes takes 17); 4 of up to 32768, 8 kv heads, 64 query heads: 26.5 us and 4 to join, 4.8 TB/s.  There the
-// vector ALUs' 200 or so instructions a unit take half the time and do not hide wholly behind the loads.  Two units of
+// vector ALUs' some 200 instructions a unit take half the time and do not hide wholly behind the loads.  Two units of
 // registers (half the waves) and 16 chunks instead of 8 gained nothing.
 template <class T, int D, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D == 256 ? 2 : 4))) void decode_kernel(Args a) {
@@ -415,8 +415,8 @@ __global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(D ==
 //
 // Measured: 2 prompts of up to 4096 tokens, 32 heads of 128 channels: 279-299 us (0.81-0.87 PFLOP/s of the visible half; the matrix cores' rate
 // alone would take 177).  The vector ALUs are busy 60% of the time (counters), the matrix cores 40%, and the clock gives way to
-// the power drawn: the same call takes 334 us on normal data of full length, 281 on zeros.  Rows with scales of their own 296 us
-// where one scale takes 282.  Of a workgroup's time 8 us are its start, first tile and end.  64 rows a wave with one wave a SIMD (half the LDS reads and unpacking a row) took 499 us, eight waves a
+// the power drawn: the same call takes 334 us on normal data of full length, 281 on zeros.  Rows with scales of their own 294 us
+// where one scale takes 284.  Of a workgroup's time 8 us are its start, first tile and end.  64 rows a wave with one wave a SIMD (half the LDS reads and unpacking a row) took 499 us, eight waves a
 // workgroup no less than four, and a schedule pinned to the products 4% more.
 template <class T, int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 256 ? 1 : 2))) void prompt_kernel(Args a) {

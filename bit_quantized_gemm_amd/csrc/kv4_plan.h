@@ -23,9 +23,9 @@ struct Plan {
 //
 // Up to 16 rows a sequence and kv head: decode_kernel in eight waves (kEight), four (kFour) from 512 workgroups on; divided until
 // there are 256 workgroups, but not up to 1024 tokens, which eight waves walk through in four steps.  Measured (one call,
-// 256 compute units): 16 sequences of 2048 tokens, 32 kv heads: 26.3 us whole in four waves, 26.0 in eight, 29.7 divided in two; 4
-// of 32768, 8 kv heads: 30.0 in 8 chunks, 30.7 in 16, 37.5 in 24; 16 of 4096 with 16 heads of 64 channels: 17.5 whole in eight
-// waves, 22.8 in four; one of 700: 6.8 whole, 8.9 divided.
+// 256 compute units): 16 sequences of 2048 tokens, 32 kv heads: 26.0 us whole in four waves, 26.1 in eight, 29.6 divided in two; 4
+// of 32768, 8 kv heads: 30.1 in 8 chunks, 30.7 in 16, 36.3 in 24; 16 of 4096 with 16 heads of 64 channels: 17.8 whole in eight
+// waves, 22.8 in four; one of 700: 6.9 whole, 9.1 divided.
 //
 // More rows: the least of these estimates (us; a round fills the compute units with four workgroups of decode_kernel or two of
 // prompt_kernel, half as many of 256 channels):
@@ -33,9 +33,9 @@ struct Plan {
 //   prompt_kernel: 3.5, 5 a round, and for each 64 tokens 2.45 or 1.55 with the units full or half full; 1.55 for the longest
 //   joining: 4, 0.4 for 1000 rows, and the partial sums' way through memory.
 // Measured (us), decode_kernel and prompt_kernel whole, and the best of both divided: 16 sequences of 2048 tokens, 8 kv heads of 128
-// channels, 80 rows each: 35, 57, 38; 256 rows: 74, 59, 68; one sequence of 8192, 512 rows: 47, 197, 42; prompts of 2 x 1600 tokens, 32
-// heads: 109, 77, 122; 4 x 1000, 4 kv heads of 256 channels, 400 rows: 23, 58, 36.  Over 37 shapes the choice is within 12% of the
-// best of all kinds and divisions, within 5% on 29.
+// channels, 80 rows each: 36, 56, 38; 256 rows: 72, 58, 68; one sequence of 8192, 512 rows: 50, 189, 42; prompts of 2 x 1600 tokens, 32
+// heads: 115, 76, 124; 4 x 1000, 4 kv heads of 256 channels, 400 rows: 24, 58, 36.  Over 37 shapes the choice is within 11% of the
+// best of all kinds and divisions, within 5% on 32.
 inline Plan plan(int q_heads, int heads, int dim, int batch, int max_q, int max_len, int cus) {
   const int64_t rows = (int64_t)max_q * (q_heads / heads);
   auto make = [&](int kind, int64_t chunks) {
