@@ -6,7 +6,7 @@
  *   sx = fl32(max|x| / 127),   qx = clamp(rint_even(fl32(x / sx)), -127, 127),  0 where sx = 0,
  *   likewise (sw, qw) for w;   Y[m,n] = round(acc * sx[m] * sw[n] + bias[n]),  acc = sum_k qx * qw.
  * acc is an exact 32-bit integer (127 * 127 * ATOM_MAX_K < 2^31); the scaling and the bias are
- * fp32 and Y is rounded once.
+ * fp32, acc * sx[m] first (which therefore has to be below 2^128), and Y is rounded once.
  *
  * The conventions of atom.h hold (device pointers owned by the caller, no allocation, no
  * synchronization, arguments checked on the host first, ATOM_E_* returned), except that
