@@ -19,8 +19,13 @@ The function names are the C entry points:
   where the shape allows (``atom_linear_workspace_bytes(M, N, K)``; the workspace starts zeroed)
 * W8A8 layer (``include/atom_w8a8.h``, in ``w8a8.py``): ``atom_quantize_w8a8(X)`` -> (Xq, sx),
   ``atom_gemm_w8a8(Xq, sx, Wq, sw, K)`` -> Y, ``linear_w8a8(X, Wq, sw, bias)`` -> Y
+* MXFP4 layer (``include/atom_mxfp4.h``, in ``mxfp4.py``): ``atom_quantize_mxfp4(X)`` -> (Xq, sx),
+  ``atom_gemm_mxfp4(Xq, sx, Wq, sw, K)`` -> Y, ``linear_mxfp4(X, Wq, sw, bias)`` -> Y
+* norm in front of those two (``include/atom_norm.h``, in ``norm.py``): ``atom_rmsnorm_w8a8(X, weight, eps, residual)``,
+  ``atom_rmsnorm_mxfp4(...)`` -> (Xq, sx, H)
 * 4-bit KV cache (``include/atom_kv4.h``, in ``kv4.py``): ``kv4_cache(...)``, ``atom_kv4_append``,
-  ``atom_kv4_read``, ``atom_kv4_attention``
+  ``atom_kv4_read``, ``atom_kv4_attention``; its pages (``include/atom_kv4_pages.h``, in ``kv4_pages.py``):
+  ``kv4_pool(...)``, ``atom_kv4_extend``, ``atom_kv4_release``
 * ``atom_row_bytes(K)``, ``atom_num_groups(K)``, ``atom_strerror(status)``
 """
 from __future__ import annotations
@@ -97,6 +102,9 @@ def load_library():
     }
     sig.update(w8a8.signatures())
     sig.update(kv4.signatures())
+    sig.update(mxfp4.signatures())
+    sig.update(norm.signatures())
+    sig.update(kv4_pages.signatures())
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -435,11 +443,16 @@ def atom_gemm_w4a8_ws(Xq, sx, Wq, sw, K, workspace, Y=None, stream=None):
     return Y
 
 
-# --------------------------------------------------------------------------- W8A8 layer, 4-bit KV cache
-from . import kv4, w8a8  # noqa: E402
+# --------------------------------------------------------------------------- W8A8 and MXFP4 layers, norm, 4-bit KV cache
+from . import kv4, kv4_pages, mxfp4, norm, w8a8  # noqa: E402
 from .kv4 import (KV4Cache, atom_kv4_append, atom_kv4_attention, atom_kv4_attention_workspace_bytes,  # noqa: E402
                   atom_kv4_read, kv4_cache)
-from .w8a8 import (atom_gemm_w8a8, atom_gemm_w8a8_workspace_bytes, atom_linear_w8a8_workspace_bytes,  # noqa: E402
-                   atom_quantize_w8a8, atom_w8a8_row_bytes, linear_w8a8)
+from .kv4_pages import KV4Pool, atom_kv4_extend, atom_kv4_release, kv4_pool  # noqa: E402
+from .mxfp4 import (atom_dequantize_mxfp4, atom_gemm_mxfp4, atom_gemm_mxfp4_workspace_bytes,  # noqa: E402
+                    atom_linear_mxfp4_workspace_bytes, atom_mxfp4_groups, atom_mxfp4_row_bytes, atom_quantize_mxfp4,
+                    linear_mxfp4)
+from .norm import atom_rmsnorm_mxfp4, atom_rmsnorm_w8a8  # noqa: E402
+from .w8a8 import (atom_dequantize_w8a8, atom_gemm_w8a8, atom_gemm_w8a8_workspace_bytes,  # noqa: E402
+                   atom_linear_w8a8_workspace_bytes, atom_quantize_w8a8, atom_w8a8_row_bytes, linear_w8a8)
 
-__all__ += w8a8.__all__ + kv4.__all__
+__all__ += w8a8.__all__ + kv4.__all__ + mxfp4.__all__ + norm.__all__ + kv4_pages.__all__

@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatom.so")
 
 SOURCES = ["atom_api.cpp", "select.hip", "quantize.hip", "gemm.hip", "gemm_small.hip", "gemm_w4a8.hip",
-           "serve_api.cpp", "w8a8_quantize.hip", "gemm_w8a8.hip", "kv4_cache.hip", "kv4_attention.hip"]
+           "serve_api.cpp", "w8a8_quantize.hip", "gemm_w8a8.hip", "kv4_cache.hip", "kv4_attention.hip",
+           "mxfp4_api.cpp", "mxfp4_quantize.hip", "gemm_mxfp4.hip", "rmsnorm.hip", "kv4_pages_api.cpp", "kv4_pages.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,528 @@
+// MXFP4 GEMM for gfx950: Y[m,n] = round(sum over blocks of 2^(ex + ew) * (32 products of 4-bit floats) + bias[n]) on
+// v_mfma_scale_f32_{32x32x64,16x16x128}_f8f6f4, which take the blocks' scale bytes as they are.
+//
+// Operand layout.  A stage is a group of 256 values: 128 bytes, a cache line, of each row, eight blocks of 16 bytes.  An
+// instruction takes one block of each row from each lane, and which block of K that is is free as long as both operands
+// agree: lane l of the 32x32x64 supplies row l & 31 and, in slice t of a stage, block 4 (l >> 5) + t, so the scale bytes
+// of its four slices are one word of the group's eight, chosen by the instruction's byte select.  The weights are the
+// first operand, so a 32x32 accumulator holds its tile transposed: lane l owns token l & 31, element r is column
+// (r >> 2) * 8 + (l >> 5) * 4 + (r & 3): four runs of four columns.
+#include "lds_ring.h"
+#include "atom_internal.h"
+#include "gemm_tile.h"
+#include "mxfp4_row.h"
+
+namespace atom {
+namespace {
+
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ i32x8 operand(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+constexpr int kFp4 = 4;          // the instructions' number of the E2M1 format
+
+// One slice: byte TB of both scale words.
+template <int TB>
+__device__ __forceinline__ f32x16 mma32(i32x4 w, i32x4 x, f32x16 c, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w), operand(x), c, kFp4, kFp4, TB, sw, TB, sx);
+}
+template <int TB>
+__device__ __forceinline__ f32x4 mma16(i32x4 w, i32x4 x, f32x4 c, int sw, int sx) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), c, kFp4, kFp4, TB, sw, TB, sx);
+}
+
+// The sum and the bias in fp32.  The empty asm keeps the compiler from folding the sum and Y's conversion into one
+// instruction with one rounding in some kernels and not in others.
+__device__ __forceinline__ float biased(float acc, float bias) {
+  float y = acc + bias;
+  asm("" : "+v"(y));
+  return y;
+}
+
+// BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
+// workgroup p * tiles + t and writes its fp32 tile to part[(p * tiles + t) * BM * BN].
+template <class T, int BM, int BN, int RING, int WAVES, bool kDivided>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
+    const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ Wq,
+    const uint8_t* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int stages, uint16_t* __restrict__ Y,
+    int tiles, int splits, float* __restrict__ part) {
+  constexpr int WM = BM / 2, WN = BN / 2, TM = WM / 32, TN = WN / 32;
+  constexpr int kDmaA = BM / 32, kDmaB = BN / 32;        // LDS-DMA instructions per wave and stage
+  constexpr int kPer = kDmaA + kDmaB;
+  constexpr int kA = BM * kStage, kB = BN * kStage;
+  // each stage buffer its own object: the compiler knows that a copy into one does not write another
+  __shared__ __attribute__((aligned(16))) uint8_t la0[kA], la1[kA], la2[kA];
+  __shared__ __attribute__((aligned(16))) uint8_t lb0[kB], lb1[kB], lb2[kB];   // (buffers past RING take no LDS)
+  auto LA = [&](int p) -> uint8_t* { return p == 0 ? la0 : p == 1 ? la1 : la2; };
+  auto LB = [&](int p) -> uint8_t* { return p == 0 ? lb0 : p == 1 ? lb1 : lb2; };
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, kh = lane >> 5;
+  const int tiles_m = (M + BM - 1) / BM, tiles_n = (N + BN - 1) / BN;
+  int lin = (int)blockIdx.x, piece = 0;
+  if (kDivided && splits > 1) {
+    piece = lin / tiles;
+    lin -= piece * tiles;
+  } else {
+    // workgroups go to the 8 XCDs in turn: give each a contiguous run of the tile order, so that
+    // the tiles of one L2 share their operands
+    const int per = tiles / 8, more = tiles % 8, x = lin % 8;
+    lin = x * per + min(x, more) + lin / 8;
+  }
+  const int2 tc = tile_coords(lin, tiles_m, tiles_n);
+  const int m0 = tc.x * BM, n0 = tc.y * BN;
+  const int sa = kDivided ? (int)((int64_t)stages * piece / splits) : 0;
+  const int sb = kDivided ? (int)((int64_t)stages * (piece + 1) / splits) : stages;
+
+  // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 8 rows an
+  // instruction: lane i lands at row i / 8, position i % 8, and loads the chunk that lies there.
+  // Rows past M / N repeat the last one (their results are never stored).
+  const int rows_a = min(BM, M - m0), rows_b = min(BN, N - n0), bytes = stages * kStage;
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(Xq + (size_t)m0 * bytes), (short)0, rows_a * bytes, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(Wq + (size_t)n0 * bytes), (short)0, rows_b * bytes, 0x00020000);
+  int va[kDmaA], vb[kDmaB];
+#pragma unroll
+  for (int h = 0; h < kDmaA; ++h) {
+    const int r = wave * (BM / 4) + 8 * h + lane / 8;
+    va[h] = min(r, rows_a - 1) * bytes + pos(r, lane & 7) * 16;
+  }
+#pragma unroll
+  for (int h = 0; h < kDmaB; ++h) {
+    const int r = wave * (BN / 4) + 8 * h + lane / 8;
+    vb[h] = min(r, rows_b - 1) * bytes + pos(r, lane & 7) * 16;
+  }
+  // Copies of stages behind the last repeat it (never read).
+  auto dma = [&](int p, int s) __attribute__((always_inline)) {
+    const int off = min(s, stages - 1) * kStage;
+#pragma unroll
+    for (int h = 0; h < kDmaA; ++h) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 8 * h) * kStage, va[h], off);
+#pragma unroll
+    for (int h = 0; h < kDmaB; ++h) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 8 * h) * kStage, vb[h], off);
+  };
+  const int swz = (l32 >> 1) & 7;
+  auto read = [&](const uint8_t* buf, int row, int t) __attribute__((always_inline)) {   // slice t of a tile row
+    return *reinterpret_cast<const i32x4*>(buf + row * kStage + (((4 * kh + t) ^ swz) << 4));
+  };
+  // Scale words of a stage, straight into registers: a tile row's 32 words of each half lie together, and a wave's loads
+  // come out of the L1 where a neighbour has been.
+  uint32_t oa[TM], ob[TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) oa[i] = (uint32_t)min(m0 + wm * WM + 32 * i + l32, M - 1) * 8 + 4 * kh;
+#pragma unroll
+  for (int j = 0; j < TN; ++j) ob[j] = (uint32_t)min(n0 + wn * WN + 32 * j + l32, N - 1) * 8 + 4 * kh;
+  struct Scales {
+    int a[TM], b[TN];
+  };
+  auto scales = [&](int s, Scales& q) __attribute__((always_inline)) {
+    const uint8_t* pa = sx + (size_t)min(s, stages - 1) * M * 8;
+    const uint8_t* pb = sw + (size_t)min(s, stages - 1) * N * 8;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) q.a[i] = *reinterpret_cast<const int*>(pa + oa[i]);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) q.b[j] = *reinterpret_cast<const int*>(pb + ob[j]);
+  };
+
+  f32x16 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
+  i32x4 a0[TM], b0[TN], a1[TM], b1[TN];
+  auto load = [&](int p, int t, i32x4 (&a)[TM], i32x4 (&b)[TN]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) a[i] = read(LA(p), wm * WM + 32 * i + l32, t);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) b[j] = read(LB(p), wn * WN + 32 * j + l32, t);
+  };
+  auto multiply = [&](auto t, const i32x4 (&a)[TM], const i32x4 (&b)[TN], const Scales& q) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma32<decltype(t)::kCur>(b[j], a[i], acc[i][j], q.b[j], q.a[i]);
+  };
+
+  // Ring.  Stage t lives in buffer (t - sa) % RING.  On entry of stage s its first slice and its scales are in registers
+  // and its copy is visible to every wave; stages s+1 .. s+RING-1 are in flight.  The barrier comes once this wave's reads
+  // of stage s are done and its copy of stage s+1 has landed: behind it the last slice is multiplied while the
+  // next stage's first is read and stage s+RING is copied into the buffer that stage s has left.  The wait counts the
+  // copies of the RING-2 stages behind s+1 alone: loads of scales lie among them, but where the last stages need
+  // none the compiler leaves them out or moves them, and a count that included them would let a copy be late.
+  Scales now, next;
+  scales(sa, now);
+#pragma unroll
+  for (int p = 0; p < RING; ++p) dma(p, sa + p);
+  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 1) * kPer));
+  wg_barrier();
+  load(0, 0, a0, b0);
+  auto stage = [&](auto ring, int s) __attribute__((always_inline)) {
+    constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext;
+    scales(s + 1, next);
+    __builtin_amdgcn_sched_barrier(0);
+    load(p, 1, a1, b1);
+    multiply(Ring<0, 4>{}, a0, b0, now);
+    interleave<TM * TN, TM + TN, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    load(p, 2, a0, b0);
+    multiply(Ring<1, 4>{}, a1, b1, now);
+    interleave<TM * TN, TM + TN, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    load(p, 3, a1, b1);
+    multiply(Ring<2, 4>{}, a0, b0, now);
+    interleave<TM * TN, TM + TN, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 2) * kPer));
+    wg_barrier();
+    load(p1, 0, a0, b0);      // behind the last stage: a repeated copy, unused
+    dma(p, s + RING);
+    multiply(Ring<3, 4>{}, a1, b1, now);
+    interleave<TM * TN, TM + TN, kPer>();
+    now = next;
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  {
+    int s = sa;
+    for (; s + RING <= sb; s += RING) ring_turn<0, RING>(stage, s);
+    ring_tail<0, RING>(stage, s, sb);
+  }
+  __builtin_amdgcn_s_waitcnt(0);                          // no copy into LDS outlives the workgroup
+
+  if (kDivided && splits > 1) {
+    float* tile = part + ((size_t)piece * tiles + lin) * (BM * BN);
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4*>(tile + (wm * WM + 32 * i + l32) * BN + wn * WN + 32 * j + 8 * q + 4 * kh) =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
+  // Epilogue through LDS, 32 rows of a wave at a time, so that whole rows of the tile are stored.  Chunk c of 4 columns
+  // of row r lies at position c ^ (r & 15): both the writes (16 rows of one chunk) and the reads (a row's chunks) cover all banks.
+  wg_barrier();                                           // every wave has read its last stage
+  constexpr int kLanes = WN / 8;                          // lanes of a row: 8 columns each
+  f32x4* own = reinterpret_cast<f32x4*>(wave == 0 ? la0 : wave == 1 ? la1 : RING == 2 ? (wave == 2 ? lb0 : lb1)
+                                                                                      : (wave == 2 ? la2 : lb0));
+  static_assert(32 * WN * 4 <= kA && 32 * WN * 4 <= kB, "a wave's rows fit a stage buffer");
+  const int c8 = lane % kLanes, n = n0 + wn * WN + 8 * c8;
+  float b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = bias ? T::load(bias[min(n + e, N - 1)]) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        own[l32 * (WN / 4) + ((8 * j + 2 * q + kh) ^ (l32 & 15))] =
+            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+#pragma unroll
+    for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
+      const int m = m0 + wm * WM + 32 * i + r;
+      const f32x4 lo = own[r * (WN / 4) + ((2 * c8) ^ (r & 15))], hi = own[r * (WN / 4) + ((2 * c8 + 1) ^ (r & 15))];
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = biased(lo[e], b[e]);
+        y[e + 4] = biased(hi[e], b[e + 4]);
+      }
+      if (m < M) store8<T>(Y + (size_t)m * N + n, y, N - n, (N & 7) == 0);
+    }
+  }
+}
+
+// Adds the pieces of a split product in their order and writes Y.  One thread per four columns of a tile row.
+template <class T, int BM, int BN>
+__global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ part, const uint16_t* __restrict__ bias, int M,
+                                                     int N, uint16_t* __restrict__ Y, int tiles, int splits) {
+  constexpr int kPerTile = BM * BN / 4 / 256;             // workgroups per tile
+  const int lin = blockIdx.x / kPerTile;
+  const int2 tc = tile_coords(lin, (M + BM - 1) / BM, (N + BN - 1) / BN);
+  const int e4 = (blockIdx.x % kPerTile) * 256 + threadIdx.x;
+  const int r = e4 / (BN / 4), c = e4 % (BN / 4) * 4;
+  const int m = tc.x * BM + r, n = tc.y * BN + c;
+  if (m >= M || n >= N) return;
+  f32x4 a = {};
+  for (int p = 0; p < splits; ++p)
+    a += *reinterpret_cast<const f32x4*>(part + ((size_t)p * tiles + lin) * (BM * BN) + r * BN + c);
+  uint16_t* dst = Y + (size_t)m * N + n;
+  float y[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) y[e] = biased(a[e], bias ? T::load(bias[min(n + e, N - 1)]) : 0.0f);
+  if (n + 4 <= N && (N & 3) == 0) {
+    *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+  } else {
+    for (int e = 0; e < 4; ++e)
+      if (n + e < N) dst[e] = T::store(y[e]);
+  }
+}
+
+// A wave's share of a product of few rows: groups [ua, ub) of 16 columns and 16 RT tokens on the 16x16x128.  In slice t
+// (0, 1) of a group lane l supplies row l & 15 and block 2 (l >> 4) + t of both operands: its two scale bytes are one
+// 16-bit word.  An accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
+constexpr int kBatch = 4;        // groups whose loads a wave has in flight
+
+struct Columns {                 // the weights' side of a lane
+  const uint8_t *codes, *scales;
+  size_t step;                   // bytes of the scales of one group
+  __device__ __forceinline__ Columns(const uint8_t* Wq, const uint8_t* sw, int rows, int row, int q, int groups)
+      : codes(Wq + (size_t)row * groups * kStage + 32 * q), scales(sw + (size_t)row * 8 + 2 * q), step((size_t)rows * 8) {}
+  __device__ __forceinline__ i32x4 block(int g, int t) const {
+    return *reinterpret_cast<const i32x4*>(codes + (size_t)g * kStage + 16 * t);
+  }
+  __device__ __forceinline__ int scale(int g) const { return *reinterpret_cast<const uint16_t*>(scales + g * step); }
+};
+
+// 16 RT tokens (blockIdx.y) against 16 columns (blockIdx.x) a workgroup, K divided among its waves.
+template <class T, int RT>
+__global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx,
+                                                         const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
+                                                         const uint16_t* __restrict__ bias, int M, int N, int groups,
+                                                         uint16_t* __restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) float sums[];   // [waves][RT][16 tokens][16 columns]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * RT);
+  const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
+  const Columns w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
+  f32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4{};
+  for (int u = ua; u < ub; u += kBatch) {
+    i32x4 b[kBatch][2], a[RT][kBatch][2];
+    int eb[kBatch], ea[RT][kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {    // past the range's end: the last group again, not multiplied
+      const int g = min(u + k, ub - 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) b[k][t] = w.block(g, t);
+      eb[k] = w.scale(g);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const Columns x(Xq, sx, M, min(m0 + 16 * i + l16, M - 1), q, groups);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) a[i][k][t] = x.block(g, t);
+        ea[i][k] = x.scale(g);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (u + k < ub) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          acc[i] = mma16<0>(b[k][0], a[i][k][0], acc[i], eb[k], ea[i][k]);
+          acc[i] = mma16<1>(b[k][1], a[i][k][1], acc[i], eb[k], ea[i][k]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    *reinterpret_cast<f32x4*>(sums + ((wave * RT + i) * 16 + l16) * 16 + 4 * q) = acc[i];
+  __syncthreads();
+  for (int e = threadIdx.x; e < RT * 256; e += blockDim.x) {
+    const int m = m0 + (e >> 4), n = n0 + (e & 15);
+    if (m >= M || n >= N) continue;
+    float s = 0.0f;
+    for (int v = 0; v < waves; ++v) s += sums[v * RT * 256 + e];
+    Y[(size_t)m * N + n] = T::store(biased(s, bias ? T::load(bias[n]) : 0.0f));
+  }
+}
+
+// The layer for at most MR <= 4 tokens in one launch: every workgroup quantizes the tokens for itself, into LDS, while its
+// first weights are on their way; then as above.
+template <class T, int MR>
+__global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx,
+                                                           const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
+                                                           const uint16_t* __restrict__ bias, int M, int N, int K,
+                                                           int groups, uint16_t* __restrict__ Y) {
+  extern __shared__ __attribute__((aligned(16))) float shared[];   // sums [waves][16 tokens][16 columns], codes, scales
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
+  const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
+  const Columns w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
+  i32x4 b[kBatch][2];
+  int eb[kBatch];
+  auto load = [&](int u) __attribute__((always_inline)) {      // past the range's end: the last group again, not multiplied
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int g = min(u + k, max(ub, 1) - 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) b[k][t] = w.block(g, t);
+      eb[k] = w.scale(g);
+    }
+  };
+  load(ua);
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint8_t* codes = reinterpret_cast<uint8_t*>(shared + waves * 256);
+  uint8_t* scales = codes + MR * groups * kStage;               // [MR][groups * 8]
+  const int chunks = groups * 32;                               // of eight elements: whole groups, so whole blocks a wave
+#pragma unroll
+  for (int m = 0; m < MR; ++m) {
+    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+      const u32x4 x = w8a8::load8<false>(X + (int64_t)min(m, M - 1) * ldx, c, K);
+      uint32_t byte;
+      const uint32_t code = mx::quantize8<T>(x, byte);
+      *reinterpret_cast<uint32_t*>(codes + m * groups * kStage + 4 * c) = code;
+      if ((c & 3) == 0) scales[m * groups * 8 + (c >> 2)] = (uint8_t)byte;
+    }
+  }
+  __syncthreads();
+
+  const uint8_t* row = codes + min(l16, MR - 1) * groups * kStage + 32 * q;
+  const uint8_t* row_scales = scales + min(l16, MR - 1) * groups * 8 + 2 * q;
+  f32x4 acc = {};
+  for (int u = ua; u < ub; u += kBatch) {
+    if (u > ua) load(u);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (u + k < ub) {
+        const i32x4 a0 = *reinterpret_cast<const i32x4*>(row + (u + k) * kStage);
+        const i32x4 a1 = *reinterpret_cast<const i32x4*>(row + (u + k) * kStage + 16);
+        const int ea = *reinterpret_cast<const uint16_t*>(row_scales + (u + k) * 8);
+        acc = mma16<0>(b[k][0], a0, acc, eb[k], ea);
+        acc = mma16<1>(b[k][1], a1, acc, eb[k], ea);
+      }
+    }
+  }
+  *reinterpret_cast<f32x4*>(shared + (wave * 16 + l16) * 16 + 4 * q) = acc;
+  __syncthreads();
+  for (int e = threadIdx.x; e < MR * 16; e += blockDim.x) {
+    const int m = e >> 4, n = n0 + (e & 15);
+    if (m < M && n < N) {
+      float sum = 0.0f;
+      for (int v = 0; v < waves; ++v) sum += shared[v * 256 + e];
+      Y[(size_t)m * N + n] = T::store(biased(sum, bias ? T::load(bias[n]) : 0.0f));
+    }
+  }
+}
+
+// The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
+constexpr int kKinds = 5;
+constexpr int kDividedKind = 1;  // the tile size whose plans may divide K
+constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
+
+// Waves of a workgroup that divide K's groups: whole batches, at most 16 waves.
+int rows_waves(int groups) {
+  if (groups <= 4 * kBatch) return 4;
+  int best = 16, least = 1 << 30;
+  for (int w = min(16, max(4, (groups + 7) / 8)); w <= 16; ++w) {
+    const int loaded = w * (((groups + w - 1) / w + kBatch - 1) / kBatch * kBatch);
+    if (loaded < least) {
+      least = loaded;
+      best = w;
+    }
+  }
+  return best;
+}
+
+template <class T>
+void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias, int M, int N,
+            int K, uint16_t* Y, float* part, const MxPlan& p, hipStream_t st) {
+  const int groups = mx::padded(K) / mx::kGroup;
+  if (p.kind == 0) {
+    const int waves = rows_waves(groups);
+    if (M <= 16)
+      hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
+                         bias, M, N, groups, Y);
+    else
+      hipLaunchKernelGGL((gemm_rows_kernel<T, 2>), dim3(p.tiles, (M + 31) / 32), dim3(64 * waves), waves * 2048, st, Xq, sx, Wq, sw,
+                         bias, M, N, groups, Y);
+    return;
+  }
+  const dim3 grid(p.tiles * p.splits);
+#define ATOM_TILE(KIND, BM, BN, RING, W)                                                                             \
+  if (p.kind == KIND)                                                                                                \
+    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind>), grid, dim3(256), 0, st, Xq, sx, \
+                       Wq, sw, bias, M, N, groups, Y, p.tiles, p.splits, part);
+  ATOM_TILE(1, 64, 128, 3, 2)
+  ATOM_TILE(2, 128, 128, 2, 2)
+  ATOM_TILE(3, 256, 128, 3, 1)
+  ATOM_TILE(4, 256, 256, 2, 1)
+#undef ATOM_TILE
+  if (p.splits > 1)
+    hipLaunchKernelGGL((finish_kernel<T, kBM[kDividedKind], kBN[kDividedKind]>),
+                       dim3(p.tiles * (kBM[kDividedKind] * kBN[kDividedKind] / 1024)), dim3(256), 0, st, part, bias, M,
+                       N, Y, p.tiles, p.splits);
+}
+
+template <class T, int MR>
+void launch_rows(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias, int M,
+                 int N, int K, uint16_t* Y, hipStream_t st) {
+  const int groups = mx::padded(K) / mx::kGroup, waves = rows_waves(groups);
+  hipLaunchKernelGGL((linear_rows_kernel<T, MR>), dim3((N + 15) / 16), dim3(64 * waves),
+                     waves * 1024 + MR * groups * (kStage + 8), st, X, ldx, Wq, sw, bias, M, N, K, groups, Y);
+}
+
+}  // namespace
+
+// The plan of a shape: the kernel whose estimated time (us) is least.
+MxPlan mx_plan(int M, int N, int K) {
+  auto tiles = [&](int kind) {
+    return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
+  };
+  struct Cost {
+    int slots;
+    double full, one, fixed;
+  };
+  constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.0}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
+  const int cus = compute_units(), stages = mx::padded(K) / mx::kGroup;
+  const double bytes = stages * 128.0;
+  MxPlan best = {0, (N + 15) / 16, 1};
+  const int64_t rounds = ((int64_t)best.tiles * (M <= 16 ? 1 : (M + 31) / 32) + cus - 1) / cus;
+  double least = M <= 16 ? 2.9 + rounds * bytes * (M <= 4 ? 0.70e-3 : 0.97e-3) : 2.4 + rounds * (1.0 + 1.45e-3 * bytes);
+  for (int kind = 1; kind < kKinds; ++kind) {
+    const Cost& c = cost[kind];
+    const int t = tiles(kind);
+    for (int splits = 1; splits <= (kind == kDividedKind ? 4 : 1); ++splits) {
+      if (splits > 1 && (stages < 8 * splits || t * splits > cus)) break;
+      const int64_t per = ((int64_t)t * splits + cus - 1) / cus;    // workgroups of the busiest unit
+      const int64_t full = per / c.slots, rest = per % c.slots;
+      const double k = splits == 1 ? bytes : (stages + splits - 1) / splits * 128;
+      const double multiply = 1e-3 * k * (full * c.full + (rest ? c.one : 0.0));
+      const double read = (double)N * bytes / (splits > 1 ? 6e6 : 4.2e6);
+      double time = (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
+      if (splits > 1) time = 1.04 * (time + 2.5 + (double)t * splits * kBM[kind] * kBN[kind] * 8 / 3.3e6);
+      if (time < least) {
+        least = time;
+        best = MxPlan{kind, t, splits};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t mx_workspace_bytes(const MxPlan& p) {
+  return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0;
+}
+
+hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
+                             int M, int N, int K, bool bf16, uint16_t* Y, float* part, const MxPlan& plan,
+                             hipStream_t stream) {
+  if (bf16)
+    launch<Bf16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
+  else
+    launch<Fp16>(Xq, sx, Wq, sw, bias, M, N, K, Y, part, plan, stream);
+  return hipGetLastError();
+}
+
+bool mx_rows_fits(int M, int N, int K) {
+  const int64_t work = (int64_t)M * K * (((N + 15) / 16 + compute_units() - 1) / compute_units());
+  return M <= 4 && work <= 16384;
+}
+
+hipError_t launch_linear_rows_mxfp4(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
+                                    int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream) {
+  if (bf16)
+    M == 1 ? launch_rows<Bf16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+           : launch_rows<Bf16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
+  else
+    M == 1 ? launch_rows<Fp16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+           : launch_rows<Fp16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
+  return hipGetLastError();
+}
+
+}  // namespace atom

@@ -1,0 +1,107 @@
+// MXFP4 row quantize for gfx950, and its inverse (formats: atom_mxfp4.h).
+//
+// What bounds it: HBM, 2 K bytes in and K / 2 + K / 32 out for a row.  A block's scale needs its own 32 values alone, so a
+// row needs no barrier: a lane loads eight elements (16 bytes), four lanes join their maxima by two DPP moves, and the
+// 16 lanes of four blocks gather a word of scale bytes.  Codes leave as 4 bytes a lane, whole lines a wave.
+//
+// Scales lie group by group ([groups, rows, 8]), so a line of them belongs to 16 rows: a workgroup takes whole runs of 16
+// rows of a few groups, and its stores to that line meet in one L2.
+#include "mxfp4_row.h"
+
+namespace atom {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 16;                               // rows of a workgroup: a line of scales
+
+// Workgroup (x, y): rows kRows x .., the 64-lane spans 512 y .. + 511 of K.
+template <class T, bool VEC>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx, int rows, int K,
+                                                            int Kp, uint8_t* __restrict__ Xq, uint8_t* __restrict__ sx) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.y * 64 + lane;                 // the lane's chunk of eight elements in every row
+  u32x4 w[kRows / 4];
+#pragma unroll
+  for (int i = 0; i < kRows / 4; ++i) {
+    const int row = blockIdx.x * kRows + 4 * i + wave;
+    w[i] = w8a8::load8<VEC>(X + (int64_t)min(row, rows - 1) * ldx, c, K);
+  }
+#pragma unroll
+  for (int i = 0; i < kRows / 4; ++i) {
+    const int row = blockIdx.x * kRows + 4 * i + wave;
+    uint32_t byte;
+    const uint32_t code = mx::quantize8<T>(w[i], byte);
+    const uint32_t four = mx::gather_scales(byte, lane);
+    if (row < rows && 8 * c < Kp) {
+      *reinterpret_cast<uint32_t*>(Xq + (int64_t)row * (Kp / 2) + 4 * c) = code;
+      if ((lane & 15) == 0)
+        *reinterpret_cast<uint32_t*>(sx + ((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 4) & 1) * 4) = four;
+    }
+  }
+}
+
+// One thread per eight elements of a row.
+template <class T, bool VEC>
+__global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx,
+                                                              int rows, int K, int Kp, uint16_t* __restrict__ X) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.y * 64 + lane;
+  if (8 * c >= K) return;
+#pragma unroll
+  for (int i = 0; i < kRows / 4; ++i) {
+    const int row = blockIdx.x * kRows + 4 * i + wave;
+    if (row >= rows) return;
+    const uint32_t code = *reinterpret_cast<const uint32_t*>(Xq + (int64_t)row * (Kp / 2) + 4 * c);
+    const uint32_t byte = sx[((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 2) & 7)];
+    // 2^e; 2^-127 is one of fp32's subnormal numbers, and all products with a code are exact
+    const float scale = __builtin_bit_cast(float, byte == mx::kNanScale ? 0x7FC00000u : byte ? byte << 23 : 0x00400000u);
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t q = code >> (4 * j), m = q & 7;
+      // 0, 0.5, 1, 1.5 in halves, then 1 or 1.5 times 2 and 4
+      const float a = m < 4 ? 0.5f * (float)m : (float)(2 + (m & 1)) * (m < 6 ? 1.0f : 2.0f);
+      v[j] = (q & 8 ? -a : a) * scale;
+    }
+    uint16_t* dst = X + (int64_t)row * K + 8 * c;
+    if (VEC) {
+      *reinterpret_cast<u32x4*>(dst) =
+          u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * c + j < K) dst[j] = T::store(v[j]);
+    }
+  }
+}
+
+dim3 grid_of(int rows, int Kp) { return dim3((rows + kRows - 1) / kRows, (Kp + 511) / 512); }
+
+}  // namespace
+
+// (rows <= 2^24 and Kp <= 2^16: at most 2^20 x 2^7 workgroups of 2^8 threads, so 2^28 threads in x.)
+hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int rows, int K, uint8_t* Xq, uint8_t* sx,
+                                 hipStream_t stream) {
+  const int Kp = mx::padded(K);
+  const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid_of(rows, Kp), dim3(kThreads), 0, stream, X, ldx, rows, K, Kp, Xq, sx);
+  };
+  if (bf16) vec ? go(quantize_kernel<Bf16, true>) : go(quantize_kernel<Bf16, false>);
+  else vec ? go(quantize_kernel<Fp16, true>) : go(quantize_kernel<Fp16, false>);
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int rows, int K, bool bf16, uint16_t* X,
+                                   hipStream_t stream) {
+  const int Kp = mx::padded(K);
+  const bool vec = K % 8 == 0;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid_of(rows, Kp), dim3(kThreads), 0, stream, Xq, sx, rows, K, Kp, X);
+  };
+  if (bf16) vec ? go(dequantize_kernel<Bf16, true>) : go(dequantize_kernel<Bf16, false>);
+  else vec ? go(dequantize_kernel<Fp16, true>) : go(dequantize_kernel<Fp16, false>);
+  return hipGetLastError();
+}
+
+}  // namespace atom

@@ -1,0 +1,265 @@
+// Root-mean-square norm with the residual's addition in front and the quantized layers' row formats behind it, for gfx950
+// (formulas: atom_norm.h).
+//
+// What bounds it: HBM.  A row is read once (twice its bytes with a residual, and once out again), kept in registers by
+// the threads that share it, and leaves as codes.
+//
+// Exact codes.  p = h * w is exact in fp32 (two 8- or 11-bit significands), so y = p / sqrt(mean + eps) is one row factor
+// away from exact: the sum of squares and the factor are fp64, and each code is made from p times that factor in fp32.  Its
+// error is at most two roundings, 2^-23 of the value, so only values that close to the border of two codes can come out
+// wrong: they are seen by their distance to it, and the wave makes that chunk's codes again in fp64.  (A norm rounded to 32
+// bits gives other codes for one value in about 2^16, and for a block's exponent the whole block's.)
+#include "mxfp4_row.h"
+#include "w8a8_rows.h"
+
+namespace atom {
+namespace {
+
+struct Norm {
+  const uint16_t *X, *R, *W;
+  int64_t ldx, ldr, ldh;
+  double eps, inv_k;
+  int first, end, rows, K;      // rows of this launch, and of the whole matrix
+  uint16_t* H;
+  uint8_t* Xq;
+  void* sx;
+};
+
+// Code of one value in fp64 units of its scale: nearest, ties to the even code, saturating.
+__device__ __forceinline__ uint32_t fp4_code(double y) {
+  const double a = __builtin_fabs(y);
+  const uint32_t m = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
+  return m | (uint32_t)(__builtin_bit_cast(uint64_t, y) >> 63) << 3;
+}
+
+template <class T, int THREADS, int CH, bool VEC, bool MX>
+__global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm a) {
+  constexpr int kBlock = w8a8::block_threads(THREADS);
+  constexpr int kRows = kBlock / THREADS;               // rows of one workgroup
+  const int t = threadIdx.x % THREADS, lane = threadIdx.x & 63;
+  const int row = a.first + blockIdx.x * kRows + threadIdx.x / THREADS;
+  if (kRows > 1 && row >= a.end) return;                // whole waves: no barrier follows
+  const uint16_t* x = a.X + (size_t)row * a.ldx;
+
+  u32x4 h[CH], w[CH];                                   // chunk c = t + i * THREADS: elements 8 c .. 8 c + 7
+#pragma unroll
+  for (int i = 0; i < CH; ++i) h[i] = w8a8::load8<VEC>(x, t + i * THREADS, a.K);
+  if (a.R) {
+    const uint16_t* r = a.R + (size_t)row * a.ldr;
+    uint16_t* dst = a.H + (size_t)row * a.ldh;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(r, t + i * THREADS, a.K);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * THREADS;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float lo = elem<T>(h[i][j], 0) + elem<T>(w[i][j], 0), hi = elem<T>(h[i][j], 1) + elem<T>(w[i][j], 1);
+        asm("" : "+v"(lo), "+v"(hi));                   // two roundings, as two steps have them: never one fused one
+        h[i][j] = pack2<T>(lo, hi);
+      }
+      if (VEC) {
+        if (8 * c < a.K) *reinterpret_cast<u32x4*>(dst + 8 * c) = h[i];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (8 * c + j < a.K) dst[8 * c + j] = (uint16_t)(h[i][j / 2] >> (16 * (j & 1)));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(a.W, t + i * THREADS, a.K);
+
+  double sum[2] = {};
+  float top = 0.0f;                                     // largest |p| (int8: the row's scale)
+#pragma unroll
+  for (int i = 0; i < CH; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float v = elem<T>(h[i][j / 2], j & 1);
+      sum[j & 1] = __builtin_fma((double)v, (double)v, sum[j & 1]);
+      if (!MX) top = __builtin_fmaxf(top, __builtin_fabsf(v * elem<T>(w[i][j / 2], j & 1)));
+    }
+  double total = sum[0] + sum[1];
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    total += __shfl_xor(total, d);
+    if (!MX) top = __builtin_fmaxf(top, __shfl_xor(top, d));
+  }
+  if constexpr (THREADS > 64) {
+    __shared__ double wave_sum[THREADS / 64];
+    __shared__ float wave_top[THREADS / 64];
+    if (lane == 0) {
+      wave_sum[threadIdx.x >> 6] = total;
+      wave_top[threadIdx.x >> 6] = top;
+    }
+    __syncthreads();
+    total = 0.0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 64; ++i) {            // the same order in every wave
+      total += wave_sum[i];
+      if (!MX) top = __builtin_fmaxf(top, wave_top[i]);
+    }
+  }
+  const double rstd = 1.0 / __builtin_sqrt(total * a.inv_k + a.eps);
+
+  if constexpr (!MX) {
+    const int Kp = (a.K + 127) / 128 * 128;
+    const float s = (float)((double)top * rstd / 127.0);
+    if (t == 0) static_cast<float*>(a.sx)[row] = s;
+    const double f = s > 0.0f ? rstd / (double)s : 0.0;
+    const float f32 = (float)f;
+    uint8_t* q = a.Xq + (size_t)row * Kp;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * THREADS;
+      uint32_t b[8];
+      bool doubt = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1) * f32;
+        const float k = u + 12582912.0f;                // 1.5 * 2^23: the integer (ties to even) in the low byte
+        // |u| <= 127 (1 + 2^-23), so u is within 2^-15.9 of the exact value
+        doubt |= !(__builtin_fabsf(u - (k - 12582912.0f)) < 0.5f - 0x1p-15f);
+        b[j] = __builtin_bit_cast(uint32_t, k);
+      }
+      if (__builtin_amdgcn_ballot_w64(doubt)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double u = (double)(elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1)) * f;
+          b[j] = (uint32_t)(int)__builtin_fmin(__builtin_fmax(__builtin_rint(u), -127.0), 127.0);
+        }
+      }
+      if (8 * c < Kp) {
+        u32x2 o;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          o[k] = __builtin_amdgcn_perm(b[4 * k + 1], b[4 * k], 0x0C0C0400u) |
+                 __builtin_amdgcn_perm(b[4 * k + 3], b[4 * k + 2], 0x04000C0Cu);
+        *reinterpret_cast<u32x2*>(q + 8 * c) = o;
+      }
+    }
+  } else {
+    const int Kp = mx::padded(a.K);
+    uint8_t* q = a.Xq + (size_t)row * (Kp / 2);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = t + i * THREADS;
+      float p[8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        p[j] = elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1);
+        m = max(m, __builtin_bit_cast(uint32_t, p[j]) & 0x7FFFFFFFu);
+      }
+      // the block's largest |y| in fp64, and its exponent
+      const double y = (double)__builtin_bit_cast(float, mx::block_max(m)) * rstd;
+      const int e = (int)(__builtin_bit_cast(uint64_t, y) >> 52);
+      const uint32_t byte = e == 2047 ? mx::kNanScale : (uint32_t)min(max(e - 1023 - 2 + 127, 0), 252);
+      const double f = rstd * __builtin_bit_cast(double, (uint64_t)(1023 + 127 - (int)byte) << 52);
+      const float f32 = (float)f;
+      float u[8];
+      bool doubt = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = p[j] * f32;
+        // within 2 units in the last place of the exact value; all borders (0.25, 0.75, 1.25, ... 5) have 21 zeros at the
+        // end of their significands.  (Not below 8.5: a factor beyond fp32.)
+        doubt |= ((__builtin_bit_cast(uint32_t, u[j]) + 4) & 0x1FFFFFu) < 8 || !(__builtin_fabsf(u[j]) < 8.5f);
+      }
+      uint32_t code = mx::codes8(u);
+      if (__builtin_amdgcn_ballot_w64(doubt)) {
+        code = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) code |= fp4_code((double)p[j] * f) << (4 * j);
+      }
+      if (byte == mx::kNanScale) code = 0;
+      const uint32_t four = mx::gather_scales(byte, lane);
+      if (8 * c < Kp) {
+        *reinterpret_cast<uint32_t*>(q + 4 * c) = code;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.sx) + ((int64_t)(c >> 5) * a.rows + row) * 8 +
+                                       ((c >> 4) & 1) * 4) = four;
+      }
+    }
+  }
+}
+
+template <class T, bool MX, int THREADS, int CH>
+void launch(const Norm& a, bool vec, hipStream_t st) {
+  constexpr int kBlock = w8a8::block_threads(THREADS), kRows = kBlock / THREADS;
+  const dim3 grid((a.end - a.first + kRows - 1) / kRows);
+  if (vec)
+    hipLaunchKernelGGL((norm_kernel<T, THREADS, CH, true, MX>), grid, dim3(kBlock), 0, st, a);
+  else
+    hipLaunchKernelGGL((norm_kernel<T, THREADS, CH, false, MX>), grid, dim3(kBlock), 0, st, a);
+}
+
+template <class T, bool MX>
+void dispatch(const Norm& a, hipStream_t st) {
+  const int Kp = MX ? mx::padded(a.K) : (a.K + 127) / 128 * 128;
+  auto wide = [&](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (a.rows == 1 || ld % 8 == 0); };
+  const bool vec = a.K % 8 == 0 && wide(a.X, a.ldx) && wide(a.W, 0) && (!a.R || (wide(a.R, a.ldr) && wide(a.H, a.ldh)));
+  const w8a8::RowShape s = w8a8::row_shape(a.rows, Kp);
+  if (s.threads == 64 && s.chunks == 1) launch<T, MX, 64, 1>(a, vec, st);
+  else if (s.threads == 64) launch<T, MX, 64, 4>(a, vec, st);
+  else if (s.threads == 256 && s.chunks == 1) launch<T, MX, 256, 1>(a, vec, st);
+  else if (s.threads == 256 && s.chunks == 2) launch<T, MX, 256, 2>(a, vec, st);
+  else if (s.threads == 256) launch<T, MX, 256, 4>(a, vec, st);
+  else if (s.threads == 512 && s.chunks == 2) launch<T, MX, 512, 2>(a, vec, st);
+  else if (s.threads == 512) launch<T, MX, 512, 4>(a, vec, st);
+  else launch<T, MX, 1024, 8>(a, vec, st);
+}
+
+// What int8 rows stand for: one thread per eight elements.
+template <class T, bool VEC>
+__global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* __restrict__ Xq, const float* __restrict__ sx, int rows,
+                                                         int K, int Kp, uint16_t* __restrict__ X) {
+  const int c = blockIdx.y * 64 + (threadIdx.x & 63), row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= rows || 8 * c >= K) return;
+  const u32x2 q = *reinterpret_cast<const u32x2*>(Xq + (size_t)row * Kp + 8 * c);
+  const float s = sx[row];
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = (float)(int8_t)(q[j / 4] >> (8 * (j & 3))) * s;
+    asm("" : "+v"(v[j]));
+  }
+  uint16_t* dst = X + (size_t)row * K + 8 * c;
+  if (VEC) {
+    *reinterpret_cast<u32x4*>(dst) =
+        u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * c + j < K) dst[j] = T::store(v[j]);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm(const NormCall& n, bool mx, hipStream_t stream) {
+  const w8a8::RowShape s = w8a8::row_shape(n.rows, mx ? mx::padded(n.K) : (n.K + 127) / 128 * 128);
+  const int64_t most = w8a8::launch_rows(s.threads);    // rows of one launch, which has less than 2^32 threads
+  for (int64_t r = 0; r < n.rows; r += most) {
+    const Norm a = {n.X, n.R, n.W, n.ldx, n.ldr, n.ldh, n.eps, 1.0 / n.K, (int)r, (int)(n.rows - r < most ? n.rows : r + most),
+                    n.rows, n.K, n.H, n.Xq, n.sx};
+    if (n.bf16)
+      mx ? dispatch<Bf16, true>(a, stream) : dispatch<Bf16, false>(a, stream);
+    else
+      mx ? dispatch<Fp16, true>(a, stream) : dispatch<Fp16, false>(a, stream);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize_w8a8(const int8_t* Xq, const float* sx, int rows, int K, bool bf16, uint16_t* X,
+                                  hipStream_t stream) {
+  const int Kp = (K + 127) / 128 * 128;
+  const dim3 grid((rows + 3) / 4, (K + 511) / 512);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, Xq, sx, rows, K, Kp, X); };
+  if (bf16) K % 8 == 0 ? go(dequantize_kernel<Bf16, true>) : go(dequantize_kernel<Bf16, false>);
+  else K % 8 == 0 ? go(dequantize_kernel<Fp16, true>) : go(dequantize_kernel<Fp16, false>);
+  return hipGetLastError();
+}
+
+}  // namespace atom

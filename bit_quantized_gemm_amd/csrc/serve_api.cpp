@@ -3,52 +3,12 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "host_checks.h"
 #include "serve_internal.h"
 
 namespace {
 
-struct Range {
-  uintptr_t lo, hi;   // [lo, hi)
-};
-
-Range range_of(const void* p, uint64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + (uintptr_t)bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Every output must be disjoint from every input and from the other outputs.
-int check_overlap(const Range* in, int n_in, const Range* out, int n_out) {
-  for (int o = 0; o < n_out; ++o) {
-    for (int i = 0; i < n_in; ++i)
-      if (overlap(out[o], in[i])) return ATOM_E_OVERLAP;
-    for (int p = o + 1; p < n_out; ++p)
-      if (overlap(out[o], out[p])) return ATOM_E_OVERLAP;
-  }
-  return ATOM_OK;
-}
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-bool aligned16(const void* p) { return aligned(p, 16); }
-bool valid_dtype(int32_t t) { return t == ATOM_FP16 || t == ATOM_BF16; }
-bool valid_rows(int32_t r) { return r >= 1 && r <= ATOM_MAX_ROWS; }
-int hip_status(hipError_t e) { return e == hipSuccess ? ATOM_OK : ATOM_E_HIP; }
-uint64_t up16(uint64_t n) { return (n + 15) & ~(uint64_t)15; }
-
-// ---- W8A8
-bool valid_k8(int32_t K) { return K >= 1 && K <= ATOM_MAX_K; }
-uint64_t row_bytes8(int32_t K) { return ((uint64_t)K + 127) / 128 * 128; }
-bool valid_gemm8(int32_t M, int32_t N, int32_t K) {
-  if (!valid_k8(K) || !valid_rows(M) || !valid_rows(N)) return false;
-  return (uint64_t)((M + 127) / 128) * (uint64_t)((N + 127) / 128) <= ATOM_MAX_TILES;
-}
-bool valid_x(const void* X, int64_t ldx, int32_t rows, int32_t K) {
-  return aligned(X, 2) && (rows == 1 || (ldx >= K && ldx <= ((int64_t)1 << 40)));
-}
-uint64_t x_bytes(int64_t ldx, int32_t rows, int32_t K) {
-  return rows == 1 ? (uint64_t)K * 2 : ((uint64_t)(rows - 1) * (uint64_t)ldx + (uint64_t)K) * 2;
-}
+using namespace atom::check;
 
 // ---- KV cache
 bool valid_cache(const atom_kv4_cache* c) {
@@ -100,6 +60,17 @@ int atom_quantize_w8a8(const void* X, int64_t ldx, int32_t dtype, int32_t rows, 
   if (int s = check_overlap(in, 1, out, 2)) return s;
   return hip_status(atom::launch_quantize_w8a8(static_cast<const uint16_t*>(X), ldx, dtype == ATOM_BF16, rows, K,
                                                static_cast<int8_t*>(Xq), sx, static_cast<hipStream_t>(stream)));
+}
+
+int atom_dequantize_w8a8(const void* Xq, const float* sx, int32_t rows, int32_t K, int32_t dtype, void* X, void* stream) {
+  if (!X || !Xq || !sx) return ATOM_E_NULL;
+  if (!valid_k8(K) || !valid_rows(rows) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  if (!aligned16(X) || !aligned16(Xq) || !aligned16(sx)) return ATOM_E_ALIGN;
+  const Range in[2] = {range_of(Xq, (uint64_t)rows * row_bytes8(K)), range_of(sx, (uint64_t)rows * 4)};
+  const Range out[1] = {range_of(X, (uint64_t)rows * (uint64_t)K * 2)};
+  if (int s = check_overlap(in, 2, out, 1)) return s;
+  return hip_status(atom::launch_dequantize_w8a8(static_cast<const int8_t*>(Xq), sx, rows, K, dtype == ATOM_BF16,
+                                                 static_cast<uint16_t*>(X), static_cast<hipStream_t>(stream)));
 }
 
 int64_t atom_gemm_w8a8_workspace_bytes(int32_t M, int32_t N, int32_t K) {

@@ -8,6 +8,8 @@
 #include <stdint.h>
 
 #include "atom_kv4.h"
+#include "atom_mxfp4.h"
+#include "atom_norm.h"
 #include "atom_w8a8.h"
 #include "kv4_plan.h"
 
@@ -66,6 +68,68 @@ hipError_t launch_gemm_w8a8(const int8_t* Xq, const float* sx, const int8_t* Wq,
 bool linear_rows_fits(int M, int N, int K);
 hipError_t launch_linear_rows(const uint16_t* X, int64_t ldx, const int8_t* Wq, const float* sw, const uint16_t* bias,
                               int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream);
+
+hipError_t launch_dequantize_w8a8(const int8_t* Xq, const float* sx, int rows, int K, bool bf16, uint16_t* X,
+                                  hipStream_t stream);
+
+// ---- MXFP4
+hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int rows, int K, uint8_t* Xq, uint8_t* sx,
+                                 hipStream_t stream);
+hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int rows, int K, bool bf16, uint16_t* X,
+                                   hipStream_t stream);
+// As W8Plan; the parts of a divided product are fp32.
+struct MxPlan {
+  int kind, tiles, splits;
+};
+MxPlan mx_plan(int M, int N, int K);
+int64_t mx_workspace_bytes(const MxPlan& plan);
+hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
+                             int M, int N, int K, bool bf16, uint16_t* Y, float* part, const MxPlan& plan,
+                             hipStream_t stream);
+bool mx_rows_fits(int M, int N, int K);
+hipError_t launch_linear_rows_mxfp4(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
+                                    int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream);
+
+// ---- norm in front of the quantized layers; R and H are null together
+struct NormCall {
+  const uint16_t* X;
+  int64_t ldx;
+  const uint16_t* R;
+  int64_t ldr;
+  const uint16_t* W;
+  double eps;
+  bool bf16;
+  int rows, K;
+  uint16_t* H;
+  int64_t ldh;
+  uint8_t* Xq;
+  void* sx;
+};
+hipError_t launch_rmsnorm(const NormCall& n, bool mx, hipStream_t stream);
+
+// ---- KV cache's bookkeeping
+struct Kv4Extend {
+  const int32_t *lens, *more;
+  int32_t* table;
+  int batch, width, log_page;
+  const int32_t* free_pages;
+  int capacity;
+  const int32_t* state;
+  int64_t* slots;
+  int total;
+  int32_t *start, *lens_out, *state_out;
+};
+hipError_t launch_kv4_extend(const Kv4Extend& a, hipStream_t stream);
+struct Kv4Release {
+  const uint8_t* done;
+  const int32_t *lens, *table;
+  int batch, width, log_page;
+  int32_t* free_pages;
+  int capacity;
+  const int32_t* state;
+  int32_t *lens_out, *state_out;
+};
+hipError_t launch_kv4_release(const Kv4Release& a, hipStream_t stream);
 
 // ---- KV cache
 hipError_t launch_kv4_append(const uint16_t* K, int64_t k_stride, const uint16_t* V, int64_t v_stride,

@@ -2,6 +2,7 @@
 scale for each token and one for each output channel, fp16 or bf16 in and out.
 
 * ``atom_quantize_w8a8(X)``                     -> (Xq int8 [rows, row bytes], sx fp32 [rows]); weights too (offline)
+* ``atom_dequantize_w8a8(Xq, sx, K)``           -> X [rows, K], what the codes stand for
 * ``atom_gemm_w8a8(Xq, sx, Wq, sw, K)``         -> Y [M, N]
 * ``linear_w8a8(X, Wq, sw, bias)``              -> Y [M, N]: both in one call
 * ``atom_w8a8_row_bytes(K)``, ``atom_gemm_w8a8_workspace_bytes(M, N, K)``,
@@ -17,12 +18,12 @@ import functools
 
 import bit_quantized_gemm_amd as _bq
 
-__all__ = ["atom_w8a8_row_bytes", "atom_quantize_w8a8", "atom_gemm_w8a8_workspace_bytes", "atom_gemm_w8a8",
-           "atom_linear_w8a8_workspace_bytes", "linear_w8a8"]
+__all__ = ["atom_w8a8_row_bytes", "atom_quantize_w8a8", "atom_dequantize_w8a8", "atom_gemm_w8a8_workspace_bytes",
+           "atom_gemm_w8a8", "atom_linear_w8a8_workspace_bytes", "linear_w8a8"]
 
 # Every symbol declared in include/atom_w8a8.h.
-EXPORTS = ("atom_w8a8_row_bytes", "atom_quantize_w8a8", "atom_gemm_w8a8_workspace_bytes", "atom_gemm_w8a8",
-           "atom_linear_w8a8_workspace_bytes", "atom_linear_w8a8")
+EXPORTS = ("atom_w8a8_row_bytes", "atom_quantize_w8a8", "atom_dequantize_w8a8", "atom_gemm_w8a8_workspace_bytes",
+           "atom_gemm_w8a8", "atom_linear_w8a8_workspace_bytes", "atom_linear_w8a8")
 
 
 def signatures():
@@ -30,6 +31,7 @@ def signatures():
     return {
         "atom_w8a8_row_bytes": (i64, [i32]),
         "atom_quantize_w8a8": (ctypes.c_int, [vp, i64, i32, i32, i32, vp, vp, vp]),
+        "atom_dequantize_w8a8": (ctypes.c_int, [vp, vp, i32, i32, i32, vp, vp]),
         "atom_gemm_w8a8_workspace_bytes": (i64, [i32, i32, i32]),
         "atom_gemm_w8a8": (ctypes.c_int, [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, i64, vp]),
         "atom_linear_w8a8_workspace_bytes": (i64, [i32, i32, i32]),
@@ -153,6 +155,24 @@ def atom_quantize_w8a8(X, Xq=None, sx=None, stream=None):
         _bq._check(_bq.load_library().atom_quantize_w8a8(X.data_ptr(), ldx, kind, rows, K, pQ, pS,
                                                          _bq._stream(stream, X.device)), "atom_quantize_w8a8")
     return Xq, sx
+
+
+def atom_dequantize_w8a8(Xq, sx, K, dtype=None, X=None, stream=None):
+    """X [rows, K] that packed rows stand for, code * scale, in `dtype` (default fp16, or X's)."""
+    torch = _bq._torch()
+    K = int(K)
+    rb = _row_bytes(K)
+    rows, _ = _bq._mat(Xq, "Xq")
+    dtype = dtype if dtype is not None else X.dtype if isinstance(X, torch.Tensor) else torch.float16
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise _bq.AtomError(f"dtype must be torch.float16 or torch.bfloat16 (got {dtype})")
+    if X is None:
+        X = empty((rows, K), dtype, Xq, stream)
+    pQ, pS, pX = _bq._ptrs((Xq, "Xq", torch.int8, (rows, rb)), (sx, "sx", torch.float32, (rows,)), (X, "X", dtype, (rows, K)))
+    with on_device(Xq):
+        _bq._check(_bq.load_library().atom_dequantize_w8a8(pQ, pS, rows, K, int(dtype is torch.bfloat16), pX,
+                                                           _bq._stream(stream, Xq.device)), "atom_dequantize_w8a8")
+    return X
 
 
 def atom_gemm_w8a8(Xq, sx, Wq, sw, K, bias=None, Y=None, dtype=None, workspace=None, stream=None):

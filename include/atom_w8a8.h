@@ -42,6 +42,12 @@ int atom_quantize_w8a8(const void *X, int64_t ldx, int32_t dtype, int32_t rows, 
                        void *stream);
 
 /*
+ * What packed rows stand for: fl32(code * scale), rounded to `dtype`.
+ *   X : fp16 / bf16 [rows, K] contiguous                                      (output)
+ */
+int atom_dequantize_w8a8(const void *Xq, const float *sx, int32_t rows, int32_t K, int32_t dtype, void *X, void *stream);
+
+/*
  * Y from packed operands.  bias (of `dtype`, [N]) may be NULL.
  *   Xq : const int8 [M, row bytes]   sx : const float [M]
  *   Wq : const int8 [N, row bytes]   sw : const float [N]
