@@ -40,7 +40,7 @@ __device__ __forceinline__ float biased(float acc, float bias) {
 
 // BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
 // workgroup p * tiles + t and writes its fp32 tile to part[(p * tiles + t) * BM * BN].
-template <class T, int BM, int BN, int RING, int WAVES, bool kDivided>
+template <class T, int BM, int BN, int RING, int WAVES, bool kDivided, bool kEarly>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
     const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ Wq,
     const uint8_t* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int stages, uint16_t* __restrict__ Y,
@@ -92,35 +92,54 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     const int r = wave * (BN / 4) + 8 * h + lane / 8;
     vb[h] = min(r, rows_b - 1) * bytes + pos(r, lane & 7) * 16;
   }
-  // Copies of stages behind the last repeat it (never read).
-  auto dma = [&](int p, int s) __attribute__((always_inline)) {
+  // Instructions [from, to) of a stage's copies.  Stages behind the last repeat it (never read).
+  auto dma = [&](int p, int s, int from, int to) __attribute__((always_inline)) {
     const int off = min(s, stages - 1) * kStage;
 #pragma unroll
-    for (int h = 0; h < kDmaA; ++h) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 8 * h) * kStage, va[h], off);
+    for (int h = 0; h < kDmaA; ++h)
+      if (h >= from && h < to) lds_dma16(ra, LA(p) + (wave * (BM / 4) + 8 * h) * kStage, va[h], off);
 #pragma unroll
-    for (int h = 0; h < kDmaB; ++h) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 8 * h) * kStage, vb[h], off);
+    for (int h = 0; h < kDmaB; ++h)
+      if (kDmaA + h >= from && kDmaA + h < to) lds_dma16(rb, LB(p) + (wave * (BN / 4) + 8 * h) * kStage, vb[h], off);
   };
   const int swz = (l32 >> 1) & 7;
   auto read = [&](const uint8_t* buf, int row, int t) __attribute__((always_inline)) {   // slice t of a tile row
     return *reinterpret_cast<const i32x4*>(buf + row * kStage + (((4 * kh + t) ^ swz) << 4));
   };
-  // Scale words of a stage, straight into registers: a tile row's 32 words of each half lie together, and a wave's loads
-  // come out of the L1 where a neighbour has been.
-  uint32_t oa[TM], ob[TN];
+  // Scales of a stage: 8 bytes a row, loaded once by the workgroup (thread t: row t of the two operands' rows, and row 256 + t)
+  // and read from LDS as words.  Loads of each wave's own words take four times the instructions, and they stand in line
+  // with the copies: 4096 x 28672 x 8192 of zeros 371 us so, 330 us without any scales.
+  constexpr int kRows = (BM + BN + 255) / 256;
+  __shared__ __attribute__((aligned(16))) u32x2 ls0[kRows * 256], ls1[kRows * 256];
+  const uint8_t* from[kRows];
+  size_t step[kRows];
 #pragma unroll
-  for (int i = 0; i < TM; ++i) oa[i] = (uint32_t)min(m0 + wm * WM + 32 * i + l32, M - 1) * 8 + 4 * kh;
+  for (int i = 0; i < kRows; ++i) {
+    const int e = tid + 256 * i;
+    const bool is_a = e < BM;
+    from[i] = (is_a ? sx : sw) + (size_t)(is_a ? min(m0 + e, M - 1) : min(n0 + e - BM, N - 1)) * 8;
+    step[i] = (size_t)(is_a ? M : N) * 8;
+  }
+  struct Rows {
+    u32x2 v[kRows];
+  };
+  auto fetch = [&](int s, Rows& r) __attribute__((always_inline)) {
 #pragma unroll
-  for (int j = 0; j < TN; ++j) ob[j] = (uint32_t)min(n0 + wn * WN + 32 * j + l32, N - 1) * 8 + 4 * kh;
+    for (int i = 0; i < kRows; ++i) r.v[i] = *reinterpret_cast<const u32x2*>(from[i] + min(s, stages - 1) * step[i]);
+  };
+  auto put = [&](int odd, const Rows& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) (odd ? ls1 : ls0)[tid + 256 * i] = r.v[i];
+  };
   struct Scales {
     int a[TM], b[TN];
   };
-  auto scales = [&](int s, Scales& q) __attribute__((always_inline)) {
-    const uint8_t* pa = sx + (size_t)min(s, stages - 1) * M * 8;
-    const uint8_t* pb = sw + (size_t)min(s, stages - 1) * N * 8;
+  auto scales = [&](int odd, Scales& q) __attribute__((always_inline)) {
+    const uint8_t* l = reinterpret_cast<const uint8_t*>(odd ? ls1 : ls0) + l32 * 8 + 4 * kh;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) q.a[i] = *reinterpret_cast<const int*>(pa + oa[i]);
+    for (int i = 0; i < TM; ++i) q.a[i] = *reinterpret_cast<const int*>(l + (wm * WM + 32 * i) * 8);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) q.b[j] = *reinterpret_cast<const int*>(pb + ob[j]);
+    for (int j = 0; j < TN; ++j) q.b[j] = *reinterpret_cast<const int*>(l + (BM + wn * WN + 32 * j) * 8);
   };
 
   f32x16 acc[TM][TN];
@@ -128,62 +147,138 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x16{};
-  i32x4 a0[TM], b0[TN], a1[TM], b1[TN];
-  auto load = [&](int p, int t, i32x4 (&a)[TM], i32x4 (&b)[TN]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < TM; ++i) a[i] = read(LA(p), wm * WM + 32 * i + l32, t);
-#pragma unroll
-    for (int j = 0; j < TN; ++j) b[j] = read(LB(p), wn * WN + 32 * j + l32, t);
+  struct Slice {
+    i32x4 a[TM], b[TN];
   };
-  auto multiply = [&](auto t, const i32x4 (&a)[TM], const i32x4 (&b)[TN], const Scales& q) __attribute__((always_inline)) {
+  auto load = [&](int p, int t, Slice& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i) r.a[i] = read(LA(p), wm * WM + 32 * i + l32, t);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) r.b[j] = read(LB(p), wn * WN + 32 * j + l32, t);
+  };
+  auto multiply = [&](auto t, const Slice& r, const Scales& q) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) acc[i][j] = mma32<decltype(t)::kCur>(b[j], a[i], acc[i][j], q.b[j], q.a[i]);
+      for (int j = 0; j < TN; ++j) acc[i][j] = mma32<decltype(t)::kCur>(r.b[j], r.a[i], acc[i][j], q.b[j], q.a[i]);
   };
 
-  // Ring.  Stage t lives in buffer (t - sa) % RING.  On entry of stage s its first slice and its scales are in registers
-  // and its copy is visible to every wave; stages s+1 .. s+RING-1 are in flight.  The barrier comes once this wave's reads
-  // of stage s are done and its copy of stage s+1 has landed: behind it the last slice is multiplied while the
-  // next stage's first is read and stage s+RING is copied into the buffer that stage s has left.  The wait counts the
-  // copies of the RING-2 stages behind s+1 alone: loads of scales lie among them, but where the last stages need
-  // none the compiler leaves them out or moves them, and a count that included them would let a copy be late.
+  // Ring.  Stage t lives in buffer (t - sa) % RING, its scales in ls0 or ls1 by its parity.  A CU takes 64 bytes of copies a
+  // cycle and a wave waits at a copy that it does not take, so a stage's copies are spread over the slices.  Waits
+  // count copies alone: loads of scales lie among them, but where the last stages need none the compiler leaves
+  // them out or moves them, and a count that included them would let a copy be late.
+  constexpr int kReads = TM + TN, kMmas = TM * TN;
+  Rows rows;
   Scales now, next;
-  scales(sa, now);
+  fetch(sa, rows);
+  put(0, rows);
+  fetch(sa + 1, rows);
+  if constexpr (kEarly) {
+    // Two buffers.  All operands of a stage are in registers after its first slice; behind that slice's barrier stage s+2
+    // is copied into the buffer, and it has six slices to arrive.
+    constexpr int kHalf = kPer / 2;
+    Slice r0, r1, r2, r3;
 #pragma unroll
-  for (int p = 0; p < RING; ++p) dma(p, sa + p);
-  __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 1) * kPer));
-  wg_barrier();
-  load(0, 0, a0, b0);
-  auto stage = [&](auto ring, int s) __attribute__((always_inline)) {
-    constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext;
-    scales(s + 1, next);
-    __builtin_amdgcn_sched_barrier(0);
-    load(p, 1, a1, b1);
-    multiply(Ring<0, 4>{}, a0, b0, now);
-    interleave<TM * TN, TM + TN, 0>();
-    __builtin_amdgcn_sched_barrier(0);
-    load(p, 2, a0, b0);
-    multiply(Ring<1, 4>{}, a1, b1, now);
-    interleave<TM * TN, TM + TN, 0>();
-    __builtin_amdgcn_sched_barrier(0);
-    load(p, 3, a1, b1);
-    multiply(Ring<2, 4>{}, a0, b0, now);
-    interleave<TM * TN, TM + TN, 0>();
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((RING - 2) * kPer));
+    for (int p = 0; p < 2; ++p) dma(p, sa + p, 0, kPer);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kPer));
     wg_barrier();
-    load(p1, 0, a0, b0);      // behind the last stage: a repeated copy, unused
-    dma(p, s + RING);
-    multiply(Ring<3, 4>{}, a1, b1, now);
-    interleave<TM * TN, TM + TN, kPer>();
-    now = next;
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  {
+    load(0, 0, r0);
+    load(0, 1, r1);
+    scales(0, now);
+    auto stage = [&](auto ring, int s) __attribute__((always_inline)) {
+      constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext;
+      load(p, 2, r2);
+      load(p, 3, r3);
+      multiply(Ring<0, 4>{}, r0, now);
+      interleave<kMmas, 2 * kReads, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(63));
+      wg_barrier();             // every wave has read stage s
+      put(p1, rows);
+      fetch(s + 2, rows);
+      dma(p, s + 2, 0, kHalf);
+      multiply(Ring<1, 4>{}, r1, now);
+      interleave<kMmas, 0, kHalf + kRows>();
+      __builtin_amdgcn_sched_barrier(0);
+      dma(p, s + 2, kHalf, kPer);
+      multiply(Ring<2, 4>{}, r2, now);
+      interleave<kMmas, 0, kPer - kHalf>();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kPer));
+      wg_barrier();             // stage s+1 and its scales are there
+      load(p1, 0, r0);          // behind the last stage: a repeated copy, unused
+      load(p1, 1, r1);
+      scales(p1, next);
+      multiply(Ring<3, 4>{}, r3, now);
+      interleave<kMmas, 3 * kReads, 0>();
+      now = next;
+      __builtin_amdgcn_sched_barrier(0);
+    };
     int s = sa;
     for (; s + RING <= sb; s += RING) ring_turn<0, RING>(stage, s);
     ring_tail<0, RING>(stage, s, sb);
+  } else {
+    // Three buffers.  On entry of stage s its first slice and its scales are in registers and its copy is visible to every
+    // wave; stage s+1 and a quarter of s+2 are in flight.  The barrier comes once this wave's reads of stage s are
+    // done and its copy of stage s+1 has landed: behind it the last slice is multiplied while the next stage's first is
+    // read and the copy of stage s+3 begins in the buffer that stage s has left.
+    constexpr int kQ1 = (kPer + 3) / 4, kQ2 = (kPer + 1) / 2, kQ3 = (3 * kPer + 3) / 4;
+    Slice r0, r1;
+    dma(0, sa, 0, kPer);
+    dma(1, sa + 1, 0, kPer);
+    dma(2, sa + 2, 0, kQ1);
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kPer));
+    wg_barrier();
+    load(0, 0, r0);
+    scales(0, now);
+    auto stage = [&](auto ring, int s, int odd) __attribute__((always_inline)) {
+      constexpr int p = decltype(ring)::kCur, p1 = decltype(ring)::kNext, p2 = decltype(ring)::kAfterNext;
+      load(p, 1, r1);
+      dma(p2, s + 2, kQ1, kQ2);
+      multiply(Ring<0, 4>{}, r0, now);
+      interleave<kMmas, kReads, kQ2 - kQ1>();
+      __builtin_amdgcn_sched_barrier(0);
+      put(!odd, rows);
+      load(p, 2, r0);
+      dma(p2, s + 2, kQ2, kQ3);
+      multiply(Ring<1, 4>{}, r1, now);
+      interleave<kMmas, kReads, kQ3 - kQ2>();
+      __builtin_amdgcn_sched_barrier(0);
+      fetch(s + 2, rows);
+      load(p, 3, r1);
+      dma(p2, s + 2, kQ3, kPer);
+      multiply(Ring<2, 4>{}, r0, now);
+      interleave<kMmas, kReads, kPer - kQ3 + kRows>();
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kPer));
+      wg_barrier();
+      load(p1, 0, r0);          // behind the last stage: a repeated copy, unused
+      scales(!odd, next);
+      dma(p, s + 3, 0, kQ1);
+      multiply(Ring<3, 4>{}, r1, now);
+      interleave<kMmas, 2 * kReads, kQ1>();
+      now = next;
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int s = sa;
+    auto turn = [&](int odd) __attribute__((always_inline)) {
+      stage(Ring<0, 3>{}, s, odd);
+      stage(Ring<1, 3>{}, s + 1, !odd);
+      stage(Ring<2, 3>{}, s + 2, odd);
+      s += 3;
+    };
+    for (; s + 6 <= sb;) {
+      turn(0);
+      turn(1);
+    }
+    if (s + 3 <= sb) {
+      turn(0);
+      if (s < sb) stage(Ring<0, 3>{}, s, 1);
+      if (s + 1 < sb) stage(Ring<1, 3>{}, s + 1, 0);
+    } else {
+      if (s < sb) stage(Ring<0, 3>{}, s, 0);
+      if (s + 1 < sb) stage(Ring<1, 3>{}, s + 1, 1);
+    }
   }
   __builtin_amdgcn_s_waitcnt(0);                          // no copy into LDS outlives the workgroup
 
@@ -207,9 +302,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
                                                                                       : (wave == 2 ? la2 : lb0));
   static_assert(32 * WN * 4 <= kA && 32 * WN * 4 <= kB, "a wave's rows fit a stage buffer");
   const int c8 = lane % kLanes, n = n0 + wn * WN + 8 * c8;
-  float b[8];
+  float b[8] = {};
+  if (bias) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) b[e] = bias ? T::load(bias[min(n + e, N - 1)]) : 0.0f;
+    for (int e = 0; e < 8; ++e) b[e] = T::load(bias[min(n + e, N - 1)]);
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -434,14 +531,14 @@ void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8
     return;
   }
   const dim3 grid(p.tiles * p.splits);
-#define ATOM_TILE(KIND, BM, BN, RING, W)                                                                             \
+#define ATOM_TILE(KIND, BM, BN, RING, W, E)                                                                             \
   if (p.kind == KIND)                                                                                                \
-    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind>), grid, dim3(256), 0, st, Xq, sx, \
+    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind, E>), grid, dim3(256), 0, st, Xq, sx, \
                        Wq, sw, bias, M, N, groups, Y, p.tiles, p.splits, part);
-  ATOM_TILE(1, 64, 128, 3, 2)
-  ATOM_TILE(2, 128, 128, 2, 2)
-  ATOM_TILE(3, 256, 128, 3, 1)
-  ATOM_TILE(4, 256, 256, 2, 1)
+  ATOM_TILE(1, 64, 128, 3, 2, false)
+  ATOM_TILE(2, 128, 128, 2, 2, true)
+  ATOM_TILE(3, 256, 128, 3, 1, false)
+  ATOM_TILE(4, 256, 256, 2, 1, true)
 #undef ATOM_TILE
   if (p.splits > 1)
     hipLaunchKernelGGL((finish_kernel<T, kBM[kDividedKind], kBN[kDividedKind]>),
