@@ -10,6 +10,7 @@
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "gemm_tile.h"
+#include "mxfp4_plan.h"
 #include "mxfp4_row.h"
 
 namespace atom {
@@ -295,9 +296,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     return;
   }
   // Epilogue through LDS, 32 rows of a wave at a time, so that whole rows of the tile are stored.  Chunk c of 4 columns
-  // of row r lies at position c ^ (r & 15): both the writes (16 rows of one chunk) and the reads (a row's chunks) cover all banks.
+  // of row r lies at position c ^ (r & 15) (& 7 where a row has eight): the writes (16 rows of one chunk) and the reads (a
+  // row's chunks) cover the banks.
   wg_barrier();                                           // every wave has read its last stage
   constexpr int kLanes = WN / 8;                          // lanes of a row: 8 columns each
+  constexpr int kTurn = WN / 4 < 16 ? WN / 4 - 1 : 15;
   f32x4* own = reinterpret_cast<f32x4*>(wave == 0 ? la0 : wave == 1 ? la1 : RING == 2 ? (wave == 2 ? lb0 : lb1)
                                                                                       : (wave == 2 ? la2 : lb0));
   static_assert(32 * WN * 4 <= kA && 32 * WN * 4 <= kB, "a wave's rows fit a stage buffer");
@@ -313,12 +316,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     for (int j = 0; j < TN; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        own[l32 * (WN / 4) + ((8 * j + 2 * q + kh) ^ (l32 & 15))] =
+        own[l32 * (WN / 4) + ((8 * j + 2 * q + kh) ^ (l32 & kTurn))] =
             f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
 #pragma unroll
     for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
       const int m = m0 + wm * WM + 32 * i + r;
-      const f32x4 lo = own[r * (WN / 4) + ((2 * c8) ^ (r & 15))], hi = own[r * (WN / 4) + ((2 * c8 + 1) ^ (r & 15))];
+      const f32x4 lo = own[r * (WN / 4) + ((2 * c8) ^ (r & kTurn))], hi = own[r * (WN / 4) + ((2 * c8 + 1) ^ (r & kTurn))];
       float y[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -356,23 +359,21 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ p
   }
 }
 
-// A wave's share of a product of few rows: groups [ua, ub) of 16 columns and 16 RT tokens on the 16x16x128.  In slice t
-// (0, 1) of a group lane l supplies row l & 15 and block 2 (l >> 4) + t of both operands: its two scale bytes are one
-// 16-bit word.  An accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
-constexpr int kBatch = 4;        // groups whose loads a wave has in flight
-
-struct Columns {                 // the weights' side of a lane
+// Few rows: 16 RT tokens (blockIdx.y) against 16 columns (blockIdx.x) a workgroup on the 16x16x128, K's groups divided among
+// its waves, operands straight into registers.  In slice t (0, 1) of a group lane l supplies row l & 15 and block 2 (l >> 4) + t
+// of both operands: its two scale bytes are one 16-bit word.  An accumulator holds token l & 15, columns 4 (l >> 4) .. + 3.
+struct Operand {                 // a lane's rows of one operand
   const uint8_t *codes, *scales;
   size_t step;                   // bytes of the scales of one group
-  __device__ __forceinline__ Columns(const uint8_t* Wq, const uint8_t* sw, int rows, int row, int q, int groups)
-      : codes(Wq + (size_t)row * groups * kStage + 32 * q), scales(sw + (size_t)row * 8 + 2 * q), step((size_t)rows * 8) {}
+  __device__ __forceinline__ Operand(const uint8_t* q, const uint8_t* s, int rows, int row, int quarter, int groups)
+      : codes(q + (size_t)row * groups * kStage + 32 * quarter), scales(s + (size_t)row * 8 + 2 * quarter), step((size_t)rows * 8) {}
   __device__ __forceinline__ i32x4 block(int g, int t) const {
     return *reinterpret_cast<const i32x4*>(codes + (size_t)g * kStage + 16 * t);
   }
   __device__ __forceinline__ int scale(int g) const { return *reinterpret_cast<const uint16_t*>(scales + g * step); }
 };
 
-// 16 RT tokens (blockIdx.y) against 16 columns (blockIdx.x) a workgroup, K divided among its waves.
+using mx::kBatch;
 template <class T, int RT>
 __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx,
                                                          const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restri
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16, m0 = blockIdx.y * (16 * RT);
   const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
-  const Columns w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
+  const Operand w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
   f32x4 acc[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) acc[i] = f32x4{};
@@ -397,7 +398,7 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restri
       eb[k] = w.scale(g);
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        const Columns x(Xq, sx, M, min(m0 + 16 * i + l16, M - 1), q, groups);
+        const Operand x(Xq, sx, M, min(m0 + 16 * i + l16, M - 1), q, groups);
 #pragma unroll
         for (int t = 0; t < 2; ++t) a[i][k][t] = x.block(g, t);
         ea[i][k] = x.scale(g);
@@ -429,8 +430,13 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restri
 }
 
 // The layer for at most MR <= 4 tokens in one launch: every workgroup quantizes the tokens for itself, into LDS, while its
-// first weights are on their way; then as above.
-template <class T, int MR>
+// first weights are on their way; then as above, against 16 columns.  Rows in LDS lie 16 bytes (their scales 4) apart beyond
+// their own length, so that their reads do not meet in one bank.  (16 tokens so: 16 x 4096 x 4096 9.0 us, in two launches 8.1.)
+using mx::kOneLaunch;
+__host__ __device__ constexpr int lds_codes(int groups) { return groups * kStage + 16; }
+__host__ __device__ constexpr int lds_scales(int groups) { return groups * 8 + 4; }
+
+template <class T, int MR, bool VEC>
 __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                            const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
                                                            const uint16_t* __restrict__ bias, int M, int N, int K,
@@ -439,7 +445,7 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
   const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
-  const Columns w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
+  const Operand w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
   i32x4 b[kBatch][2];
   int eb[kBatch];
   auto load = [&](int u) __attribute__((always_inline)) {      // past the range's end: the last group again, not multiplied
@@ -455,22 +461,24 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
   __builtin_amdgcn_sched_barrier(0);
 
   uint8_t* codes = reinterpret_cast<uint8_t*>(shared + waves * 256);
-  uint8_t* scales = codes + MR * groups * kStage;               // [MR][groups * 8]
+  uint8_t* scales = codes + MR * lds_codes(groups);
   const int chunks = groups * 32;                               // of eight elements: whole groups, so whole blocks a wave
+  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
+    u32x4 x[MR];
 #pragma unroll
-  for (int m = 0; m < MR; ++m) {
-    for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-      const u32x4 x = w8a8::load8<false>(X + (int64_t)min(m, M - 1) * ldx, c, K);
+    for (int m = 0; m < MR; ++m) x[m] = w8a8::load8<VEC>(X + (int64_t)min(m, M - 1) * ldx, c, K);
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
       uint32_t byte;
-      const uint32_t code = mx::quantize8<T>(x, byte);
-      *reinterpret_cast<uint32_t*>(codes + m * groups * kStage + 4 * c) = code;
-      if ((c & 3) == 0) scales[m * groups * 8 + (c >> 2)] = (uint8_t)byte;
+      const uint32_t code = mx::quantize8<T>(x[m], byte);
+      *reinterpret_cast<uint32_t*>(codes + m * lds_codes(groups) + 4 * c) = code;
+      if ((c & 3) == 0) scales[m * lds_scales(groups) + (c >> 2)] = (uint8_t)byte;
     }
   }
   __syncthreads();
 
-  const uint8_t* row = codes + min(l16, MR - 1) * groups * kStage + 32 * q;
-  const uint8_t* row_scales = scales + min(l16, MR - 1) * groups * 8 + 2 * q;
+  const uint8_t* row = codes + min(l16, MR - 1) * lds_codes(groups) + 32 * q;
+  const uint8_t* row_scales = scales + min(l16, MR - 1) * lds_scales(groups) + 2 * q;
   f32x4 acc = {};
   for (int u = ua; u < ub; u += kBatch) {
     if (u > ua) load(u);
@@ -497,48 +505,35 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
   }
 }
 
-// The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
-constexpr int kKinds = 5;
-constexpr int kDividedKind = 1;  // the tile size whose plans may divide K
-constexpr int kBM[kKinds] = {16, 64, 128, 256, 256}, kBN[kKinds] = {16, 128, 128, 128, 256};
-
-// Waves of a workgroup that divide K's groups: whole batches, at most 16 waves.
-int rows_waves(int groups) {
-  if (groups <= 4 * kBatch) return 4;
-  int best = 16, least = 1 << 30;
-  for (int w = min(16, max(4, (groups + 7) / 8)); w <= 16; ++w) {
-    const int loaded = w * (((groups + w - 1) / w + kBatch - 1) / kBatch * kBatch);
-    if (loaded < least) {
-      least = loaded;
-      best = w;
-    }
-  }
-  return best;
-}
+using mx::kBM;
+using mx::kBN;
+using mx::kDividedKind;
+using mx::rows_waves;
 
 template <class T>
 void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias, int M, int N,
             int K, uint16_t* Y, float* part, const MxPlan& p, hipStream_t st) {
   const int groups = mx::padded(K) / mx::kGroup;
-  if (p.kind == 0) {
-    const int waves = rows_waves(groups);
-    if (M <= 16)
-      hipLaunchKernelGGL((gemm_rows_kernel<T, 1>), dim3(p.tiles), dim3(64 * waves), waves * 1024, st, Xq, sx, Wq, sw,
-                         bias, M, N, groups, Y);
-    else
-      hipLaunchKernelGGL((gemm_rows_kernel<T, 2>), dim3(p.tiles, (M + 31) / 32), dim3(64 * waves), waves * 2048, st, Xq, sx, Wq, sw,
-                         bias, M, N, groups, Y);
-    return;
+#define ATOM_ROWS(KIND, RT)                                                                                              \
+  if (p.kind == KIND) {                                                                                                  \
+    const int waves = rows_waves(groups);                                                                                \
+    hipLaunchKernelGGL((gemm_rows_kernel<T, RT>), dim3((N + 15) / 16, (M + 16 * RT - 1) / (16 * RT)), dim3(64 * waves),  \
+                       waves * RT * 1024, st, Xq, sx, Wq, sw, bias, M, N, groups, Y);                                    \
+    return;                                                                                                              \
   }
+  ATOM_ROWS(0, 1)
+  ATOM_ROWS(1, 2)
+#undef ATOM_ROWS
   const dim3 grid(p.tiles * p.splits);
 #define ATOM_TILE(KIND, BM, BN, RING, W, E)                                                                             \
   if (p.kind == KIND)                                                                                                \
     hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind, E>), grid, dim3(256), 0, st, Xq, sx, \
                        Wq, sw, bias, M, N, groups, Y, p.tiles, p.splits, part);
-  ATOM_TILE(1, 64, 128, 3, 2, false)
-  ATOM_TILE(2, 128, 128, 2, 2, true)
-  ATOM_TILE(3, 256, 128, 3, 1, false)
-  ATOM_TILE(4, 256, 256, 2, 1, true)
+  ATOM_TILE(2, 64, 64, 3, 3, false)
+  ATOM_TILE(3, 64, 128, 3, 2, false)
+  ATOM_TILE(4, 128, 128, 2, 2, true)
+  ATOM_TILE(5, 256, 128, 3, 1, false)
+  ATOM_TILE(6, 256, 256, 2, 1, true)
 #undef ATOM_TILE
   if (p.splits > 1)
     hipLaunchKernelGGL((finish_kernel<T, kBM[kDividedKind], kBN[kDividedKind]>),
@@ -546,51 +541,20 @@ void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8
                        N, Y, p.tiles, p.splits);
 }
 
-template <class T, int MR>
+template <class T, bool VEC>
 void launch_rows(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias, int M,
                  int N, int K, uint16_t* Y, hipStream_t st) {
-  const int groups = mx::padded(K) / mx::kGroup, waves = rows_waves(groups);
-  hipLaunchKernelGGL((linear_rows_kernel<T, MR>), dim3((N + 15) / 16), dim3(64 * waves),
-                     waves * 1024 + MR * groups * (kStage + 8), st, X, ldx, Wq, sw, bias, M, N, K, groups, Y);
+  const int groups = mx::padded(K) / mx::kGroup, waves = rows_waves(groups), rows = M == 1 ? 1 : kOneLaunch;
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((N + 15) / 16), dim3(64 * waves), waves * 1024 + rows * (lds_codes(groups) + lds_scales(groups)),
+                       st, X, ldx, Wq, sw, bias, M, N, K, groups, Y);
+  };
+  rows == 1 ? go(linear_rows_kernel<T, 1, VEC>) : go(linear_rows_kernel<T, kOneLaunch, VEC>);
 }
 
 }  // namespace
 
-// The plan of a shape: the kernel whose estimated time (us) is least.
-MxPlan mx_plan(int M, int N, int K) {
-  auto tiles = [&](int kind) {
-    return (int)((int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]));
-  };
-  struct Cost {
-    int slots;
-    double full, one, fixed;
-  };
-  constexpr Cost cost[kKinds] = {{}, {2, 5.3, 4.0, 3.0}, {2, 8.1, 6.2, 5.0}, {1, 7.6, 7.6, 7.0}, {1, 13.5, 13.5, 12.0}};
-  const int cus = compute_units(), stages = mx::padded(K) / mx::kGroup;
-  const double bytes = stages * 128.0;
-  MxPlan best = {0, (N + 15) / 16, 1};
-  const int64_t rounds = ((int64_t)best.tiles * (M <= 16 ? 1 : (M + 31) / 32) + cus - 1) / cus;
-  double least = M <= 16 ? 2.9 + rounds * bytes * (M <= 4 ? 0.70e-3 : 0.97e-3) : 2.4 + rounds * (1.0 + 1.45e-3 * bytes);
-  for (int kind = 1; kind < kKinds; ++kind) {
-    const Cost& c = cost[kind];
-    const int t = tiles(kind);
-    for (int splits = 1; splits <= (kind == kDividedKind ? 4 : 1); ++splits) {
-      if (splits > 1 && (stages < 8 * splits || t * splits > cus)) break;
-      const int64_t per = ((int64_t)t * splits + cus - 1) / cus;    // workgroups of the busiest unit
-      const int64_t full = per / c.slots, rest = per % c.slots;
-      const double k = splits == 1 ? bytes : (stages + splits - 1) / splits * 128;
-      const double multiply = 1e-3 * k * (full * c.full + (rest ? c.one : 0.0));
-      const double read = (double)N * bytes / (splits > 1 ? 6e6 : 4.2e6);
-      double time = (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
-      if (splits > 1) time = 1.04 * (time + 2.5 + (double)t * splits * kBM[kind] * kBN[kind] * 8 / 3.3e6);
-      if (time < least) {
-        least = time;
-        best = MxPlan{kind, t, splits};
-      }
-    }
-  }
-  return best;
-}
+MxPlan mx_plan(int M, int N, int K) { return mx::plan(M, N, K, compute_units()); }
 
 int64_t mx_workspace_bytes(const MxPlan& p) {
   return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0;
@@ -606,19 +570,15 @@ hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t
   return hipGetLastError();
 }
 
-bool mx_rows_fits(int M, int N, int K) {
-  const int64_t work = (int64_t)M * K * (((N + 15) / 16 + compute_units() - 1) / compute_units());
-  return M <= 4 && work <= 16384;
-}
-
 hipError_t launch_linear_rows_mxfp4(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
                                     int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream) {
+  const bool vec = K % 8 == 0 && (M == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
   if (bf16)
-    M == 1 ? launch_rows<Bf16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
-           : launch_rows<Bf16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
+    vec ? launch_rows<Bf16, true>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+        : launch_rows<Bf16, false>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
   else
-    M == 1 ? launch_rows<Fp16, 1>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
-           : launch_rows<Fp16, 4>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
+    vec ? launch_rows<Fp16, true>(X, ldx, Wq, sw, bias, M, N, K, Y, stream)
+        : launch_rows<Fp16, false>(X, ldx, Wq, sw, bias, M, N, K, Y, stream);
   return hipGetLastError();
 }
 

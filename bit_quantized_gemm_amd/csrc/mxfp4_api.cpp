@@ -15,6 +15,17 @@ uint64_t row_bytes4(int32_t K) { return groups_of(K) * (ATOM_MX_GROUP / 2); }
 uint64_t code_bytes(int32_t rows, int32_t K) { return (uint64_t)rows * row_bytes4(K); }
 uint64_t scale_bytes(int32_t rows, int32_t K) { return (uint64_t)rows * groups_of(K) * 8; }
 
+// The plan of a valid shape; false where no launch would hold it.
+bool plan_of(int32_t M, int32_t N, int32_t K, atom::MxPlan& plan) {
+  if (!valid_gemm8(M, N, K)) return false;
+  plan = atom::mx_plan(M, N, K);
+  return plan.tiles > 0;
+}
+int64_t linear_bytes(int32_t M, int32_t K, const atom::MxPlan& plan) {
+  if (atom::mx::rows_fit(M, K)) return 0;
+  return (int64_t)(code_bytes(M, K) + up16(scale_bytes(M, K))) + atom::mx_workspace_bytes(plan);
+}
+
 // The checks that both norms share; `codes` and `scales`: bytes of their outputs.
 int check_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* W, double eps, int32_t dtype, int32_t rows,
                int32_t K, const void* H, int64_t ldh, const void* Xq, const void* sx, uint64_t (*codes)(int32_t, int32_t),
@@ -84,17 +95,18 @@ int atom_dequantize_mxfp4(const void* Xq, const void* sx, int32_t rows, int32_t 
 }
 
 int64_t atom_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K) {
-  if (!valid_gemm8(M, N, K)) return -(int64_t)ATOM_E_SHAPE;
-  return atom::mx_workspace_bytes(atom::mx_plan(M, N, K));
+  atom::MxPlan plan;
+  if (!plan_of(M, N, K, plan)) return -(int64_t)ATOM_E_SHAPE;
+  return atom::mx_workspace_bytes(plan);
 }
 
 int atom_gemm_mxfp4(const void* Xq, const void* sx, const void* Wq, const void* sw, const void* bias, int32_t M, int32_t N,
                     int32_t K, int32_t dtype, void* Y, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!Xq || !sx || !Wq || !sw || !Y) return ATOM_E_NULL;
-  if (!valid_gemm8(M, N, K) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  atom::MxPlan plan;
+  if (!plan_of(M, N, K, plan) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
   if (!aligned16(Xq) || !aligned16(sx) || !aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y))
     return ATOM_E_ALIGN;
-  atom::MxPlan plan = atom::mx_plan(M, N, K);
   int64_t need = atom::mx_workspace_bytes(plan);
   if (need > 0 && (!workspace || workspace_bytes < need)) {   // too little scratch: undivided
     plan.splits = 1;
@@ -113,17 +125,18 @@ int atom_gemm_mxfp4(const void* Xq, const void* sx, const void* Wq, const void* 
 }
 
 int64_t atom_linear_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K) {
-  if (!valid_gemm8(M, N, K)) return -(int64_t)ATOM_E_SHAPE;
-  if (atom::mx_rows_fits(M, N, K)) return 0;
-  return (int64_t)(code_bytes(M, K) + up16(scale_bytes(M, K))) + atom::mx_workspace_bytes(atom::mx_plan(M, N, K));
+  atom::MxPlan plan;
+  if (!plan_of(M, N, K, plan)) return -(int64_t)ATOM_E_SHAPE;
+  return linear_bytes(M, K, plan);
 }
 
 int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq, const void* sw, const void* bias, int32_t M,
                       int32_t N, int32_t K, void* Y, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!X || !Wq || !sw || !Y) return ATOM_E_NULL;
-  if (!valid_gemm8(M, N, K) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  atom::MxPlan plan;
+  if (!plan_of(M, N, K, plan) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
   if (!valid_x(X, ldx, M, K)) return aligned(X, 2) ? ATOM_E_SHAPE : ATOM_E_ALIGN;
-  const int64_t need = atom_linear_mxfp4_workspace_bytes(M, N, K);
+  const int64_t need = linear_bytes(M, K, plan);
   if (need > 0 && !workspace) return ATOM_E_NULL;
   if (workspace_bytes < need) return ATOM_E_SHAPE;
   if (!aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y) || (need > 0 && !aligned16(workspace)))
@@ -144,7 +157,7 @@ int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq,
   const hipError_t e = atom::launch_quantize_mxfp4(static_cast<const uint16_t*>(X), ldx, dtype == ATOM_BF16, M, K, xq, sx, st);
   if (e != hipSuccess) return ATOM_E_HIP;
   return hip_status(atom::launch_gemm_mxfp4(xq, sx, wq, ws, static_cast<const uint16_t*>(bias), M, N, K, dtype == ATOM_BF16,
-                                            static_cast<uint16_t*>(Y), part, atom::mx_plan(M, N, K), st));
+                                            static_cast<uint16_t*>(Y), part, plan, st));
 }
 
 int atom_rmsnorm_w8a8(const void* X, int64_t ldx, const void* residual, int64_t ldr, const void* weight, double eps,

@@ -1,0 +1,101 @@
+// How MXFP4 products are run: plain arithmetic on a call's sizes, shared by the host code and by a host test that pins the
+// kernel each shape takes.
+#pragma once
+
+#include <stdint.h>
+
+namespace atom {
+namespace mx {
+
+constexpr int kBatch = 4;        // groups of K whose loads a wave of the few-rows kernels has in flight
+constexpr int kOneLaunch = 4;    // most tokens that one launch quantizes and multiplies
+
+// The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
+constexpr int kRowKinds = 2, kKinds = 7;
+constexpr int kDividedKind = 2;  // the tile size whose plans may divide K
+constexpr int kBM[kKinds] = {16, 32, 64, 64, 128, 256, 256}, kBN[kKinds] = {16, 16, 64, 128, 128, 128, 256};
+
+// Waves of a few-rows workgroup, which divide K's groups: as few turns of whole batches as possible, then as little behind
+// the ranges' ends.  (1 x 4096 x 4096, 16 groups: 4 waves 4.9 us, 8 5.3, 16 6.8; 1 x 4096 x 11008, 43 groups: 4 11.5, 8 9.7, 11 7.9.)
+inline int rows_waves(int groups) {
+  int best = 4, turns = 1 << 30, loaded = 1 << 30;
+  for (int w = 4; w <= 16; ++w) {
+    const int t = ((groups + w - 1) / w + kBatch - 1) / kBatch;
+    if (t < turns || (t == turns && w * t * kBatch < loaded)) {
+      best = w;
+      turns = t;
+      loaded = w * t * kBatch;
+    }
+  }
+  return best;
+}
+
+// `tiles` workgroups; `splits` of them divide K for each output tile (their fp32 parts are added by a second kernel).
+struct Plan {
+  int kind, tiles, splits;
+};
+
+// The plan of a shape: the kernel whose estimated time (us) is least.
+//   Few rows: a start, and for each 16 columns of a compute unit a rate for K's groups and its end.
+//   Tiles: a round of the grid takes `fixed` us (first stages, epilogue) and `full` us for each group of K when every unit
+//     holds `slots` workgroups, `one` us when it holds one; reading the weights sets a floor (`read` bytes a us).
+//   64 x 64 tiles with K divided two to four ways, at least four groups each: the second kernel's 2.3 us and the parts' way
+//     through memory on top.
+// Fitted on 256 units to 137 shapes of products alone (1 to 4096 rows, 64 to 28672 columns, K 256 to 11008, weights that come from
+// HBM): the choice is 1.7% slower than the best kernel on average, over 10% on six.  Measured (us), few rows and the tiles from
+// 64 x 64 up (M x N x K): 16 x 4096 x 4096 5.0, 10.5, 12.5, 13.6, 17.4, 25.4; 16 x 28672 x 8192 37, 28, 30, 31, 39, 48; 32 x 4096 x 4096
+// 7.0 (16 rows at a time), 6.3 (32), 10.7, 12.8, 13.9; 256 x 11008 x 4096 18.6, 19.3, 17.0, 21.8, 32 (tiles); 1024 x 11008 x 4096 56, 47, 38, 43, 35;
+// 2048 x 4096 x 11008 97, 76, 57, 53, 72; 4096 x 28672 x 8192 925, 760, 537, 535, 449.  64 x 4096 x 11008 whole, two, three and four ways 24.7,
+// 17.9, 16.3 and 15.6; 777 x 777 x 8192 21.3, 17, 15.7 and 17.
+inline Plan plan(int M, int N, int K, int cus) {
+  auto tiles = [&](int kind) {
+    return (int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]);
+  };
+  struct Rows {
+    double start, group, end;
+  };
+  constexpr Rows rows[kRowKinds] = {{2.1, 0.118, 0.515}, {1.6, 0.155, 1.4}};
+  struct Cost {
+    int slots;
+    double full, one, fixed, read;
+  };
+  constexpr Cost cost[kKinds] = {{}, {}, {3, 0.91, 0.38, 2.8, 3.6e6}, {2, 0.88, 0.55, 3.3, 4.6e6}, {2, 1.25, 0.70, 4.1, 4.5e6},
+                                 {1, 0.90, 0.90, 6.8, 3.4e6}, {1, 1.45, 1.45, 12.8, 5.7e6}};
+  const int groups = (K + 255) / 256;
+  Plan best = {0, 0, 1};
+  double least = -1.0;
+  // (a launch has less than 2^32 threads, and at most 65535 workgroups in y)
+  auto offer = [&](int kind, int64_t t, int splits, double time) {
+    if ((least >= 0.0 && time >= least) || t * splits * (kind < kRowKinds ? 1024 : 256) >= (int64_t)1 << 32) return;
+    if (kind < kRowKinds && M > 65535 * kBM[kind]) return;
+    least = time;
+    best = Plan{kind, (int)t, splits};
+  };
+  for (int kind = 0; kind < kRowKinds; ++kind) {
+    const double per = (double)tiles(kind) / cus, r = per > 1.0 ? per : 1.0;
+    offer(kind, tiles(kind), 1, rows[kind].start + r * (groups * rows[kind].group + rows[kind].end));
+  }
+  for (int kind = kRowKinds; kind < kKinds; ++kind) {
+    const Cost& c = cost[kind];
+    const int64_t t = tiles(kind);
+    for (int splits = 1; splits <= (kind == kDividedKind ? 4 : 1); ++splits) {
+      if (splits > 1 && (groups < 4 * splits || t * splits > c.slots * cus)) break;
+      const int64_t per = (t * splits + cus - 1) / cus;    // workgroups of the busiest unit
+      const int64_t full = per / c.slots, rest = per % c.slots;
+      const double part = rest ? c.one + (c.full - c.one) * (rest - 1) / (c.slots > 1 ? c.slots - 1 : 1) : 0.0;
+      const double multiply = (groups + splits - 1) / splits * (full * c.full + part);
+      const double read = (double)N * groups * 136 / (splits > 1 ? 5.6e6 : c.read);
+      double time = 0.3 + (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
+      if (splits > 1) time += 2.3 + (double)t * splits * kBM[kind] * kBN[kind] * 8 / 4.0e6;
+      offer(kind, t, splits, time);
+    }
+  }
+  return best;
+}
+
+// One launch or two (us, M x N x K): 1 x 4096 x 4096 4.9 and 6.5, 1 x 28672 x 8192 25 and 33, 1 x 8192 x 28672 27 and 30; 4 x 11008 x 4096 9.5
+// and 10.5, 4 x 8192 x 8192 12.5 and 12.4, 2 x 8192 x 16384 21.6 and 20.4, 4 x 8192 x 16384 22.8 and 21.2.
+inline bool rows_fit(int M, int K) { return M == 1 || (M <= kOneLaunch && (int64_t)M * K <= 32768); }
+
+}  // namespace mx
+}  // namespace atom

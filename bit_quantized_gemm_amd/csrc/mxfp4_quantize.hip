@@ -14,21 +14,21 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 16;                               // rows of a workgroup: a line of scales
 
-// Workgroup (x, y): rows kRows x .., the 64-lane spans 512 y .. + 511 of K.
-template <class T, bool VEC>
+// Workgroup (x, y): rows ROWS x .., the 64-lane span 512 y .. + 511 of K.
+template <class T, bool VEC, int ROWS>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx, int rows, int K,
                                                             int Kp, uint8_t* __restrict__ Xq, uint8_t* __restrict__ sx) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.y * 64 + lane;                 // the lane's chunk of eight elements in every row
-  u32x4 w[kRows / 4];
+  u32x4 w[ROWS / 4];
 #pragma unroll
-  for (int i = 0; i < kRows / 4; ++i) {
-    const int row = blockIdx.x * kRows + 4 * i + wave;
+  for (int i = 0; i < ROWS / 4; ++i) {
+    const int row = blockIdx.x * ROWS + 4 * i + wave;
     w[i] = w8a8::load8<VEC>(X + (int64_t)min(row, rows - 1) * ldx, c, K);
   }
 #pragma unroll
-  for (int i = 0; i < kRows / 4; ++i) {
-    const int row = blockIdx.x * kRows + 4 * i + wave;
+  for (int i = 0; i < ROWS / 4; ++i) {
+    const int row = blockIdx.x * ROWS + 4 * i + wave;
     uint32_t byte;
     const uint32_t code = mx::quantize8<T>(w[i], byte);
     const uint32_t four = mx::gather_scales(byte, lane);
@@ -40,25 +40,29 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __re
   }
 }
 
-// One thread per eight elements of a row.
-template <class T, bool VEC>
+// One thread per eight elements of each of ROWS / 4 rows.
+template <class T, bool VEC, int ROWS>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx,
                                                               int rows, int K, int Kp, uint16_t* __restrict__ X) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.y * 64 + lane;
+  const int c = blockIdx.y * 64 + (threadIdx.x & 63), wave = threadIdx.x >> 6;
   if (8 * c >= K) return;
+  uint32_t code[ROWS / 4], byte[ROWS / 4];
 #pragma unroll
-  for (int i = 0; i < kRows / 4; ++i) {
-    const int row = blockIdx.x * kRows + 4 * i + wave;
+  for (int i = 0; i < ROWS / 4; ++i) {
+    const int64_t row = min((int)blockIdx.x * ROWS + 4 * i + wave, rows - 1);
+    code[i] = *reinterpret_cast<const uint32_t*>(Xq + row * (Kp / 2) + 4 * c);
+    byte[i] = sx[((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 2) & 7)];
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS / 4; ++i) {
+    const int row = blockIdx.x * ROWS + 4 * i + wave;
     if (row >= rows) return;
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(Xq + (int64_t)row * (Kp / 2) + 4 * c);
-    const uint32_t byte = sx[((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 2) & 7)];
     // 2^e; 2^-127 is one of fp32's subnormal numbers, and all products with a code are exact
-    const float scale = __builtin_bit_cast(float, byte == mx::kNanScale ? 0x7FC00000u : byte ? byte << 23 : 0x00400000u);
+    const float scale = __builtin_bit_cast(float, byte[i] == mx::kNanScale ? 0x7FC00000u : byte[i] ? byte[i] << 23 : 0x00400000u);
     float v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t q = code >> (4 * j), m = q & 7;
+      const uint32_t q = code[i] >> (4 * j), m = q & 7;
       // 0, 0.5, 1, 1.5 in halves, then 1 or 1.5 times 2 and 4
       const float a = m < 4 ? 0.5f * (float)m : (float)(2 + (m & 1)) * (m < 6 ? 1.0f : 2.0f);
       v[j] = (q & 8 ? -a : a) * scale;
@@ -75,20 +79,26 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
   }
 }
 
-dim3 grid_of(int rows, int Kp) { return dim3((rows + kRows - 1) / kRows, (Kp + 511) / 512); }
+// Rows of a workgroup: a whole line of scales once there are workgroups enough for it.  (us, 4 and 16 rows: quantize
+// 16 x 4096 1.9 and 2.3, 333 x 1155 2.4 and 4.3; back 16 x 4096 2.0 and 3.3, 8192 x 8192 49 and 38.)
+bool whole_lines(int rows, int Kp) { return (int64_t)((rows + kRows - 1) / kRows) * ((Kp + 511) / 512) >= 2048; }
 
 }  // namespace
 
-// (rows <= 2^24 and Kp <= 2^16: at most 2^20 x 2^7 workgroups of 2^8 threads, so 2^28 threads in x.)
+// (rows <= 2^24: at most 2^22 workgroups of 2^8 threads in x.)
 hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int rows, int K, uint8_t* Xq, uint8_t* sx,
                                  hipStream_t stream) {
   const int Kp = mx::padded(K);
   const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid_of(rows, Kp), dim3(kThreads), 0, stream, X, ldx, rows, K, Kp, Xq, sx);
+  auto go = [&](auto kernel, int per) {
+    hipLaunchKernelGGL(kernel, dim3((rows + per - 1) / per, (Kp + 511) / 512), dim3(kThreads), 0, stream, X, ldx, rows, K, Kp, Xq, sx);
   };
-  if (bf16) vec ? go(quantize_kernel<Bf16, true>) : go(quantize_kernel<Bf16, false>);
-  else vec ? go(quantize_kernel<Fp16, true>) : go(quantize_kernel<Fp16, false>);
+  auto pick = [&](auto type) {
+    using T = decltype(type);
+    if (whole_lines(rows, Kp)) vec ? go(quantize_kernel<T, true, kRows>, kRows) : go(quantize_kernel<T, false, kRows>, kRows);
+    else vec ? go(quantize_kernel<T, true, 4>, 4) : go(quantize_kernel<T, false, 4>, 4);
+  };
+  bf16 ? pick(Bf16{}) : pick(Fp16{});
   return hipGetLastError();
 }
 
@@ -96,11 +106,15 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int row
                                    hipStream_t stream) {
   const int Kp = mx::padded(K);
   const bool vec = K % 8 == 0;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid_of(rows, Kp), dim3(kThreads), 0, stream, Xq, sx, rows, K, Kp, X);
+  auto go = [&](auto kernel, int per) {
+    hipLaunchKernelGGL(kernel, dim3((rows + per - 1) / per, (Kp + 511) / 512), dim3(kThreads), 0, stream, Xq, sx, rows, K, Kp, X);
   };
-  if (bf16) vec ? go(dequantize_kernel<Bf16, true>) : go(dequantize_kernel<Bf16, false>);
-  else vec ? go(dequantize_kernel<Fp16, true>) : go(dequantize_kernel<Fp16, false>);
+  auto pick = [&](auto type) {
+    using T = decltype(type);
+    if (whole_lines(rows, Kp)) vec ? go(dequantize_kernel<T, true, kRows>, kRows) : go(dequantize_kernel<T, false, kRows>, kRows);
+    else vec ? go(dequantize_kernel<T, true, 4>, 4) : go(dequantize_kernel<T, false, 4>, 4);
+  };
+  bf16 ? pick(Bf16{}) : pick(Fp16{});
   return hipGetLastError();
 }
 

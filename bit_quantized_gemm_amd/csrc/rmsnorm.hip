@@ -25,6 +25,31 @@ struct Norm {
   void* sx;
 };
 
+// v of the lane that CTRL names, within rows of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)mx::dpp<CTRL>((uint32_t)(b >> 32)) << 32 | mx::dpp<CTRL>((uint32_t)b));
+}
+// Sum and maximum over a wave, in every lane: lane ^ 1, ^ 2, 7 - lane of 8, 15 - lane of 16, then across rows.
+__device__ __forceinline__ double wave_sum(double v) {
+  v += moved<0xB1>(v);
+  v += moved<0x4E>(v);
+  v += moved<0x141>(v);
+  v += moved<0x140>(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ float wave_top(float v) {
+  uint32_t b = __builtin_bit_cast(uint32_t, v);          // not negative: the order of the bits
+  b = max(b, mx::dpp<0xB1>(b));
+  b = max(b, mx::dpp<0x4E>(b));
+  b = max(b, mx::dpp<0x141>(b));
+  b = max(b, mx::dpp<0x140>(b));
+  b = max(b, (uint32_t)__shfl_xor((int)b, 16));
+  return __builtin_bit_cast(float, max(b, (uint32_t)__shfl_xor((int)b, 32)));
+}
+
 // Code of one value in fp64 units of its scale: nearest, ties to the even code, saturating.
 __device__ __forceinline__ uint32_t fp4_code(double y) {
   const double a = __builtin_fabs(y);
@@ -45,16 +70,20 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
 #pragma unroll
   for (int i = 0; i < CH; ++i) h[i] = w8a8::load8<VEC>(x, t + i * THREADS, a.K);
   if (a.R) {
-    const uint16_t* r = a.R + (size_t)row * a.ldr;
+    const uint16_t* from = a.R + (size_t)row * a.ldr;
     uint16_t* dst = a.H + (size_t)row * a.ldh;
+    u32x4 r[CH];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(r, t + i * THREADS, a.K);
+    for (int i = 0; i < CH; ++i) r[i] = w8a8::load8<VEC>(from, t + i * THREADS, a.K);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(a.W, t + i * THREADS, a.K);
+    __builtin_amdgcn_sched_barrier(0);                  // all loads are on their way before the first sum
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * THREADS;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float lo = elem<T>(h[i][j], 0) + elem<T>(w[i][j], 0), hi = elem<T>(h[i][j], 1) + elem<T>(w[i][j], 1);
+        float lo = elem<T>(h[i][j], 0) + elem<T>(r[i][j], 0), hi = elem<T>(h[i][j], 1) + elem<T>(r[i][j], 1);
         asm("" : "+v"(lo), "+v"(hi));                   // two roundings, as two steps have them: never one fused one
         h[i][j] = pack2<T>(lo, hi);
       }
@@ -66,9 +95,10 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
           if (8 * c + j < a.K) dst[8 * c + j] = (uint16_t)(h[i][j / 2] >> (16 * (j & 1)));
       }
     }
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(a.W, t + i * THREADS, a.K);
+    for (int i = 0; i < CH; ++i) w[i] = w8a8::load8<VEC>(a.W, t + i * THREADS, a.K);
+  }
 
   double sum[2] = {};
   float top = 0.0f;                                     // largest |p| (int8: the row's scale)
@@ -80,25 +110,21 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       sum[j & 1] = __builtin_fma((double)v, (double)v, sum[j & 1]);
       if (!MX) top = __builtin_fmaxf(top, __builtin_fabsf(v * elem<T>(w[i][j / 2], j & 1)));
     }
-  double total = sum[0] + sum[1];
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    total += __shfl_xor(total, d);
-    if (!MX) top = __builtin_fmaxf(top, __shfl_xor(top, d));
-  }
+  double total = wave_sum(sum[0] + sum[1]);
+  if (!MX) top = wave_top(top);
   if constexpr (THREADS > 64) {
-    __shared__ double wave_sum[THREADS / 64];
-    __shared__ float wave_top[THREADS / 64];
+    __shared__ double sums[THREADS / 64];
+    __shared__ float tops[THREADS / 64];
     if (lane == 0) {
-      wave_sum[threadIdx.x >> 6] = total;
-      wave_top[threadIdx.x >> 6] = top;
+      sums[threadIdx.x >> 6] = total;
+      tops[threadIdx.x >> 6] = top;
     }
     __syncthreads();
     total = 0.0;
 #pragma unroll
     for (int i = 0; i < THREADS / 64; ++i) {            // the same order in every wave
-      total += wave_sum[i];
-      if (!MX) top = __builtin_fmaxf(top, wave_top[i]);
+      total += sums[i];
+      if (!MX) top = __builtin_fmaxf(top, tops[i]);
     }
   }
   const double rstd = 1.0 / __builtin_sqrt(total * a.inv_k + a.eps);

@@ -12,6 +12,7 @@
 #include "atom_norm.h"
 #include "atom_w8a8.h"
 #include "kv4_plan.h"
+#include "mxfp4_plan.h"
 
 namespace atom {
 
@@ -77,16 +78,12 @@ hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int 
                                  hipStream_t stream);
 hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int rows, int K, bool bf16, uint16_t* X,
                                    hipStream_t stream);
-// As W8Plan; the parts of a divided product are fp32.
-struct MxPlan {
-  int kind, tiles, splits;
-};
-MxPlan mx_plan(int M, int N, int K);
+using MxPlan = mx::Plan;
+MxPlan mx_plan(int M, int N, int K);                     // for this device's compute units
 int64_t mx_workspace_bytes(const MxPlan& plan);
 hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
                              int M, int N, int K, bool bf16, uint16_t* Y, float* part, const MxPlan& plan,
                              hipStream_t stream);
-bool mx_rows_fits(int M, int N, int K);
 hipError_t launch_linear_rows_mxfp4(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
                                     int M, int N, int K, bool bf16, uint16_t* Y, hipStream_t stream);
 

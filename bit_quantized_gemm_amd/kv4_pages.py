@@ -55,11 +55,6 @@ def _pool(pool):
     return free, state
 
 
-def _fast(d, i32, *tensors):
-    """Whether these are contiguous int32 tensors on device d."""
-    return all(t.dtype is i32 and t.is_contiguous() and t.get_device() == d for t in tensors)
-
-
 def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=None, lens_out=None, state_out=None, stream=None):
     """Admit new[b] tokens (int32 [batch]) to each sequence of lens[b] (int32 [batch]): pages of `page` tokens are taken from the
     pool where none of the sequence's holds them yet, and written into its row of `table` (int32 [batch, width]).
@@ -78,11 +73,15 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
             and table.dim() == 2 and total > 0):
         d = fast_device(lens)
         batch, width = table.shape
-        if (d >= 0 and lens.shape == new.shape == (batch,) and state.shape == (2,) and _fast(d, i32, lens, new, table, free, state)):
+        if (d >= 0 and lens.shape == new.shape == (batch,) and state.shape == (2,)
+                and lens.dtype is i32 and new.dtype is i32 and table.dtype is i32 and free.dtype is i32 and state.dtype is i32
+                and lens.is_contiguous() and new.is_contiguous() and table.is_contiguous() and free.is_contiguous()
+                and state.is_contiguous() and new.get_device() == d and table.get_device() == d and free.get_device() == d
+                and state.get_device() == d):
             device = lens.device
             slots = torch.empty(total, dtype=torch.int64, device=device)
             q_start = torch.empty(batch + 1, dtype=i32, device=device)
-            lens_out, state_out = torch.empty(batch, dtype=i32, device=device), torch.empty(2, dtype=i32, device=device)
+            lens_out, state_out = torch.empty_like(lens), torch.empty_like(state)
             status = _bq.load_library().atom_kv4_extend(
                 lens.data_ptr(), new.data_ptr(), table.data_ptr(), batch, width, page, free.data_ptr(), free.shape[0],
                 state.data_ptr(), slots.data_ptr(), total, q_start.data_ptr(), lens_out.data_ptr(), state_out.data_ptr(),
@@ -121,9 +120,11 @@ def atom_kv4_release(done, lens, table, pool, page, lens_out=None, state_out=Non
         d = fast_device(lens)
         batch, width = table.shape
         if (d >= 0 and done.dtype is torch.bool and done.is_contiguous() and done.get_device() == d
-                and lens.shape == done.shape == (batch,) and state.shape == (2,) and _fast(d, i32, lens, table, free, state)):
-            lens_out = torch.empty(batch, dtype=i32, device=lens.device)
-            state_out = torch.empty(2, dtype=i32, device=lens.device)
+                and lens.shape == done.shape == (batch,) and state.shape == (2,)
+                and lens.dtype is i32 and table.dtype is i32 and free.dtype is i32 and state.dtype is i32
+                and lens.is_contiguous() and table.is_contiguous() and free.is_contiguous() and state.is_contiguous()
+                and table.get_device() == d and free.get_device() == d and state.get_device() == d):
+            lens_out, state_out = torch.empty_like(lens), torch.empty_like(state)
             status = _bq.load_library().atom_kv4_release(
                 done.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, width, page, free.data_ptr(), free.shape[0],
                 state.data_ptr(), lens_out.data_ptr(), state_out.data_ptr(), torch._C._cuda_getCurrentRawStream(d))

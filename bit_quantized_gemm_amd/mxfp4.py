@@ -73,11 +73,24 @@ _linear_bytes = functools.lru_cache(maxsize=1024)(atom_linear_mxfp4_workspace_by
 def atom_quantize_mxfp4(X, Xq=None, sx=None, stream=None):
     """Codes and scales of the rows of X (fp16 / bf16 [rows, K]; rows may lie apart)."""
     torch = _bq._torch()
+    u8 = torch.uint8
+    if stream is None and Xq is None and sx is None and type(X) is torch.Tensor and X.is_cuda and X.dim() == 2:
+        d, t = fast_device(X), X.dtype
+        rows, K = X.shape
+        ldx, step = X.stride()
+        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and rows and 1 <= K <= _bq.MAX_K and (step == 1 or K == 1)
+                and (ldx >= K or rows == 1)):
+            g, device = K + 255 >> 8, X.device
+            Xq, sx = torch.empty((rows, g * 128), dtype=u8, device=device), torch.empty((g, rows, 8), dtype=u8, device=device)
+            status = _bq.load_library().atom_quantize_mxfp4(X.data_ptr(), ldx, int(t is torch.bfloat16), rows, K, Xq.data_ptr(),
+                                                            sx.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if status:
+                _bq._check(status, "atom_quantize_mxfp4")
+            return Xq, sx
     rows, K = _bq._mat(X, "X")
     kind = float_type(X, "X")
     rb, g = packed(K)
     ldx = check_rows(X, "X", (rows, K))
-    u8 = torch.uint8
     if Xq is None:
         Xq = empty((rows, rb), u8, X, stream)
     if sx is None:
@@ -95,6 +108,20 @@ def atom_quantize_mxfp4(X, Xq=None, sx=None, stream=None):
 def atom_dequantize_mxfp4(Xq, sx, K, dtype=None, X=None, stream=None):
     """X [rows, K] that packed rows stand for, in `dtype` (default fp16, or X's)."""
     torch = _bq._torch()
+    T, u8 = torch.Tensor, torch.uint8
+    if stream is None and X is None and type(Xq) is T and type(sx) is T and Xq.is_cuda and type(K) is int:
+        d, qs = fast_device(Xq), Xq.shape
+        t = torch.float16 if dtype is None else dtype
+        g = K + 255 >> 8
+        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and 1 <= K <= _bq.MAX_K and len(qs) == 2 and qs[0]
+                and qs[1] == g * 128 and Xq.dtype is u8 and Xq.is_contiguous() and sx.dtype is u8
+                and sx.shape == (g, qs[0], 8) and sx.is_contiguous() and sx.get_device() == d):
+            X = torch.empty((qs[0], K), dtype=t, device=Xq.device)
+            status = _bq.load_library().atom_dequantize_mxfp4(Xq.data_ptr(), sx.data_ptr(), qs[0], K, int(t is torch.bfloat16),
+                                                              X.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if status:
+                _bq._check(status, "atom_dequantize_mxfp4")
+            return X
     K = int(K)
     rb, g = packed(K)
     rows, _ = _bq._mat(Xq, "Xq")
@@ -103,7 +130,6 @@ def atom_dequantize_mxfp4(Xq, sx, K, dtype=None, X=None, stream=None):
         raise _bq.AtomError(f"dtype must be torch.float16 or torch.bfloat16 (got {dtype})")
     if X is None:
         X = empty((rows, K), dtype, Xq, stream)
-    u8 = torch.uint8
     pQ, pS, pX = _bq._ptrs((Xq, "Xq", u8, (rows, rb)), (sx, "sx", u8, (g, rows, 8)), (X, "X", dtype, (rows, K)))
     with on_device(Xq):
         _bq._check(_bq.load_library().atom_dequantize_mxfp4(pQ, pS, rows, K, int(dtype is torch.bfloat16), pX,

@@ -28,39 +28,44 @@ def signatures():
     return {name: (ctypes.c_int, args) for name in EXPORTS}
 
 
-def _fast(t, dtype, rows, K, d):
-    """The row distance of well-formed rows on device d, else 0."""
-    if type(t) is not _bq._torch().Tensor or t.dtype is not dtype or t.shape != (rows, K) or t.get_device() != d:
-        return 0
-    ld, step = t.stride()
-    return 0 if step != 1 and K != 1 else ld if rows > 1 and ld >= K else K if rows == 1 else 0
-
-
-def _rmsnorm(name, shapes, X, weight, eps, residual, H, Xq, sx, stream):
+def _rmsnorm(name, mx, X, weight, eps, residual, H, Xq, sx, stream):
     torch = _bq._torch()
-    call = getattr(_bq.load_library(), name)
-    if stream is None and H is None and Xq is None and sx is None and type(X) is torch.Tensor and X.is_cuda and X.dim() == 2:
-        d, t = fast_device(X), X.dtype
-        rows, K = X.shape
-        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and rows and 1 <= K <= _bq.MAX_K
-                and type(weight) is torch.Tensor and weight.dtype is t and weight.shape == (K,) and weight.is_contiguous()
-                and weight.get_device() == d):
-            ldx = _fast(X, t, rows, K, d)
-            ldr = _fast(residual, t, rows, K, d) if residual is not None else K
-            if ldx and ldr:
-                (qs, qt), (ss, st) = shapes(rows, K)
-                Xq, sx = torch.empty(qs, dtype=qt, device=X.device), torch.empty(ss, dtype=st, device=X.device)
-                if residual is not None:
-                    H = torch.empty((rows, K), dtype=t, device=X.device)
-                status = call(X.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, weight.data_ptr(),
-                              float(eps), int(t is torch.bfloat16), rows, K, None if H is None else H.data_ptr(), K,
-                              Xq.data_ptr(), sx.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-                if status:
-                    _bq._check(status, name)
-                return Xq, sx, H
+    T = torch.Tensor
+    if (stream is None and H is None and Xq is None and sx is None and type(X) is T and type(weight) is T and X.is_cuda
+            and X.dim() == 2):
+        d, t, xs = fast_device(X), X.dtype, X.shape
+        rows, K = xs
+        ldx, step = X.stride()
+        ok = (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and rows and 1 <= K <= _bq.MAX_K and (step == 1 or K == 1)
+              and (ldx >= K or rows == 1) and weight.dtype is t and weight.shape == (K,) and weight.is_contiguous()
+              and weight.get_device() == d)
+        ldr = K
+        if ok and residual is not None:
+            ok = type(residual) is T and residual.dtype is t and residual.shape == xs and residual.get_device() == d
+            if ok:
+                ldr, step = residual.stride()
+                ok = (step == 1 or K == 1) and (ldr >= K or rows == 1)
+        if ok:
+            device, pR, pH = X.device, None, None
+            if mx:
+                g = K + 255 >> 8
+                Xq = torch.empty((rows, g * 128), dtype=torch.uint8, device=device)
+                sx = torch.empty((g, rows, 8), dtype=torch.uint8, device=device)
+            else:
+                Xq = torch.empty((rows, K + 127 & -128), dtype=torch.int8, device=device)
+                sx = torch.empty((rows,), dtype=torch.float32, device=device)
+            if residual is not None:
+                H = torch.empty((rows, K), dtype=t, device=device)
+                pR, pH = residual.data_ptr(), H.data_ptr()
+            status = getattr(_bq.load_library(), name)(
+                X.data_ptr(), ldx, pR, ldr, weight.data_ptr(), float(eps), int(t is torch.bfloat16), rows, K, pH, K,
+                Xq.data_ptr(), sx.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
+            if status:
+                _bq._check(status, name)
+            return Xq, sx, H
     rows, K = _bq._mat(X, "X")
     kind = float_type(X, "X")
-    (qs, qt), (ss, st) = shapes(rows, K)
+    (qs, qt), (ss, st) = (_mx if mx else _w8)(rows, K)
     ldx = check_rows(X, "X", (rows, K))
     if residual is None and H is not None:
         raise _bq.AtomError("H must be None without a residual")
@@ -83,6 +88,7 @@ def _rmsnorm(name, shapes, X, weight, eps, residual, H, Xq, sx, stream):
             if t.get_device() != Xq.get_device():
                 raise _bq.AtomError(f"{n} is on {t.device}, the other operands on {Xq.device}")
     with on_device(X):
+        call = getattr(_bq.load_library(), name)
         _bq._check(call(X.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, pW, float(eps), kind, rows, K,
                         None if H is None else H.data_ptr(), ldh, pQ, pS, _bq._stream(stream, X.device)), name)
     return Xq, sx, H
@@ -103,9 +109,9 @@ def atom_rmsnorm_w8a8(X, weight, eps=1e-6, residual=None, H=None, Xq=None, sx=No
     """The rows of X (fp16 / bf16 [rows, K]; rows may lie apart), plus `residual` if one is given, normed and quantized to
     int8: (Xq int8 [rows, row bytes], sx fp32 [rows], H).  H, the sum in X's type, is what the next layer's residual is;
     it may be given as the residual (or X) itself, which is then replaced."""
-    return _rmsnorm("atom_rmsnorm_w8a8", _w8, X, weight, eps, residual, H, Xq, sx, stream)
+    return _rmsnorm("atom_rmsnorm_w8a8", False, X, weight, eps, residual, H, Xq, sx, stream)
 
 
 def atom_rmsnorm_mxfp4(X, weight, eps=1e-6, residual=None, H=None, Xq=None, sx=None, stream=None):
     """As ``atom_rmsnorm_w8a8``, quantized to MXFP4: (Xq uint8 [rows, row bytes], sx uint8 [groups, rows, 8], H)."""
-    return _rmsnorm("atom_rmsnorm_mxfp4", _mx, X, weight, eps, residual, H, Xq, sx, stream)
+    return _rmsnorm("atom_rmsnorm_mxfp4", True, X, weight, eps, residual, H, Xq, sx, stream)

@@ -86,10 +86,10 @@ def test_gemm_and_linear_validation(lib):
     for n, p in (("xq", A), ("sx", B), ("wq", C), ("sw", D), ("y", E), ("bias", F)):
         assert g(**{n: p + 4}) == E_ALIGN
     assert g(y=A + 16) == g(y=C + 1008) == g(y=D + 48) == g(bias=F, y=F) == E_OVERLAP
-    need = bq.atom_gemm_mxfp4_workspace_bytes(64, 128, 16384)
+    need = bq.atom_gemm_mxfp4_workspace_bytes(64, 4096, 11008)
     assert need > 0
-    assert g(m=64, n=128, k=16384, ws=F + 4, nws=need) == E_ALIGN
-    assert g(m=64, n=128, k=16384, ws=E, nws=need) == E_OVERLAP
+    assert g(m=64, n=4096, k=11008, ws=F + 4, nws=need) == E_ALIGN
+    assert g(m=64, n=4096, k=11008, ws=E, nws=need) == E_OVERLAP
     assert lib.atom_gemm_mxfp4_workspace_bytes(0, 4, 4) == lib.atom_linear_mxfp4_workspace_bytes(4, 0, 4) == -E_SHAPE
     assert bq.atom_linear_mxfp4_workspace_bytes(4, 4, 256) == 0          # one launch: nothing to keep
     need = bq.atom_linear_mxfp4_workspace_bytes(8, 4, 256)

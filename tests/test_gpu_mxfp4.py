@@ -144,7 +144,13 @@ def test_inf_and_nan(dtype):
 SHAPES = [(1, 1, 1), (1, 17, 300), (1, 4096, 4096), (3, 130, 127), (16, 100, 11008), (17, 33, 1000), (32, 1000, 513),
           (33, 64, 128), (33, 65, 4096), (33, 65, 6145), (127, 1000, 5000), (300, 300, 300), (4000, 31, 1000), (64, 128, 2048),
           (65, 127, 4100), (100, 260, 65536), (128, 4096, 1024), (333, 777, 1155), (257, 4097, 300), (512, 8192, 256),
-          (1024, 4100, 384), (4000, 4104, 200), (2304, 11008, 130), (1100, 4100, 700), (2304, 4200, 1000), (64, 4096, 8192)]
+          (1024, 4100, 384), (4000, 4104, 200), (2304, 11008, 130), (1100, 4100, 700), (2304, 4200, 1000), (64, 4096, 8192),
+          (201, 16403, 2300), (501, 16403, 2600), (1000, 10900, 4000), (777, 777, 7000), (100, 4096, 6000), (300, 777, 4100)]
+
+# every position at which K can end in the rings of stage buffers, for each tile size (M, N, groups of K)
+RINGS = ([(131, 1003, g) for g in range(1, 14)] + [(131, 16403, g) for g in range(1, 6)] + [(131, 6003, g) for g in range(6, 14)] +
+         [(201, 16403, g) for g in range(1, 5)] + [(333, 8203, 5), (333, 8203, 6)] + [(131, 11003, g) for g in range(7, 12)] +
+         [(201, 16403, g) for g in range(8, 15)] + [(701, 16403, g) for g in range(5, 10)] + [(501, 16403, g) for g in range(10, 14)])
 
 
 @pytest.mark.parametrize("bias", [False, True])
@@ -184,7 +190,7 @@ def codes(rows, K, seed, lo=126, hi=128):
     return torch.from_numpy(q).cuda(), torch.from_numpy(s3).cuda()
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + [(m, n, 256 * g - 5) for m, n, g in RINGS])
 def test_exact_sums(M, N, K):
     """Codes of every kind with scales 1/2, 1 and 2: products are multiples of 2^-4 and the sums of their magnitudes stay below
     2^20, so every step of fp32 is exact, in every kernel and division, and Y is the sum rounded once."""
