@@ -58,6 +58,7 @@ EXPORTS = (
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
+_SHORT = None        # the extension module `_short` (csrc/short_calls.cpp), bound to _LIB; None: every call takes the full checks
 
 
 class AtomError(RuntimeError):
@@ -70,7 +71,7 @@ def lib_path() -> str:
 
 def load_library():
     """Load libatom.so (once) and declare the C signatures."""
-    global _LIB
+    global _LIB, _SHORT
     if _LIB is not None:
         return _LIB
     path = lib_path()
@@ -110,7 +111,19 @@ def load_library():
         fn.restype = res
         fn.argtypes = args
     _LIB = lib
+    _SHORT = _bind_short(lib, sig)
     return lib
+
+
+def _bind_short(lib, names):
+    """The extension module with the library's addresses, or None where it is not built."""
+    try:
+        stream = _torch()._C._cuda_getCurrentRawStream
+        from . import _short
+    except (ImportError, AttributeError):
+        return None
+    _short.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, stream)
+    return _short
 
 
 def atom_row_bytes(K: int) -> int:

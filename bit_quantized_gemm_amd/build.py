@@ -1,7 +1,8 @@
-"""Build libatom.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build libatom.so (the C-ABI library) for gfx950 with hipcc, and the Python extension module ``_short`` (the binding's
+short way into it) with the host compiler, in-tree.
 
 Usage: ``python -m bit_quantized_gemm_amd.build``.  Objects go to ``_build/``; the shared
-library is written next to this file.  Every call recompiles.
+libraries are written next to this file.  Every call recompiles.
 """
 from __future__ import annotations
 
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatom.so")
+SHORT = os.path.join(HERE, "_short.so")
 
 SOURCES = ["atom_api.cpp", "select.hip", "quantize.hip", "gemm.hip", "gemm_small.hip", "gemm_w4a8.hip",
            "serve_api.cpp", "w8a8_quantize.hip", "gemm_w8a8.hip", "kv4_cache.hip", "kv4_attention.hip",
@@ -45,10 +47,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_short() -> None:
+    """The extension module, against the headers and libraries of the torch that will load it."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cxx = os.environ.get("CXX", shutil.which("g++") or "c++")
+    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [cxx, "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{INCLUDE}", *(a for i in include for a in ("-isystem", i)), os.path.join(CSRC, "short_calls.cpp"), "-o", SHORT + ".tmp",
+           f"-L{lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for short_calls.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(SHORT + ".tmp", SHORT)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=8) as ex:
+        short = ex.submit(_build_short)
         objs = list(ex.map(_compile, SOURCES))
+        short.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -56,7 +79,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB} and {SHORT}")
     return LIB
 
 

@@ -16,7 +16,7 @@ from typing import NamedTuple
 
 import bit_quantized_gemm_amd as _bq
 
-from .w8a8 import empty, fast_device, on_device
+from .w8a8 import empty, on_device
 
 __all__ = ["KV4Pool", "kv4_pool", "atom_kv4_extend", "atom_kv4_release"]
 
@@ -64,31 +64,14 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
     int32 [2]: the pool's new state).  The inputs stay as they were but for the table, unless lens_out is lens or state_out
     the pool's state, which are then replaced (more than 4096 rows take a second launch for it).  If the pool holds
     too few pages nothing is taken: all slots are -1, lengths and pool stay, state_out[1] says how many are missing."""
-    torch = _bq._torch()
-    T, i32 = torch.Tensor, torch.int32
     free, state = _pool(pool)
     total, page = int(total), int(page)
-    if (stream is None and slots is None and q_start is None and lens_out is None and state_out is None and type(lens) is T
-            and type(new) is T and type(table) is T and type(free) is T and type(state) is T and lens.is_cuda
-            and table.dim() == 2 and total > 0):
-        d = fast_device(lens)
-        batch, width = table.shape
-        if (d >= 0 and lens.shape == new.shape == (batch,) and state.shape == (2,)
-                and lens.dtype is i32 and new.dtype is i32 and table.dtype is i32 and free.dtype is i32 and state.dtype is i32
-                and lens.is_contiguous() and new.is_contiguous() and table.is_contiguous() and free.is_contiguous()
-                and state.is_contiguous() and new.get_device() == d and table.get_device() == d and free.get_device() == d
-                and state.get_device() == d):
-            device = lens.device
-            slots = torch.empty(total, dtype=torch.int64, device=device)
-            q_start = torch.empty(batch + 1, dtype=i32, device=device)
-            lens_out, state_out = torch.empty_like(lens), torch.empty_like(state)
-            status = _bq.load_library().atom_kv4_extend(
-                lens.data_ptr(), new.data_ptr(), table.data_ptr(), batch, width, page, free.data_ptr(), free.shape[0],
-                state.data_ptr(), slots.data_ptr(), total, q_start.data_ptr(), lens_out.data_ptr(), state_out.data_ptr(),
-                torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, "atom_kv4_extend")
-            return slots, q_start, lens_out, state_out
+    if stream is None and slots is None and q_start is None and lens_out is None and state_out is None and _bq._SHORT is not None:
+        out = _bq._SHORT.kv4_extend(lens, new, table, free, state, page, total)
+        if out is not None:
+            return out
+    torch = _bq._torch()
+    i32 = torch.int32
     batch, width = _bq._mat(table, "table")
     if total < 1:
         raise _bq.AtomError(f"total must be at least 1 (got {total})")
@@ -111,26 +94,14 @@ def atom_kv4_release(done, lens, table, pool, page, lens_out=None, state_out=Non
     """Give the pages of the sequences with done[b] (bool [batch]) back to the pool, whose `free` is written behind its free
     pages.  Returns (lens_out, state_out): lengths, 0 where done, and the pool's new state; either may be given as its input,
     which is then replaced (more than 16 sequences take a second launch for it)."""
-    torch = _bq._torch()
-    T, i32 = torch.Tensor, torch.int32
     free, state = _pool(pool)
     page = int(page)
-    if (stream is None and lens_out is None and state_out is None and type(done) is T and type(lens) is T and type(table) is T
-            and type(free) is T and type(state) is T and lens.is_cuda and table.dim() == 2):
-        d = fast_device(lens)
-        batch, width = table.shape
-        if (d >= 0 and done.dtype is torch.bool and done.is_contiguous() and done.get_device() == d
-                and lens.shape == done.shape == (batch,) and state.shape == (2,)
-                and lens.dtype is i32 and table.dtype is i32 and free.dtype is i32 and state.dtype is i32
-                and lens.is_contiguous() and table.is_contiguous() and free.is_contiguous() and state.is_contiguous()
-                and table.get_device() == d and free.get_device() == d and state.get_device() == d):
-            lens_out, state_out = torch.empty_like(lens), torch.empty_like(state)
-            status = _bq.load_library().atom_kv4_release(
-                done.data_ptr(), lens.data_ptr(), table.data_ptr(), batch, width, page, free.data_ptr(), free.shape[0],
-                state.data_ptr(), lens_out.data_ptr(), state_out.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, "atom_kv4_release")
-            return lens_out, state_out
+    if stream is None and lens_out is None and state_out is None and _bq._SHORT is not None:
+        out = _bq._SHORT.kv4_release(done, lens, table, free, state, page)
+        if out is not None:
+            return out
+    torch = _bq._torch()
+    i32 = torch.int32
     batch, width = _bq._mat(table, "table")
     lens_out = empty((batch,), i32, table, stream) if lens_out is None else lens_out
     state_out = empty((2,), i32, table, stream) if state_out is None else state_out

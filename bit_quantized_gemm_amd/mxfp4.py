@@ -18,7 +18,7 @@ import functools
 
 import bit_quantized_gemm_amd as _bq
 
-from .w8a8 import _bytes, check_device, check_rows, empty, fast_device, float_type, on_device
+from .w8a8 import _bytes, check_device, check_rows, empty, float_type, on_device
 
 __all__ = ["atom_mxfp4_row_bytes", "atom_mxfp4_groups", "atom_quantize_mxfp4", "atom_dequantize_mxfp4",
            "atom_gemm_mxfp4_workspace_bytes", "atom_gemm_mxfp4", "atom_linear_mxfp4_workspace_bytes", "linear_mxfp4"]
@@ -72,21 +72,12 @@ _linear_bytes = functools.lru_cache(maxsize=1024)(atom_linear_mxfp4_workspace_by
 
 def atom_quantize_mxfp4(X, Xq=None, sx=None, stream=None):
     """Codes and scales of the rows of X (fp16 / bf16 [rows, K]; rows may lie apart)."""
+    if stream is None and Xq is None and sx is None and _bq._SHORT is not None:
+        out = _bq._SHORT.quantize_mxfp4(X)
+        if out is not None:
+            return out
     torch = _bq._torch()
     u8 = torch.uint8
-    if stream is None and Xq is None and sx is None and type(X) is torch.Tensor and X.is_cuda and X.dim() == 2:
-        d, t = fast_device(X), X.dtype
-        rows, K = X.shape
-        ldx, step = X.stride()
-        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and rows and 1 <= K <= _bq.MAX_K and (step == 1 or K == 1)
-                and (ldx >= K or rows == 1)):
-            g, device = K + 255 >> 8, X.device
-            Xq, sx = torch.empty((rows, g * 128), dtype=u8, device=device), torch.empty((g, rows, 8), dtype=u8, device=device)
-            status = _bq.load_library().atom_quantize_mxfp4(X.data_ptr(), ldx, int(t is torch.bfloat16), rows, K, Xq.data_ptr(),
-                                                            sx.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, "atom_quantize_mxfp4")
-            return Xq, sx
     rows, K = _bq._mat(X, "X")
     kind = float_type(X, "X")
     rb, g = packed(K)
@@ -108,19 +99,10 @@ def atom_quantize_mxfp4(X, Xq=None, sx=None, stream=None):
 def atom_dequantize_mxfp4(Xq, sx, K, dtype=None, X=None, stream=None):
     """X [rows, K] that packed rows stand for, in `dtype` (default fp16, or X's)."""
     torch = _bq._torch()
-    T, u8 = torch.Tensor, torch.uint8
-    if stream is None and X is None and type(Xq) is T and type(sx) is T and Xq.is_cuda and type(K) is int:
-        d, qs = fast_device(Xq), Xq.shape
-        t = torch.float16 if dtype is None else dtype
-        g = K + 255 >> 8
-        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and 1 <= K <= _bq.MAX_K and len(qs) == 2 and qs[0]
-                and qs[1] == g * 128 and Xq.dtype is u8 and Xq.is_contiguous() and sx.dtype is u8
-                and sx.shape == (g, qs[0], 8) and sx.is_contiguous() and sx.get_device() == d):
-            X = torch.empty((qs[0], K), dtype=t, device=Xq.device)
-            status = _bq.load_library().atom_dequantize_mxfp4(Xq.data_ptr(), sx.data_ptr(), qs[0], K, int(t is torch.bfloat16),
-                                                              X.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, "atom_dequantize_mxfp4")
+    u8 = torch.uint8
+    if stream is None and X is None and _bq._SHORT is not None and dtype in (None, torch.float16, torch.bfloat16):
+        X = _bq._SHORT.dequantize_mxfp4(Xq, sx, K, dtype is torch.bfloat16)
+        if X is not None:
             return X
     K = int(K)
     rb, g = packed(K)
@@ -170,33 +152,12 @@ def linear_mxfp4(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
     one call.  Y has X's type.  `workspace`: 1-D uint8 of at least ``atom_linear_mxfp4_workspace_bytes``
     bytes (calls that may overlap need one each; none for the few tokens that take one launch), else a torch buffer is
     taken for the call when one is needed."""
+    if stream is None and Y is None and workspace is None and _bq._SHORT is not None:
+        Y = _bq._SHORT.linear_mxfp4(X, Wq, sw, bias)
+        if Y is not None:
+            return Y
     torch = _bq._torch()
-    T = torch.Tensor
     u8 = torch.uint8
-    if stream is None and Y is None and workspace is None and type(X) is T and type(Wq) is T and type(sw) is T:
-        t, xs, ws = X.dtype, X.shape, Wq.shape
-        if X.is_cuda and len(xs) == 2 and len(ws) == 2 and (t is torch.float16 or t is torch.bfloat16):
-            M, K = xs
-            N = ws[0]
-            ldx, step = X.stride()
-            d = fast_device(X)
-            g = K + 255 >> 8
-            if (d >= 0 and 1 <= K <= _bq.MAX_K and M and N and (step == 1 or K == 1) and (ldx >= K or M == 1)
-                    and Wq.dtype is u8 and ws[1] == g * 128 and Wq.is_contiguous()
-                    and Wq.get_device() == d and sw.dtype is u8 and sw.shape == (g, N, 8) and sw.is_contiguous()
-                    and sw.get_device() == d
-                    and (bias is None or type(bias) is T and bias.dtype is t and bias.shape == (N,)
-                         and bias.is_contiguous() and bias.get_device() == d)):
-                need = _linear_bytes(M, N, K)
-                Y = X.new_empty((M, N))
-                workspace = torch.empty(need, dtype=u8, device=X.device) if need else None
-                status = _bq.load_library().atom_linear_mxfp4(
-                    X.data_ptr(), ldx, int(t is torch.bfloat16), Wq.data_ptr(), sw.data_ptr(),
-                    None if bias is None else bias.data_ptr(), M, N, K, Y.data_ptr(), workspace.data_ptr() if need else None, need,
-                    torch._C._cuda_getCurrentRawStream(d))
-                if status:
-                    _bq._check(status, "atom_linear_mxfp4")
-                return Y
     M, K = _bq._mat(X, "X")
     N, _ = _bq._mat(Wq, "Wq")
     kind = float_type(X, "X")

@@ -14,7 +14,7 @@ import ctypes
 import bit_quantized_gemm_amd as _bq
 
 from .mxfp4 import packed
-from .w8a8 import _row_bytes, check_device, check_rows, empty, fast_device, float_type, on_device
+from .w8a8 import _row_bytes, check_device, check_rows, empty, float_type, on_device
 
 __all__ = ["atom_rmsnorm_w8a8", "atom_rmsnorm_mxfp4"]
 
@@ -29,40 +29,10 @@ def signatures():
 
 
 def _rmsnorm(name, mx, X, weight, eps, residual, H, Xq, sx, stream):
-    torch = _bq._torch()
-    T = torch.Tensor
-    if (stream is None and H is None and Xq is None and sx is None and type(X) is T and type(weight) is T and X.is_cuda
-            and X.dim() == 2):
-        d, t, xs = fast_device(X), X.dtype, X.shape
-        rows, K = xs
-        ldx, step = X.stride()
-        ok = (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and rows and 1 <= K <= _bq.MAX_K and (step == 1 or K == 1)
-              and (ldx >= K or rows == 1) and weight.dtype is t and weight.shape == (K,) and weight.is_contiguous()
-              and weight.get_device() == d)
-        ldr = K
-        if ok and residual is not None:
-            ok = type(residual) is T and residual.dtype is t and residual.shape == xs and residual.get_device() == d
-            if ok:
-                ldr, step = residual.stride()
-                ok = (step == 1 or K == 1) and (ldr >= K or rows == 1)
-        if ok:
-            device, pR, pH = X.device, None, None
-            if mx:
-                g = K + 255 >> 8
-                Xq = torch.empty((rows, g * 128), dtype=torch.uint8, device=device)
-                sx = torch.empty((g, rows, 8), dtype=torch.uint8, device=device)
-            else:
-                Xq = torch.empty((rows, K + 127 & -128), dtype=torch.int8, device=device)
-                sx = torch.empty((rows,), dtype=torch.float32, device=device)
-            if residual is not None:
-                H = torch.empty((rows, K), dtype=t, device=device)
-                pR, pH = residual.data_ptr(), H.data_ptr()
-            status = getattr(_bq.load_library(), name)(
-                X.data_ptr(), ldx, pR, ldr, weight.data_ptr(), float(eps), int(t is torch.bfloat16), rows, K, pH, K,
-                Xq.data_ptr(), sx.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, name)
-            return Xq, sx, H
+    if stream is None and H is None and Xq is None and sx is None and _bq._SHORT is not None:
+        out = (_bq._SHORT.rmsnorm_mxfp4 if mx else _bq._SHORT.rmsnorm_w8a8)(X, weight, float(eps), residual)
+        if out is not None:
+            return out
     rows, K = _bq._mat(X, "X")
     kind = float_type(X, "X")
     (qs, qt), (ss, st) = (_mx if mx else _w8)(rows, K)

@@ -160,18 +160,9 @@ def atom_quantize_w8a8(X, Xq=None, sx=None, stream=None):
 def atom_dequantize_w8a8(Xq, sx, K, dtype=None, X=None, stream=None):
     """X [rows, K] that packed rows stand for, code * scale, in `dtype` (default fp16, or X's)."""
     torch = _bq._torch()
-    T = torch.Tensor
-    if stream is None and X is None and type(Xq) is T and type(sx) is T and Xq.is_cuda and type(K) is int:
-        d, qs = fast_device(Xq), Xq.shape
-        t = torch.float16 if dtype is None else dtype
-        if (d >= 0 and (t is torch.float16 or t is torch.bfloat16) and 1 <= K <= _bq.MAX_K and len(qs) == 2 and qs[0]
-                and qs[1] == (K + 127 & -128) and Xq.dtype is torch.int8 and Xq.is_contiguous() and sx.dtype is torch.float32
-                and sx.shape == (qs[0],) and sx.is_contiguous() and sx.get_device() == d):
-            X = torch.empty((qs[0], K), dtype=t, device=Xq.device)
-            status = _bq.load_library().atom_dequantize_w8a8(Xq.data_ptr(), sx.data_ptr(), qs[0], K, int(t is torch.bfloat16),
-                                                             X.data_ptr(), torch._C._cuda_getCurrentRawStream(d))
-            if status:
-                _bq._check(status, "atom_dequantize_w8a8")
+    if stream is None and X is None and _bq._SHORT is not None and dtype in (None, torch.float16, torch.bfloat16):
+        X = _bq._SHORT.dequantize_w8a8(Xq, sx, K, dtype is torch.bfloat16)
+        if X is not None:
             return X
     K = int(K)
     rb = _row_bytes(K)

@@ -148,7 +148,7 @@ SHAPES = [(1, 1, 1), (1, 17, 300), (1, 4096, 4096), (3, 130, 127), (16, 100, 110
           (201, 16403, 2300), (501, 16403, 2600), (1000, 10900, 4000), (777, 777, 7000), (100, 4096, 6000), (300, 777, 4100)]
 
 # every position at which K can end in the rings of stage buffers, for each tile size (M, N, groups of K)
-RINGS = ([(131, 1003, g) for g in range(1, 14)] + [(131, 16403, g) for g in range(1, 6)] + [(131, 6003, g) for g in range(6, 14)] +
+RINGS = ([(201, 1003, g) for g in range(1, 9)] + [(501, 501, g) for g in range(9, 14)] + [(131, 16403, g) for g in range(1, 6)] + [(131, 6003, g) for g in range(6, 14)] +
          [(201, 16403, g) for g in range(1, 5)] + [(333, 8203, 5), (333, 8203, 6)] + [(131, 11003, g) for g in range(7, 12)] +
          [(201, 16403, g) for g in range(8, 15)] + [(701, 16403, g) for g in range(5, 10)] + [(501, 16403, g) for g in range(10, 14)])
 
