@@ -1,5 +1,6 @@
 // MXFP4 GEMM for gfx950: Y[m,n] = round(sum over blocks of 2^(ex + ew) * (32 products of 4-bit floats) + bias[n]) on
-// v_mfma_scale_f32_{32x32x64,16x16x128}_f8f6f4, which take the blocks' scale bytes as they are.
+// v_mfma_scale_f32_{32x32x64,16x16x128}_f8f6f4, which take the blocks' scale bytes as they are: twice the operations of the
+// int8 product a cycle, from half its bytes.
 //
 // Operand layout.  A stage is a group of 256 values: 128 bytes, a cache line, of each row, eight blocks of 16 bytes.  An
 // instruction takes one block of each row from each lane, and which block of K that is is free as long as both operands
@@ -7,6 +8,26 @@
 // of its four slices are one word of the group's eight, chosen by the instruction's byte select.  The weights are the
 // first operand, so a 32x32 accumulator holds its tile transposed: lane l owns token l & 31, element r is column
 // (r >> 2) * 8 + (l >> 5) * 4 + (r & 3): four runs of four columns.
+//
+// Precision.  A block's 32 products and their sum are exact; instructions add blocks' sums to the fp32 accumulator, aligned to
+// the largest of them (errors of 2^-23 of the magnitudes, measured on operands of very different scales).
+//
+// Kernels.
+//   gemm_tile_kernel: the workgroup's four waves each own a quarter of a BM x BN tile; stages are copied from global memory
+//     straight into LDS (LDS-DMA).  At the largest sizes the power that random operands draw bounds it: 4096 x 28672 x 8192
+//     (M x N x K) takes 449 us, 4.3 PFLOP/s, with zeros 348 us; the same kernel without copies and LDS reads 327 and 266 us (the
+//     matrix cores alone at the clock that power leaves), without its stores 416 and 308.  The library's product reaches 3.0 PFLOP/s
+//     there.  Below that it is bound by how fast a compute unit gets lines that miss its L2: 2048 x 4096 x 11008 53 us (3.5
+//     PFLOP/s), 48 with zeros, 46 the copies alone.
+//     On the way there (4096 x 28672 x 8192 and 2048 x 4096 x 11008): 485 and 61 us with each wave's scale words loaded into
+//     registers and a stage's copies issued in one slice; 478 and 62 with all of a stage's operands in registers after its first slice
+//     (256 x 256 tiles); 449 and 53 with scales through LDS and copies spread over the slices.
+//   gemm_rows_kernel (few tokens, or few outputs): bound by reading the weights and the launch.  A workgroup owns 16 columns, its
+//     waves divide K, each loads its operands straight into registers, all of them at once where K is short; the waves' sums
+//     meet in LDS.  Weights from HBM: 16 x 4096 x 4096 5.0 us, 16 x 11008 x 4096 9.6 us (2.5 TB/s; as many bytes of codes from
+//     the L2), 1 x 11008 x 4096 7.7 us.
+//   linear_rows_kernel: the same for at most four tokens with the quantizer in front, one launch for two: 1 x 4096 x 4096 4.9 us
+//     against 6.5.
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "gemm_tile.h"
@@ -108,8 +129,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     return *reinterpret_cast<const i32x4*>(buf + row * kStage + (((4 * kh + t) ^ swz) << 4));
   };
   // Scales of a stage: 8 bytes a row, loaded once by the workgroup (thread t: row t of the two operands' rows, and row 256 + t)
-  // and read from LDS as words.  Loads of each wave's own words take four times the instructions, and they stand in line
-  // with the copies: 4096 x 28672 x 8192 of zeros 371 us so, 330 us without any scales.
+  // and read from LDS as words.  Each wave loading its own words takes four times the instructions, which stand in line
+  // with the copies: 4096 x 28672 x 8192 of zeros 371 us so, 330 us without any scales, 348 us through LDS.
   constexpr int kRows = (BM + BN + 255) / 256;
   __shared__ __attribute__((aligned(16))) u32x2 ls0[kRows * 256], ls1[kRows * 256];
   const uint8_t* from[kRows];
@@ -295,40 +316,48 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
               f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     return;
   }
-  // Epilogue through LDS, 32 rows of a wave at a time, so that whole rows of the tile are stored.  Chunk c of 4 columns
-  // of row r lies at position c ^ (r & 15) (& 7 where a row has eight): the writes (16 rows of one chunk) and the reads (a
-  // row's chunks) cover the banks.
+  // Epilogue: a wave's tile in Y's type through LDS (it fits a stage buffer), so that whole rows of it are stored.  A lane has
+  // four neighbouring columns of a row: half a chunk of 16 bytes.  Chunk c of row r lies at position c ^ r (modulo the
+  // row's chunks), its halves swapped in rows 16 to 31 of 32, so that 32 rows' halves cover all banks.
   wg_barrier();                                           // every wave has read its last stage
-  constexpr int kLanes = WN / 8;                          // lanes of a row: 8 columns each
-  constexpr int kTurn = WN / 4 < 16 ? WN / 4 - 1 : 15;
-  f32x4* own = reinterpret_cast<f32x4*>(wave == 0 ? la0 : wave == 1 ? la1 : RING == 2 ? (wave == 2 ? lb0 : lb1)
-                                                                                      : (wave == 2 ? la2 : lb0));
-  static_assert(32 * WN * 4 <= kA && 32 * WN * 4 <= kB, "a wave's rows fit a stage buffer");
-  const int c8 = lane % kLanes, n = n0 + wn * WN + 8 * c8;
-  float b[8] = {};
-  if (bias) {
+  constexpr int kChunks = WN / 8;                         // 16-byte chunks of a row: one lane's store
+  static_assert(WM * WN * 2 <= kA && WM * WN * 2 <= kB, "a wave's tile fits a stage buffer");
+  uint8_t* own = wave == 0 ? la0 : wave == 1 ? la1 : RING == 2 ? (wave == 2 ? lb0 : lb1) : (wave == 2 ? la2 : lb0);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) b[e] = T::load(bias[min(n + e, N - 1)]);
-  }
+  for (int j = 0; j < TN; ++j)
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
+    for (int q = 0; q < 4; ++q) {
+      float b[4] = {};
+      if (bias) {
+        const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * kh;
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        own[l32 * (WN / 4) + ((8 * j + 2 * q + kh) ^ (l32 & kTurn))] =
-            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-#pragma unroll
-    for (int r = lane / kLanes; r < 32; r += 64 / kLanes) {
-      const int m = m0 + wm * WM + 32 * i + r;
-      const f32x4 lo = own[r * (WN / 4) + ((2 * c8) ^ (r & kTurn))], hi = own[r * (WN / 4) + ((2 * c8 + 1) ^ (r & kTurn))];
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = biased(lo[e], b[e]);
-        y[e + 4] = biased(hi[e], b[e + 4]);
+        for (int e = 0; e < 4; ++e) b[e] = T::load(bias[min(n + e, N - 1)]);
       }
-      if (m < M) store8<T>(Y + (size_t)m * N + n, y, N - n, (N & 7) == 0);
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = biased(acc[i][j][4 * q + e], b[e]);
+        const int chunk = (4 * j + q) ^ (l32 & (kChunks - 1));
+        *reinterpret_cast<u32x2*>(own + ((32 * i + l32) * kChunks + chunk) * 16 + 8 * (kh ^ (l32 >> 4))) =
+            u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+      }
+    }
+  const int c = lane % kChunks, n = n0 + wn * WN + 8 * c;
+#pragma unroll
+  for (int it = 0; it < WM * kChunks / 64; ++it) {
+    const int r = it * (64 / kChunks) + lane / kChunks, m = m0 + wm * WM + r;
+    u32x4 v = *reinterpret_cast<const u32x4*>(own + (r * kChunks + (c ^ (r & (kChunks - 1)))) * 16);
+    if ((it * (64 / kChunks)) & 16) v = u32x4{v[2], v[3], v[0], v[1]};
+    if (m < M) {
+      uint16_t* dst = Y + (size_t)m * N + n;
+      if ((N & 7) == 0) {
+        if (n < N) *reinterpret_cast<u32x4*>(dst) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (n + e < N) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+      }
     }
   }
 }

@@ -46,6 +46,19 @@ __device__ __forceinline__ float scaled(int acc, float sx, float sw, float bias)
   return y;
 }
 
+// Eight outputs of a row, `left` of them inside it; wide: the row's start is 16-byte aligned.
+template <class T>
+__device__ __forceinline__ void store8(uint16_t* dst, const float (&y)[8], int left, bool wide) {
+  if (wide && left >= 8) {
+    *reinterpret_cast<u32x4*>(dst) =
+        u32x4{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7])};
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < left) dst[e] = T::store(y[e]);
+  }
+}
+
 // BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
 // workgroup p * tiles + t and writes its int32 tile to part[(p * tiles + t) * BM * BN].
 template <class T, int BM, int BN, int RING, int WAVES, bool kDivided>
