@@ -62,7 +62,7 @@ __device__ __forceinline__ float biased(float acc, float bias) {
 
 // BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
 // workgroup p * tiles + t and writes its fp32 tile to part[(p * tiles + t) * BM * BN].
-template <class T, int BM, int BN, int RING, int WAVES, bool kDivided, bool kEarly>
+template <class T, int BM, int BN, int RING, int WAVES, bool kDivided, bool kEarly, bool kBias>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) void gemm_tile_kernel(
     const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ sx, const uint8_t* __restrict__ Wq,
     const uint8_t* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int stages, uint16_t* __restrict__ Y,
@@ -94,6 +94,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   const int m0 = tc.x * BM, n0 = tc.y * BN;
   const int sa = kDivided ? (int)((int64_t)stages * piece / splits) : 0;
   const int sb = kDivided ? (int)((int64_t)stages * (piece + 1) / splits) : stages;
+
+  // The tile's bias, for the epilogue (the first barrier comes before it).
+  __shared__ __attribute__((aligned(16))) uint16_t l_bias[kBias ? BN : 4];
+  if (kBias && tid < BN) l_bias[tid] = bias[min(n0 + tid, N - 1)];
 
   // Stage copies: wave w copies rows [w B / 4, (w + 1) B / 4) of both operands, 8 rows an
   // instruction: lane i lands at row i / 8, position i % 8, and loads the chunk that lies there.
@@ -327,17 +331,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
   for (int j = 0; j < TN; ++j)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float b[4] = {};
-      if (bias) {
-        const int n = n0 + wn * WN + 32 * j + 8 * q + 4 * kh;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = T::load(bias[min(n + e, N - 1)]);
-      }
+      u32x2 b = {0, 0};
+      if (kBias) b = *reinterpret_cast<const u32x2*>(l_bias + wn * WN + 32 * j + 8 * q + 4 * kh);
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         float y[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = biased(acc[i][j][4 * q + e], b[e]);
+        for (int e = 0; e < 4; ++e) y[e] = biased(acc[i][j][4 * q + e], elem<T>(b[e / 2], e & 1));
         const int chunk = (4 * j + q) ^ (l32 & (kChunks - 1));
         *reinterpret_cast<u32x2*>(own + ((32 * i + l32) * kChunks + chunk) * 16 + 8 * (kh ^ (l32 >> 4))) =
             u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
@@ -554,10 +554,15 @@ void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8
   ATOM_ROWS(1, 2)
 #undef ATOM_ROWS
   const dim3 grid(p.tiles * p.splits);
-#define ATOM_TILE(KIND, BM, BN, RING, W, E)                                                                             \
-  if (p.kind == KIND)                                                                                                \
-    hipLaunchKernelGGL((gemm_tile_kernel<T, BM, BN, RING, W, KIND == kDividedKind, E>), grid, dim3(256), 0, st, Xq, sx, \
-                       Wq, sw, bias, M, N, groups, Y, p.tiles, p.splits, part);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, Xq, sx, Wq, sw, bias, M, N, groups, Y, p.tiles, p.splits, part);
+  };
+#define ATOM_TILE(KIND, BM, BN, RING, W, E)                                                  \
+  if (p.kind == KIND) {                                                                      \
+    constexpr bool kDivided = KIND == kDividedKind;                                          \
+    bias && p.splits == 1 ? go(gemm_tile_kernel<T, BM, BN, RING, W, kDivided, E, true>)      \
+                          : go(gemm_tile_kernel<T, BM, BN, RING, W, kDivided, E, false>);    \
+  }
   ATOM_TILE(2, 64, 64, 3, 3, false)
   ATOM_TILE(3, 64, 128, 3, 2, false)
   ATOM_TILE(4, 128, 128, 2, 2, true)
