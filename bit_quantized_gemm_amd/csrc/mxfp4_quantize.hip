@@ -4,40 +4,43 @@
 // row needs no barrier: a lane loads eight elements (16 bytes), four lanes join their maxima by two DPP moves, and the
 // 16 lanes of four blocks gather a word of scale bytes.  Codes leave as 4 bytes a lane, whole lines a wave.
 //
-// Scales lie group by group ([groups, rows, 8]), so a line of them belongs to 16 rows: a workgroup takes whole runs of 16
-// rows of a few groups, and its stores to that line meet in one L2.
+// Scales lie group by group ([groups, rows, 8]), so a line of them belongs to 16 rows: a workgroup takes neighbouring rows,
+// whose pieces of it meet in one L2.
+//
+// Measured: 8192 x 8192 38 us (4.4 TB/s, a copy of memory reaches 4.75), 2048 x 11008 14.6 us, 16 x 4096 1.9 us, of which the launch is
+// most; back to values 8192 x 8192 38 us.
 #include "mxfp4_row.h"
 
 namespace atom {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 16;                               // rows of a workgroup: a line of scales
-
-// Workgroup (x, y): rows ROWS x .., the 64-lane span 512 y .. + 511 of K.
-template <class T, bool VEC, int ROWS>
+// Workgroup (x, y): rows 4 RW x .., elements 512 CW y .. + 512 CW - 1 of each; a wave takes one row in four.
+template <class T, bool VEC, int RW, int CW>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t* __restrict__ X, int64_t ldx, int rows, int K,
                                                             int Kp, uint8_t* __restrict__ Xq, uint8_t* __restrict__ sx) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.y * 64 + lane;                 // the lane's chunk of eight elements in every row
-  u32x4 w[ROWS / 4];
+  auto row_of = [&](int i) { return (int)blockIdx.x * 4 * RW + 4 * i + wave; };
+  auto chunk_of = [&](int j) { return ((int)blockIdx.y * CW + j) * 64 + lane; };   // of eight elements
+  u32x4 w[RW][CW];
 #pragma unroll
-  for (int i = 0; i < ROWS / 4; ++i) {
-    const int row = blockIdx.x * ROWS + 4 * i + wave;
-    w[i] = w8a8::load8<VEC>(X + (int64_t)min(row, rows - 1) * ldx, c, K);
-  }
+  for (int i = 0; i < RW; ++i)
 #pragma unroll
-  for (int i = 0; i < ROWS / 4; ++i) {
-    const int row = blockIdx.x * ROWS + 4 * i + wave;
-    uint32_t byte;
-    const uint32_t code = mx::quantize8<T>(w[i], byte);
-    const uint32_t four = mx::gather_scales(byte, lane);
-    if (row < rows && 8 * c < Kp) {
-      *reinterpret_cast<uint32_t*>(Xq + (int64_t)row * (Kp / 2) + 4 * c) = code;
-      if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(sx + ((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 4) & 1) * 4) = four;
+    for (int j = 0; j < CW; ++j) w[i][j] = w8a8::load8<VEC>(X + (int64_t)min(row_of(i), rows - 1) * ldx, chunk_of(j), K);
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int j = 0; j < CW; ++j) {
+      const int row = row_of(i), c = chunk_of(j);
+      uint32_t byte;
+      const uint32_t code = mx::quantize8<T>(w[i][j], byte);
+      const uint32_t four = mx::gather_scales(byte, lane);
+      if (row < rows && 8 * c < Kp) {
+        *reinterpret_cast<uint32_t*>(Xq + (int64_t)row * (Kp / 2) + 4 * c) = code;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(sx + ((int64_t)(c >> 5) * rows + row) * 8 + ((c >> 4) & 1) * 4) = four;
+      }
     }
-  }
 }
 
 // One thread per eight elements of each of ROWS / 4 rows.
@@ -79,9 +82,10 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
   }
 }
 
-// Rows of a workgroup: a whole line of scales once there are workgroups enough for it.  (us, 4 and 16 rows: quantize
-// 16 x 4096 1.9 and 2.3, 333 x 1155 2.4 and 4.3; back 16 x 4096 2.0 and 3.3, 8192 x 8192 49 and 38.)
-bool whole_lines(int rows, int Kp) { return (int64_t)((rows + kRows - 1) / kRows) * ((Kp + 511) / 512) >= 2048; }
+// Whether there are workgroups enough for several rows each.
+bool many(int rows, int Kp, int per, int columns) {
+  return (int64_t)((rows + per - 1) / per) * ((Kp + columns - 1) / columns) >= 2048;
+}
 
 }  // namespace
 
@@ -90,13 +94,16 @@ hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int 
                                  hipStream_t stream) {
   const int Kp = mx::padded(K);
   const bool vec = K % 8 == 0 && (rows == 1 || ldx % 8 == 0) && (reinterpret_cast<uintptr_t>(X) & 15) == 0;
-  auto go = [&](auto kernel, int per) {
-    hipLaunchKernelGGL(kernel, dim3((rows + per - 1) / per, (Kp + 511) / 512), dim3(kThreads), 0, stream, X, ldx, rows, K, Kp, Xq, sx);
+  auto go = [&](auto kernel, int per, int columns) {
+    hipLaunchKernelGGL(kernel, dim3((rows + per - 1) / per, (Kp + columns - 1) / columns), dim3(kThreads), 0, stream, X, ldx, rows, K,
+                       Kp, Xq, sx);
   };
+  // (us, rows x columns of a workgroup 4 x 512, 16 x 512, 8 x 1024: 512 x 4096 2.8, 3.2, 3.2; 2048 x 4096 6.9, 6.5, 6.5; 4096 x 8192 19.8,
+  // 20.6, 19.7; 2048 x 11008 16.6, 14.6, 14.6; unaligned 333 x 1155 2.4 and 4.3)
   auto pick = [&](auto type) {
     using T = decltype(type);
-    if (whole_lines(rows, Kp)) vec ? go(quantize_kernel<T, true, kRows>, kRows) : go(quantize_kernel<T, false, kRows>, kRows);
-    else vec ? go(quantize_kernel<T, true, 4>, 4) : go(quantize_kernel<T, false, 4>, 4);
+    if (many(rows, Kp, 4, 512)) vec ? go(quantize_kernel<T, true, 2, 2>, 8, 1024) : go(quantize_kernel<T, false, 2, 2>, 8, 1024);
+    else vec ? go(quantize_kernel<T, true, 1, 1>, 4, 512) : go(quantize_kernel<T, false, 1, 1>, 4, 512);
   };
   bf16 ? pick(Bf16{}) : pick(Fp16{});
   return hipGetLastError();
@@ -111,7 +118,8 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int row
   };
   auto pick = [&](auto type) {
     using T = decltype(type);
-    if (whole_lines(rows, Kp)) vec ? go(dequantize_kernel<T, true, kRows>, kRows) : go(dequantize_kernel<T, false, kRows>, kRows);
+    // (us, 4 and 16 rows: 16 x 4096 2.0 and 3.3, 8192 x 8192 49 and 38: a line of scales is read once for 16 rows)
+    if (many(rows, Kp, 16, 512)) vec ? go(dequantize_kernel<T, true, 16>, 16) : go(dequantize_kernel<T, false, 16>, 16);
     else vec ? go(dequantize_kernel<T, true, 4>, 4) : go(dequantize_kernel<T, false, 4>, 4);
   };
   bf16 ? pick(Bf16{}) : pick(Fp16{});

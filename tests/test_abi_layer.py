@@ -244,3 +244,32 @@ def test_binding_refusals(lib, monkeypatch):
         with pytest.raises(bq.AtomError, match="ROCm device"):
             print(i)
             call()
+
+
+def test_short_calls_leave_the_rest_to_the_full_checks(lib):
+    """The extension module takes plain device tensors alone: anything else is None, whatever it is, and no Python error."""
+    torch = pytest.importorskip("torch")
+    short = bq._SHORT
+    if short is None:
+        pytest.skip("_short.so not built (python -m bit_quantized_gemm_amd.build)")
+    t, i = torch.zeros((4, 300), dtype=torch.float16), torch.zeros(5, dtype=torch.int32)
+
+    class Sub(torch.Tensor):
+        pass
+    odd = [None, 0, 1.5, "x", [t], t, i, t.numpy(), t.as_subclass(Sub), torch.nn.Parameter(t), object(), 1 << 80, -1]
+    sizes = {"quantize_mxfp4": 1, "linear_mxfp4": 4, "dequantize_mxfp4": 4, "dequantize_w8a8": 4, "rmsnorm_w8a8": 4, "rmsnorm_mxfp4": 4,
+             "kv4_extend": 7, "kv4_release": 6}
+    for name, n in sizes.items():
+        f = getattr(short, name)
+        for k in range(n + 2):                       # wrong numbers of arguments too
+            for o in odd:
+                assert f(*[o] * k) is None, (name, k, o)
+        for a in odd:
+            for b in odd:
+                assert f(*([a, b] * n)[:n]) is None, (name, a, b)
+    for bad in ((), ({},), ([], None), ({"atom_kv4_extend": "x"}, None)):
+        with pytest.raises(TypeError):
+            short.bind(*bad)
+    assert bq._bind_short(lib, ("atom_linear_mxfp4",)) is short           # (names left out: those calls return None)
+    assert short.quantize_mxfp4(t) is None
+    assert bq._bind_short(lib, [n for m in (mxfp4, norm, kv4_pages) for n in m.EXPORTS] + ["atom_dequantize_w8a8"]) is short

@@ -214,3 +214,72 @@ def test_refusals_on_the_device():
         print(i, flush=True)
         with pytest.raises(bq.AtomError):
             call()
+
+
+def calls(t=torch.float16):
+    """Each new operator's call on well-formed tensors, as a function of a stream (None: the short way)."""
+    g = torch.Generator().manual_seed(3)
+    X, W = torch.randn(9, 700, generator=g).to(t).cuda(), torch.randn(700, generator=g).to(t).cuda()
+    Wq, sw = bq.atom_quantize_mxfp4(torch.randn(50, 700, generator=g).to(t).cuda())
+    b = torch.randn(50, generator=g).to(t).cuda()
+    q4, q8 = bq.atom_quantize_mxfp4(X), bq.atom_quantize_w8a8(X)
+    lens = torch.tensor([3, 40, 0, 17], dtype=torch.int32, device="cuda")
+    new, done = torch.tensor([5, 1, 2, 30], dtype=torch.int32, device="cuda"), torch.tensor([True, False, True, True], device="cuda")
+    table, pool = torch.arange(16, dtype=torch.int32, device="cuda").view(4, 4), bq.kv4_pool(30)
+    return [lambda s: bq.linear_mxfp4(X, Wq, sw, stream=s), lambda s: bq.linear_mxfp4(X[:2], Wq, sw, b, stream=s),
+            lambda s: bq.linear_mxfp4(X[::2], Wq, sw, b, stream=s), lambda s: bq.atom_quantize_mxfp4(X, stream=s),
+            lambda s: bq.atom_dequantize_mxfp4(*q4, 700, dtype=t, stream=s), lambda s: bq.atom_dequantize_w8a8(*q8, 700, dtype=t, stream=s),
+            *(lambda s, f=f, r=r: f(X, W, 1e-5, residual=r, stream=s) for f in (bq.atom_rmsnorm_w8a8, bq.atom_rmsnorm_mxfp4)
+              for r in (None, X.flip(0).contiguous())),
+            lambda s: bq.atom_kv4_extend(lens, new, table, pool, 16, 41, stream=s),
+            lambda s: bq.atom_kv4_release(done, lens, table, pool, 16, stream=s)]
+
+
+def flat(out):
+    return [t for t in (out if isinstance(out, tuple) else (out,)) if t is not None]
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_short_and_full_way_agree(dtype):
+    """The extension module and the full checks call the same kernels: the same outputs, types and shapes; neither keeps a reference
+    or memory.  (The extension module is built with the library.)"""
+    import sys
+    assert bq._SHORT is not None
+    for i, call in enumerate(calls(dtype)):
+        print(i, flush=True)
+        short, full = flat(call(None)), flat(call(torch.cuda.current_stream()))
+        keep = bq._SHORT
+        bq._SHORT = None
+        try:
+            without = flat(call(None))
+        finally:
+            bq._SHORT = keep
+        assert len(short) == len(full) == len(without)
+        for a, b, c in zip(short, full, without):
+            assert a.dtype == b.dtype == c.dtype and a.shape == b.shape == c.shape and a.is_contiguous() and not a.requires_grad
+            torch.testing.assert_close(a, b, rtol=0, atol=0)
+            torch.testing.assert_close(a, c, rtol=0, atol=0)
+        del short, full, without, a, b, c
+        call(None)
+        torch.cuda.synchronize()
+        used, none = torch.cuda.memory_allocated(), sys.getrefcount(None)
+        for _ in range(500):
+            call(None)
+        torch.cuda.synchronize()
+        assert torch.cuda.memory_allocated() == used and abs(sys.getrefcount(None) - none) < 100
+
+
+def test_short_way_takes_the_current_stream():
+    """Work queued on a side stream in front of a call there is seen by it."""
+    side = torch.cuda.Stream()
+    X = torch.zeros(64, 4096, dtype=torch.float16, device="cuda")
+    Wq, sw = bq.atom_quantize_mxfp4(torch.ones(32, 4096, dtype=torch.float16, device="cuda"))
+    big = torch.randn(4096, 4096, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(5):
+            big = big @ big * 1e-3
+        X.fill_(1.0)
+        Y = bq.linear_mxfp4(X, Wq, sw)
+    side.synchronize()
+    torch.testing.assert_close(Y, torch.full_like(Y, 4096.0), rtol=0, atol=0)

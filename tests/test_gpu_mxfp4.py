@@ -71,7 +71,7 @@ def check_y(Y, x, w, bias, K, what):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,K", [(1, 1), (3, 7), (5, 31), (4, 32), (9, 33), (2, 255), (7, 256), (17, 257), (16, 520), (15, 2048),
-                                    (5, 2049), (33, 4096), (2, 11008), (1, 65535), (2, 65536), (385, 1155)])
+                                    (5, 2049), (33, 4096), (2, 11008), (1, 65535), (2, 65536), (385, 1155), (11003, 1155), (8203, 2056)])
 def test_quantize_and_back(rows, K, dtype):
     say(f"[mxfp4 quantize] {rows}x{K} {dtype}")
     t = TYPES[dtype]
