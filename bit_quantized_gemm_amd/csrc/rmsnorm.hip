@@ -135,21 +135,23 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
     if (t == 0) static_cast<float*>(a.sx)[row] = s;
     const double f = s > 0.0f ? rstd / (double)s : 0.0;
     const float f32 = (float)f;
+    // A factor beyond fp32, or a scale whose own rounding can carry a code past 127: all codes in fp64.
+    const bool extreme = !(f32 < 0x1p100f) || s < 0x1p-100f;
     uint8_t* q = a.Xq + (size_t)row * Kp;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int c = t + i * THREADS;
       uint32_t b[8];
-      bool doubt = false;
+      float far = 0.0f;                                 // largest distance to an integer
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float u = elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1) * f32;
         const float k = u + 12582912.0f;                // 1.5 * 2^23: the integer (ties to even) in the low byte
-        // |u| <= 127 (1 + 2^-23), so u is within 2^-15.9 of the exact value
-        doubt |= !(__builtin_fabsf(u - (k - 12582912.0f)) < 0.5f - 0x1p-15f);
+        far = __builtin_fmaxf(far, __builtin_fabsf(u - (k - 12582912.0f)));
         b[j] = __builtin_bit_cast(uint32_t, k);
       }
-      if (__builtin_amdgcn_ballot_w64(doubt)) {
+      // |u| <= 127 (1 + 2^-23), so u is within 2^-15.9 of the exact value
+      if (__builtin_amdgcn_ballot_w64(extreme || far >= 0.5f - 0x1p-15f)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const double u = (double)(elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1)) * f;
@@ -185,16 +187,17 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       const double f = rstd * __builtin_bit_cast(double, (uint64_t)(1023 + 127 - (int)byte) << 52);
       const float f32 = (float)f;
       float u[8];
-      bool doubt = false;
+      uint32_t near = 8;                                // distance to a border, in units of the last place
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         u[j] = p[j] * f32;
         // within 2 units in the last place of the exact value; all borders (0.25, 0.75, 1.25, ... 5) have 21 zeros at the
-        // end of their significands.  (Not below 8.5: a factor beyond fp32.)
-        doubt |= ((__builtin_bit_cast(uint32_t, u[j]) + 4) & 0x1FFFFFu) < 8 || !(__builtin_fabsf(u[j]) < 8.5f);
+        // end of their significands
+        near = min(near, (__builtin_bit_cast(uint32_t, u[j]) + 4) & 0x1FFFFFu);
       }
       uint32_t code = mx::codes8(u);
-      if (__builtin_amdgcn_ballot_w64(doubt)) {
+      // (the last: a factor beyond fp32)
+      if (__builtin_amdgcn_ballot_w64(near < 8 || !(f32 < 0x1p100f))) {
         code = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) code |= fp4_code((double)p[j] * f) << (4 * j);

@@ -224,7 +224,7 @@ def test_scales_of_the_whole_range():
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("M,N,K", [(1, 33, 16384), (2, 20, 8192), (3, 48, 5461), (4, 65, 4096), (4, 16, 4097), (1, 70, 16385), (2, 5, 1),
-                                   (4, 1, 129), (3, 4096, 513), (1, 300, 255)])
+                                   (4, 1, 129), (3, 4096, 513), (1, 300, 255), (1, 33, 65536), (4, 20, 8192), (2, 20, 16384)])
 def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
     """Quantized and multiplied in one launch, at the ends of what that takes: the bits of the two steps, also from rows
     that lie apart and start at odd elements."""
@@ -302,3 +302,18 @@ def test_output_past_32_bits():
     for rows in (slice(0, 40), slice(70000, 70040), slice(M - 40, M)):
         part = bq.atom_gemm_mxfp4(Xq[rows].contiguous(), sx[:, rows].contiguous(), Wq, sw, K)
         torch.testing.assert_close(Y[rows], part, rtol=0, atol=0)
+
+
+def test_rows_past_32_bits():
+    """More than 2^32 bytes of X: the last rows as by themselves, and back."""
+    rows, K = 300000, 8192
+    say(f"[mxfp4 quantize] {rows}x{K}")
+    x = torch.zeros(rows, K, dtype=torch.float16, device="cuda")
+    at = torch.tensor([0, 131071, 262143, 262144, rows - 1], device="cuda")
+    x[at] = make(len(at), K, torch.float16, 7)
+    Xq, sx = bq.atom_quantize_mxfp4(x)
+    check_codes(Xq[at], sx[:, at], x[at])
+    assert int((Xq != 0).any(1).sum()) == len(at)
+    back = bq.atom_dequantize_mxfp4(Xq, sx, K)
+    torch.testing.assert_close(back[at], bq.atom_dequantize_mxfp4(Xq[at], sx[:, at].contiguous(), K), rtol=0, atol=0)
+    assert int((back != 0).any(1).sum()) == len(at)

@@ -215,3 +215,35 @@ def test_dequantize_w8a8(rows, K, dtype):
     assert bq.atom_dequantize_w8a8(Xq, sx, K, X=X[:rows]).dtype is t
     torch.testing.assert_close(X[:rows], want, rtol=0, atol=0)
     assert torch.all(X[rows] == 7)
+
+
+def test_rows_past_32_bits():
+    """More than 2^32 bytes of X, and of H: the last rows as by themselves."""
+    rows, K, t = 300000, 8192, torch.bfloat16
+    say(f"[norm] {rows}x{K}")
+    x, w = torch.zeros(rows, K, dtype=t, device="cuda"), weights(K, t)
+    at = torch.tensor([0, 131071, 262143, 262144, rows - 1], device="cuda")
+    x[at] = make(len(at), K, t, 7)
+    for call in (bq.atom_rmsnorm_w8a8, bq.atom_rmsnorm_mxfp4):
+        Xq, sx, H = call(x, w, 1e-5, residual=x)
+        q, s, h = call(x[at], w, 1e-5, residual=x[at])
+        torch.testing.assert_close(Xq[at], q, rtol=0, atol=0)
+        torch.testing.assert_close(sx[at] if sx.dim() == 1 else sx[:, at], s, rtol=0, atol=0)
+        torch.testing.assert_close(H[at], h, rtol=0, atol=0)
+        some = Xq != 0 if Xq.dtype == torch.int8 else (Xq & 0x77) != 0      # (a zero keeps its sign: a negative weight's)
+        assert int(some.any(1).sum()) == int((H != 0).any(1).sum()) == len(at)
+
+
+def test_scales_next_to_nothing():
+    """bf16 weights so small that a row's scale is one of fp32's smallest numbers: codes stay within +-127."""
+    x = make(6, 300, torch.bfloat16, 4)
+    for e in (-118, -126, -130, -133):
+        w = torch.full((300,), 2.0**e, device="cuda").bfloat16()
+        y, _ = O.rmsnorm(f32(x), f32(w), 1e-6)
+        if e > -120:
+            check(x, w, 1e-6)
+        Xq, sx, _ = bq.atom_rmsnorm_w8a8(x, w, 1e-6)
+        assert int(Xq.min()) >= -127
+        # products below 2^-126 are rounded to steps of 2^-149, which is up to 2^-149 / 2 of y / h before the factor
+        back = Xq[:, :300].double().cpu().numpy() * sx.double().cpu().numpy()[:, None]
+        assert (np.abs(back - y) <= np.abs(y).max(1, keepdims=True) * 2.0**-6 + 2.0**-147).all()
