@@ -17,8 +17,8 @@
 //     straight into LDS (LDS-DMA).  At the largest sizes the power that random operands draw bounds it: 4096 x 28672 x 8192
 //     (M x N x K) takes 449 us, 4.3 PFLOP/s, with zeros 348 us; the same kernel without copies and LDS reads 327 and 266 us (the
 //     matrix cores alone at the clock that power leaves), without its stores 416 and 308.  The library's product reaches 3.0 PFLOP/s
-//     there.  Below that it is bound by how fast a compute unit gets lines that miss its L2: 2048 x 4096 x 11008 53 us (3.5
-//     PFLOP/s), 48 with zeros, 46 the copies alone.
+//     there.  Below that it is bound by how fast a compute unit gets lines that miss its L2: 2048 x 4096 x 11008 51 us (3.6
+//     PFLOP/s), 47 with zeros, 46 the copies alone.
 //     On the way there (4096 x 28672 x 8192 and 2048 x 4096 x 11008): 485 and 61 us with each wave's scale words loaded into
 //     registers and a stage's copies issued in one slice; 478 and 62 with all of a stage's operands in registers after its first slice
 //     (256 x 256 tiles); 449 and 53 with scales through LDS and copies spread over the slices.
@@ -60,6 +60,16 @@ __device__ __forceinline__ float biased(float acc, float bias) {
   return y;
 }
 
+// Tile order: bands of tile rows, the rows fastest inside a band, so that the tiles that share an L2 form a block.  Four rows of
+// 256 tokens a band: 2048 x 4096 x 11008 51.3 us, with eight 52.2; eight of 128: 2048 x 11008 x 4096 65.4 us, with four 66.5.
+template <int BM>
+__device__ __forceinline__ int2 tile_at(int lin, int tiles_m, int tiles_n) {
+  constexpr int kBand = BM == 256 ? 4 : 8;
+  const int band = lin / (kBand * tiles_n), first = band * kBand, rows = min(tiles_m - first, kBand);
+  const int in_band = lin - band * kBand * tiles_n;
+  return int2{first + in_band % rows, in_band / rows};
+}
+
 // BM x BN output tile of four waves (2 x 2), RING stage buffers.  kDivided (K may be divided): with splits > 1 piece p of tile t is
 // workgroup p * tiles + t and writes its fp32 tile to part[(p * tiles + t) * BM * BN].
 template <class T, int BM, int BN, int RING, int WAVES, bool kDivided, bool kEarly, bool kBias>
@@ -90,7 +100,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     const int per = tiles / 8, more = tiles % 8, x = lin % 8;
     lin = x * per + min(x, more) + lin / 8;
   }
-  const int2 tc = tile_coords(lin, tiles_m, tiles_n);
+  const int2 tc = tile_at<BM>(lin, tiles_m, tiles_n);
   const int m0 = tc.x * BM, n0 = tc.y * BN;
   const int sa = kDivided ? (int)((int64_t)stages * piece / splits) : 0;
   const int sb = kDivided ? (int)((int64_t)stages * (piece + 1) / splits) : stages;
@@ -368,7 +378,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ p
                                                      int N, uint16_t* __restrict__ Y, int tiles, int splits) {
   constexpr int kPerTile = BM * BN / 4 / 256;             // workgroups per tile
   const int lin = blockIdx.x / kPerTile;
-  const int2 tc = tile_coords(lin, (M + BM - 1) / BM, (N + BN - 1) / BN);
+  const int2 tc = tile_at<BM>(lin, (M + BM - 1) / BM, (N + BN - 1) / BN);
   const int e4 = (blockIdx.x % kPerTile) * 256 + threadIdx.x;
   const int r = e4 / (BN / 4), c = e4 % (BN / 4) * 4;
   const int m = tc.x * BM + r, n = tc.y * BN + c;

@@ -3,7 +3,8 @@
 //
 // What bounds it: latency.  Every workgroup scans the sequences for itself (a tile of as many as it has threads at a
 // time), which costs less than a launch that does it once, and then takes its own rows: a row's sequence is found by
-// bisection in LDS, its page is an entry of the table or of the pool.  Decoding steps take one workgroup.
+// bisection in LDS, its page is an entry of the table or of the pool.  Measured: 64 sequences, a token each 3.1 us, 256 sequences,
+// 230528 tokens 4.3 us; pages of 64 and 1024 sequences given back 3.1 and 4.3 us (a launch alone is 1.8).
 //
 // Sums saturate where they no longer matter (behind the last row, behind the pool's end), so 32 bits hold them.
 #include "kv4_layout.h"
@@ -179,12 +180,19 @@ __global__ __launch_bounds__(THREADS) void release_kernel(Kv4Release a, int copy
 }  // namespace
 
 hipError_t launch_kv4_extend(const Kv4Extend& a, hipStream_t stream) {
-  // one workgroup walks through a few thousand rows in about the time that it takes to scan the sequences
-  const int span = a.total <= 4096 ? 4096 : 2048;
+  // A row a thread, and at most 512 workgroups where each has many sequences to scan.  Us, by rows of a workgroup of 256 threads (64
+  // sequences): 288 rows in all 3.3 (256), 3.9 (512); 4096 rows 3.5, 4.0 and 11.8 (4096); 256 sequences, 230528 rows 4.3 and 4.5; 1024 sequences,
+  // 262144 rows in workgroups of 1024 threads 5.2 (1024), 5.8 (2048).  In place one workgroup takes up to 1024 rows (5.4
+  // us) rather than a second launch.
+  const int threads = a.batch <= 256 ? 256 : 1024;
+  const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+  int span = threads;
+  if (in_place && a.total <= 1024) span = 1024;
+  if (a.batch > 1024 && a.total > 512 * span) span = (a.total + 511) / 512;
   const int groups = (a.total + span - 1) / span;
-  const bool later = groups > 1 && (a.lens_out == a.lens || a.state_out == a.state);
+  const bool later = groups > 1 && in_place;
   auto go = [&](int g, int n, int commit) {
-    if (a.batch <= 256 && g == 1)
+    if (threads == 256)
       hipLaunchKernelGGL((extend_kernel<256>), dim3(g), dim3(256), 0, stream, a, n, commit);
     else
       hipLaunchKernelGGL((extend_kernel<1024>), dim3(g), dim3(1024), 0, stream, a, n, commit);
@@ -195,8 +203,10 @@ hipError_t launch_kv4_extend(const Kv4Extend& a, hipStream_t stream) {
 }
 
 hipError_t launch_kv4_release(const Kv4Release& a, hipStream_t stream) {
-  const int groups = a.batch < 1024 ? (a.batch + 15) / 16 : 64;
-  const bool later = groups > 1 && (a.lens_out == a.lens || a.state_out == a.state);
+  // A sequence a wave; in place one workgroup takes up to 64 sequences rather than a second launch.
+  const bool in_place = a.lens_out == a.lens || a.state_out == a.state;
+  const int groups = in_place && a.batch <= 64 ? 1 : a.batch < 1024 ? (a.batch + 15) / 16 : 64;
+  const bool later = groups > 1 && in_place;
   auto go = [&](int g, int copy, int commit) {
     hipLaunchKernelGGL((release_kernel<1024>), dim3(g), dim3(1024), 0, stream, a, copy, commit);
   };

@@ -62,7 +62,7 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
     `total` is the number of rows that hold all new tokens, one sequence behind the other.  Returns (slots int64 [total]: each
     row's slot, -1 for rows behind the last one; q_start int32 [batch + 1]; lens_out int32 [batch], with the new tokens; state_out
     int32 [2]: the pool's new state).  The inputs stay as they were but for the table, unless lens_out is lens or state_out
-    the pool's state, which are then replaced (more than 4096 rows take a second launch for it).  If the pool holds
+    the pool's state, which are then replaced (more than 1024 rows take a second launch for it).  If the pool holds
     too few pages nothing is taken: all slots are -1, lengths and pool stay, state_out[1] says how many are missing."""
     free, state = _pool(pool)
     total, page = int(total), int(page)
@@ -93,7 +93,7 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
 def atom_kv4_release(done, lens, table, pool, page, lens_out=None, state_out=None, stream=None):
     """Give the pages of the sequences with done[b] (bool [batch]) back to the pool, whose `free` is written behind its free
     pages.  Returns (lens_out, state_out): lengths, 0 where done, and the pool's new state; either may be given as its input,
-    which is then replaced (more than 16 sequences take a second launch for it)."""
+    which is then replaced (more than 64 sequences take a second launch for it)."""
     free, state = _pool(pool)
     page = int(page)
     if stream is None and lens_out is None and state_out is None and _bq._SHORT is not None:

@@ -60,7 +60,7 @@ def check_release(done, lens, table, free, st, page):
 
 CASES = [(1, 1, 16, 0, 1), (1, 3, 16, 20, 28), (5, 4, 16, 40, 1), (64, 8, 64, 400, 1), (64, 8, 64, 400, 5), (255, 4, 128, 300, 200),
          (256, 20, 16, 200, 100), (257, 4, 32, 90, 30), (300, 3, 256, 500, 1), (1000, 4, 16, 40, 20), (1024, 3, 16, 40, 1),
-         (1025, 3, 16, 40, 1), (1025, 5, 16, 40, 20), (3000, 2, 16, 30, 2), (4, 300, 16, 100, 3000), (2, 200, 256, 5, 20000)]
+         (1025, 3, 16, 40, 1), (1025, 5, 16, 40, 20), (3000, 2, 16, 30, 2), (4, 300, 16, 100, 3000), (2, 200, 256, 5, 20000), (1500, 70, 16, 40, 1000)]
 
 
 @pytest.mark.parametrize("batch,width,page,longest,most", CASES)
@@ -104,7 +104,7 @@ def test_values_out_of_range():
             check_release(new > 2, lens, table, free, np.array([pool, 9]), 16)
 
 
-@pytest.mark.parametrize("batch,total", [(3, 60), (300, 900), (700, 9000), (2000, 4000), (2000, 30000)])
+@pytest.mark.parametrize("batch,total", [(3, 60), (60, 1000), (65, 1030), (300, 900), (700, 9000), (2000, 4000), (2000, 30000)])
 def test_in_place(batch, total):
     """Lengths and the pool's state replaced, in one launch or two: the results of a call with outputs of their own."""
     say(f"[pages in place] {batch} sequences, {total} rows")
