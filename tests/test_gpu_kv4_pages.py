@@ -175,3 +175,19 @@ def test_streams_and_graphs():
         lens, table, st = want[2], want[3], want[4]
         for a, b in zip((slots, start, l, t, pool.state, pool.free), (*want, free)):
             np.testing.assert_array_equal(a.cpu().numpy(), b)
+
+
+def test_very_many_sequences():
+    """More sequences than workgroups have threads many times over: scans of 69 tiles, in several workgroups and in place."""
+    batch = 70001
+    say(f"[pages] {batch} sequences")
+    lens, table, free, st = state(batch, 2, 16, 20, 8)
+    new = np.random.default_rng(9).integers(0, 4, batch)
+    total = int(new.sum()) + 10
+    want = check_extend(lens, new, table, free, st, 16, total)
+    l, t, pool = dev(lens), dev(table), bq.KV4Pool(dev(free), dev(st))
+    bq.atom_kv4_extend(l, dev(new), t, pool, 16, total, lens_out=l, state_out=pool.state)
+    for a, b in zip((l, t, pool.state), (want[2], want[3], want[4])):
+        np.testing.assert_array_equal(a.cpu().numpy(), b)
+    check_extend(lens, np.where(np.arange(batch) % 1000 == 0, 1, 0), table, free, st, 16, 71)
+    check_release(np.arange(batch) % 3 == 0, want[2], want[3], free, want[4], 16)

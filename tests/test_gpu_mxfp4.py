@@ -249,7 +249,7 @@ def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
 
 def test_two_graphs_and_eager_calls_between():
     """Two captured graphs of the same shapes and eager calls in turn: none reads another's workspace."""
-    for M, N, K in ((2, 300, 1000), (64, 128, 4096), (64, 128, 8192)):
+    for M, N, K in ((2, 300, 1000), (64, 128, 4096), (64, 4096, 8192)):      # the last divides K
         Wq, sw = bq.atom_quantize_mxfp4(make(N, K, torch.float16, 1, 0.02))
         xs = [make(M, K, torch.float16, 2 + i) for i in range(2)]
         bq.linear_mxfp4(xs[0], Wq, sw)
@@ -317,3 +317,54 @@ def test_rows_past_32_bits():
     back = bq.atom_dequantize_mxfp4(Xq, sx, K)
     torch.testing.assert_close(back[at], bq.atom_dequantize_mxfp4(Xq[at], sx[:, at].contiguous(), K), rtol=0, atol=0)
     assert int((back != 0).any(1).sum()) == len(at)
+
+
+@pytest.mark.parametrize("M,N,K", [(2100001, 3, 5), (5, 2000003, 40), (70001, 33, 300), (3, 70001, 257), (1, 200003, 1)])
+def test_tall_and_wide(M, N, K):
+    """Far more rows or columns than a launch has workgroups in one direction: the ends and the middle against fp64."""
+    say(f"[mxfp4 linear] {M}x{N}x{K}")
+    Xq, sx = codes(M, K, 7)
+    Wq, sw = codes(N, K, 8)
+    Y = bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K, dtype=torch.bfloat16)
+    part = lambda n: torch.cat([torch.arange(min(n, 50)), torch.arange(max(0, n // 2 - 30), n // 2), torch.arange(max(0, n - 50), n)]).cuda()  # noqa: E731
+    m, n = part(M), part(N)
+    y = values(Xq[m], sx[:, m]) @ values(Wq[n], sw[:, n]).t().contiguous()
+    torch.testing.assert_close(Y[m][:, n], y.float().bfloat16(), rtol=0, atol=0)
+    torch.testing.assert_close(Y[m], bq.atom_gemm_mxfp4(Xq[m], sx[:, m].contiguous(), Wq, sw, K, dtype=torch.bfloat16), rtol=0, atol=0)
+
+
+def test_too_little_workspace():
+    """Less scratch than a division needs: the undivided product's bits, and nothing written into it."""
+    M, N, K = 64, 4096, 8192
+    Xq, sx = bq.atom_quantize_mxfp4(make(M, K, torch.float16, 1))
+    Wq, sw = bq.atom_quantize_mxfp4(make(N, K, torch.float16, 2, 0.02))
+    need = bq.atom_gemm_mxfp4_workspace_bytes(M, N, K)
+    assert need > 0
+    want = bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K)
+    for size in (16, need - 16):
+        ws = torch.full((size,), 0xA5, dtype=torch.uint8, device="cuda")
+        torch.testing.assert_close(bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K, workspace=ws), want, rtol=0, atol=0)
+        assert torch.all(ws == 0xA5)
+    guard = torch.full((need + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K, workspace=guard[:need])
+    assert torch.all(guard[need:] == 0xA5)
+    lin = bq.atom_linear_mxfp4_workspace_bytes(M, N, K)
+    guard = torch.full((lin + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    x = make(M, K, torch.float16, 1)
+    torch.testing.assert_close(bq.linear_mxfp4(x, Wq, sw, workspace=guard[:lin]), bq.linear_mxfp4(x, Wq, sw), rtol=0, atol=0)
+    assert torch.all(guard[lin:] == 0xA5)
+
+
+def test_outputs_stay_inside():
+    """Bytes around every output of every kernel keep their values (rows and columns that end inside a tile)."""
+    for M, N, K in ((3, 130, 127), (33, 65, 1000), (333, 777, 1155), (131, 6003, 300), (131, 11003, 2000), (201, 16403, 2300), (501, 16403, 2600),
+                    (300, 777, 4100)):
+        Xq, sx = codes(M, K, 9)
+        Wq, sw = codes(N, K, 10)
+        flat = torch.full((M * N + 64,), 7.0, dtype=torch.float16, device="cuda")
+        Y = flat[32:32 + M * N].view(M, N)
+        need = bq.atom_gemm_mxfp4_workspace_bytes(M, N, K)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+        bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K, Y=Y, workspace=ws)
+        torch.testing.assert_close(Y, bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, K, workspace=ws), rtol=0, atol=0)
+        assert torch.all(flat[:32] == 7) and torch.all(flat[32 + M * N:] == 7)
