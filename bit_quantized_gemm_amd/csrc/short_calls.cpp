@@ -25,6 +25,7 @@ namespace {
 // ---- the C entry points, by name
 #define ATOM_CALLS(X)                                                                                                     \
   X(atom_quantize_mxfp4) X(atom_dequantize_mxfp4) X(atom_linear_mxfp4_workspace_bytes) X(atom_linear_mxfp4)               \
+  X(atom_gemm_mxfp4)                                                                                                      \
   X(atom_rmsnorm_w8a8) X(atom_rmsnorm_mxfp4) X(atom_dequantize_w8a8) X(atom_kv4_extend) X(atom_kv4_release)
 struct {
 #define X(name) decltype(&::name) name;
@@ -140,6 +141,33 @@ PyObject* linear_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {   // X, Wq
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_linear_mxfp4(x->data_ptr(), ld, kind(*x), w->data_ptr(), s->data_ptr(), bias, (int32_t)M, (int32_t)N, (int32_t)K,
                                  y.data_ptr(), p, need, stream);
+  });
+  return status ? otherwise() : THPVariable_Wrap(std::move(y));
+  END_HANDLE_TH_ERRORS
+}
+
+PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {   // Xq, sx, Wq, sw, K, bias, bf16, workspace
+  HANDLE_TH_ERRORS
+  const at::Tensor *x = n == 8 ? tensor(a[0]) : nullptr, *s = x ? tensor(a[1]) : nullptr, *w = s ? tensor(a[2]) : nullptr,
+                   *t = w ? tensor(a[3]) : nullptr, *scratch = nullptr;
+  int64_t K;
+  if (!t || !lib.atom_gemm_mxfp4 || !x->is_cuda() || x->dim() != 2 || w->dim() != 2 || !integer(a[4], K) || K < 1 || K > ATOM_MAX_K)
+    return otherwise();
+  const Here h;
+  const int64_t M = x->size(0), N = w->size(0), g = groups_of(K), bytes = g * (ATOM_MX_GROUP / 2);
+  const bool bf16 = PyObject_IsTrue(a[6]) == 1;
+  const void* bias;
+  if (M < 1 || M > ATOM_MAX_ROWS || N < 1 || N > ATOM_MAX_ROWS || !dense(h, x, at::kByte, {M, bytes}) || !dense(h, s, at::kByte, {g, M, 8}) ||
+      !dense(h, w, at::kByte, {N, bytes}) || !dense(h, t, at::kByte, {g, N, 8}) || !vector(h, a[5], bf16 ? at::kBFloat16 : at::kHalf, N, bias))
+    return otherwise();
+  if (a[7] != Py_None) {
+    scratch = tensor(a[7]);
+    if (!scratch || scratch->dim() != 1 || !dense(h, scratch, at::kByte, {scratch->numel()})) return otherwise();
+  }
+  at::Tensor y = fresh({M, N}, bf16 ? at::kBFloat16 : at::kHalf, h);
+  const int status = on_stream(h, [&](void* stream) {
+    return lib.atom_gemm_mxfp4(x->data_ptr(), s->data_ptr(), w->data_ptr(), t->data_ptr(), bias, (int32_t)M, (int32_t)N, (int32_t)K, bf16,
+                               y.data_ptr(), scratch ? scratch->data_ptr() : nullptr, scratch ? scratch->numel() : 0, stream);
   });
   return status ? otherwise() : THPVariable_Wrap(std::move(y));
   END_HANDLE_TH_ERRORS
@@ -294,7 +322,7 @@ PyObject* kv4_release(PyObject*, PyObject* const* a, Py_ssize_t n) {   // done, 
 
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, "bind(addresses, stream): the C entry points by name, and the function that gives a device's current stream"},
-                         FAST(linear_mxfp4), FAST(quantize_mxfp4), FAST(dequantize_mxfp4), FAST(dequantize_w8a8), FAST(rmsnorm_w8a8),
+                         FAST(linear_mxfp4), FAST(gemm_mxfp4), FAST(quantize_mxfp4), FAST(dequantize_mxfp4), FAST(dequantize_w8a8), FAST(rmsnorm_w8a8),
                          FAST(rmsnorm_mxfp4), FAST(kv4_extend), FAST(kv4_release), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_short", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -123,6 +123,12 @@ def atom_gemm_mxfp4(Xq, sx, Wq, sw, K, bias=None, Y=None, dtype=None, workspace=
     """Y [M, N] of packed operands; its type is Y's, or the bias's, or `dtype` (default fp16).  With a
     workspace (1-D uint8, ``atom_gemm_mxfp4_workspace_bytes``) grids of few output tiles divide K."""
     torch = _bq._torch()
+    if stream is None and Y is None and _bq._SHORT is not None:
+        kind = dtype if dtype is not None else getattr(bias, "dtype", torch.float16)
+        if kind is torch.float16 or kind is torch.bfloat16:
+            Y = _bq._SHORT.gemm_mxfp4(Xq, sx, Wq, sw, K, bias, kind is torch.bfloat16, workspace)
+            if Y is not None:
+                return Y
     K = int(K)
     rb, g = packed(K)
     M, _ = _bq._mat(Xq, "Xq")

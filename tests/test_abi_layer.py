@@ -257,7 +257,7 @@ def test_short_calls_leave_the_rest_to_the_full_checks(lib):
     class Sub(torch.Tensor):
         pass
     odd = [None, 0, 1.5, "x", [t], t, i, t.numpy(), t.as_subclass(Sub), torch.nn.Parameter(t), object(), 1 << 80, -1]
-    sizes = {"quantize_mxfp4": 1, "linear_mxfp4": 4, "dequantize_mxfp4": 4, "dequantize_w8a8": 4, "rmsnorm_w8a8": 4, "rmsnorm_mxfp4": 4,
+    sizes = {"quantize_mxfp4": 1, "linear_mxfp4": 4, "gemm_mxfp4": 8, "dequantize_mxfp4": 4, "dequantize_w8a8": 4, "rmsnorm_w8a8": 4, "rmsnorm_mxfp4": 4,
              "kv4_extend": 7, "kv4_release": 6}
     for name, n in sizes.items():
         f = getattr(short, name)

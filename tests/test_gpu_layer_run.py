@@ -189,7 +189,11 @@ def test_refusals_on_the_device():
         *(lambda a=a: bq.atom_dequantize_w8a8(*a) for a in ((Q8, s8, 0), (Q8, s8, 385), (Q8, s8, 200), (Q8, s8[:3], 300), (Q8.view(u8), s8, 300),
                                                             (Q8, s8, 300, f32), (Q8, s8.half(), 300), (Q8, s8.cpu(), 300))),
         *(lambda a=a: bq.atom_gemm_mxfp4(*a) for a in ((Xq, sx, Wq, sw, 600), (Xq, sx[:1], Wq, sw, 300), (Xq, sx, Wq[:, :128], sw, 300),
-                                                       (Xq, sx, Wq, sw, 300, z(5)), (Xq, sx, Wq, sw, 300, None, z(4, 5)))),
+                                                       (Xq, sx, Wq, sw, 300, z(5)), (Xq, sx, Wq, sw, 300, None, z(4, 5)),
+                                                       (Xq, sx, Wq, sw, 300, z(6).bfloat16(), None, torch.float16),
+                                                       (Xq, sx, Wq, sw, 300, None, None, f32), (Xq, sx, Wq.cpu(), sw, 300),
+                                                       (Xq, sx, Wq, sw, 300, None, None, None, z(9)),
+                                                       (Xq, sx, Wq, sw, 300, None, None, None, z(4, 4, dtype=u8)))),
         *(lambda f=f, k=k: f(**{**dict(X=X, weight=W), **k}) for f in (bq.atom_rmsnorm_w8a8, bq.atom_rmsnorm_mxfp4) for k in (
             dict(X=z()), dict(X=X[0]), dict(X=z(0, 300)), dict(X=X.float()), dict(X=X[:, ::2]), dict(X=z(300, 4).t()), dict(weight=W[:299]),
             dict(weight=W.bfloat16()), dict(weight=W.cpu()), dict(weight=z(600)[::2]), dict(residual=X[:3]), dict(residual=X.bfloat16()),
@@ -228,6 +232,8 @@ def calls(t=torch.float16):
     table, pool = torch.arange(16, dtype=torch.int32, device="cuda").view(4, 4), bq.kv4_pool(30)
     return [lambda s: bq.linear_mxfp4(X, Wq, sw, stream=s), lambda s: bq.linear_mxfp4(X[:2], Wq, sw, b, stream=s),
             lambda s: bq.linear_mxfp4(X[::2], Wq, sw, b, stream=s), lambda s: bq.atom_quantize_mxfp4(X, stream=s),
+            lambda s: bq.atom_gemm_mxfp4(*q4, Wq, sw, 700, dtype=t, stream=s), lambda s: bq.atom_gemm_mxfp4(*q4, Wq, sw, 700, b, stream=s),
+            lambda s: bq.atom_gemm_mxfp4(*q4, Wq, sw, 700, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"), stream=s),
             lambda s: bq.atom_dequantize_mxfp4(*q4, 700, dtype=t, stream=s), lambda s: bq.atom_dequantize_w8a8(*q8, 700, dtype=t, stream=s),
             *(lambda s, f=f, r=r: f(X, W, 1e-5, residual=r, stream=s) for f in (bq.atom_rmsnorm_w8a8, bq.atom_rmsnorm_mxfp4)
               for r in (None, X.flip(0).contiguous())),
