@@ -7,8 +7,8 @@
 // Scales lie group by group ([groups, rows, 8]), so a line of them belongs to 16 rows: a workgroup takes neighbouring rows,
 // whose pieces of it meet in one L2.
 //
-// Measured: 8192 x 8192 38 us (4.4 TB/s, a copy of memory reaches 4.75), 2048 x 11008 14.6 us, 16 x 4096 1.9 us, of which the launch is
-// most; back to values 8192 x 8192 38 us.
+// Measured: 8192 x 8192 36 us (4.7 TB/s, a copy of memory reaches 4.75; 38 with the elements multiplied in fp32 before the conversion),
+// 2048 x 11008 13.3 us (14.6), 16 x 4096 2.1 us, of which the launch is most; back to values 8192 x 8192 38 us.
 #include "mxfp4_row.h"
 
 namespace atom {
@@ -83,8 +83,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
 }
 
 // Whether there are workgroups enough for several rows each.
-bool many(int rows, int Kp, int per, int columns) {
-  return (int64_t)((rows + per - 1) / per) * ((Kp + columns - 1) / columns) >= 2048;
+bool many(int rows, int Kp, int per, int columns, int64_t enough) {
+  return (int64_t)((rows + per - 1) / per) * ((Kp + columns - 1) / columns) >= enough;
 }
 
 }  // namespace
@@ -98,11 +98,11 @@ hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int 
     hipLaunchKernelGGL(kernel, dim3((rows + per - 1) / per, (Kp + columns - 1) / columns), dim3(kThreads), 0, stream, X, ldx, rows, K,
                        Kp, Xq, sx);
   };
-  // (us, rows x columns of a workgroup 4 x 512, 16 x 512, 8 x 1024: 512 x 4096 2.8, 3.2, 3.2; 2048 x 4096 6.9, 6.5, 6.5; 4096 x 8192 19.8,
-  // 20.6, 19.7; 2048 x 11008 16.6, 14.6, 14.6; unaligned 333 x 1155 2.4 and 4.3)
+  // (us, rows x columns of a workgroup 4 x 512, 16 x 512, 8 x 1024: 512 x 4096 2.9, 3.2, 3.2; 1024 x 4096 3.6, 3.9, 4.0; 2048 x 4096 6.8, 6.2, 6.2;
+  // 2048 x 11008 16.2, 14.3, 14.2; 8192 x 8192 36.3, 38.3, 37.8; unaligned 333 x 1155 2.3, 3.5, 3.2, 3000 x 1155 4.4, 5.5, 5.1)
   auto pick = [&](auto type) {
     using T = decltype(type);
-    if (many(rows, Kp, 4, 512)) vec ? go(quantize_kernel<T, true, 2, 2>, 8, 1024) : go(quantize_kernel<T, false, 2, 2>, 8, 1024);
+    if (many(rows, Kp, 4, 512, 4096)) vec ? go(quantize_kernel<T, true, 2, 2>, 8, 1024) : go(quantize_kernel<T, false, 2, 2>, 8, 1024);
     else vec ? go(quantize_kernel<T, true, 1, 1>, 4, 512) : go(quantize_kernel<T, false, 1, 1>, 4, 512);
   };
   bf16 ? pick(Bf16{}) : pick(Fp16{});
@@ -119,7 +119,7 @@ hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int row
   auto pick = [&](auto type) {
     using T = decltype(type);
     // (us, 4 and 16 rows: 16 x 4096 2.0 and 3.3, 8192 x 8192 49 and 38: a line of scales is read once for 16 rows)
-    if (many(rows, Kp, 16, 512)) vec ? go(dequantize_kernel<T, true, 16>, 16) : go(dequantize_kernel<T, false, 16>, 16);
+    if (many(rows, Kp, 16, 512, 2048)) vec ? go(dequantize_kernel<T, true, 16>, 16) : go(dequantize_kernel<T, false, 16>, 16);
     else vec ? go(dequantize_kernel<T, true, 4>, 4) : go(dequantize_kernel<T, false, 4>, 4);
   };
   bf16 ? pick(Bf16{}) : pick(Fp16{});

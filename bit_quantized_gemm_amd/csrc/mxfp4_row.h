@@ -36,8 +36,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   const int e = (int)(top >> 23);
   return e == 255 ? kNanScale : (uint32_t)max(e - 2, 0);
 }
-// 1 / 2^e of a scale byte below 253, exact: 2^127 for byte 0 (2^-127).
-__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __builtin_bit_cast(float, (254u - byte) << 23); }
 
 // The codes of eight values in units of their scale: nearest, ties to the even code, saturating (the conversion's
 // own rounding; walked over all fp16 values and the borders' neighbours by a test).
@@ -49,18 +47,36 @@ __device__ __forceinline__ uint32_t codes8(const float (&u)[8]) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[6], u[7], 1.0f, 3);
 }
 
-// Codes and scale byte of a lane's eight 16-bit elements; all lanes of the wave call it.  x * 2^-e is exact but for
-// values below 2^-125 of the block's largest, which round to zero either way.
+// The largest magnitude of eight 16-bit elements, as bits.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t max8(u32x4 w) {
+  u16x2 m[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m[j] = __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu);
+  const u16x2 t = __builtin_elementwise_max(__builtin_elementwise_max(m[0], m[1]), __builtin_elementwise_max(m[2], m[3]));
+  return max((uint32_t)t[0], (uint32_t)t[1]);
+}
+
+// The codes of two elements into byte J of c: elements / scale, of which the conversion takes the exponent alone.
+template <int J>
+__device__ __forceinline__ uint32_t codes2(Fp16, uint32_t c, uint32_t w, float scale) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(h2, w), scale, J);
+}
+template <int J>
+__device__ __forceinline__ uint32_t codes2(Bf16, uint32_t c, uint32_t w, float scale) {
+  typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(b2, w), scale, J);
+}
+
+// Codes and scale byte of a lane's eight 16-bit elements; all lanes of the wave call it.  The conversion takes the elements as
+// they are and rounds once; byte << 23 is 2^(byte - 127) as it reads a scale, with byte 0 as well.
 template <class T>
 __device__ __forceinline__ uint32_t quantize8(u32x4 w, uint32_t& byte) {
-  byte = scale_byte(__builtin_bit_cast(uint32_t, T::load(block_max(w8a8::max8(w, 0)))));
-  const bool nan = byte == kNanScale;
-  const float inv = nan ? 0.0f : inverse_scale(byte);
-  float u[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) u[j] = elem<T>(w[j / 2], j & 1) * inv;
-  const uint32_t c = codes8(u);
-  return nan ? 0u : c;
+  byte = scale_byte(__builtin_bit_cast(uint32_t, T::load(block_max(max8(w)))));
+  const float scale = __builtin_bit_cast(float, byte << 23);
+  const uint32_t c = codes2<3>(T{}, codes2<2>(T{}, codes2<1>(T{}, codes2<0>(T{}, 0, w[0], scale), w[1], scale), w[2], scale), w[3], scale);
+  return byte == kNanScale ? 0u : c;
 }
 
 }  // namespace mx
