@@ -26,8 +26,8 @@
 //     waves divide K, each loads its operands straight into registers, all of them at once where K is short; the waves' sums
 //     meet in LDS.  Weights from HBM: 16 x 4096 x 4096 5.0 us, 16 x 11008 x 4096 9.6 us (2.5 TB/s; as many bytes of codes from
 //     the L2), 1 x 11008 x 4096 7.7 us.
-//   linear_rows_kernel: the same for at most four tokens with the quantizer in front, one launch for two: 1 x 4096 x 4096 4.9 us
-//     against 6.5.
+//   linear_rows_kernel: the same for at most 16 tokens with the quantizer in front, one launch for two (us): 1 x 4096 x 4096 4.5 and
+//     6.3, 4 x 11008 x 4096 8.2 and 10.1, 16 x 11008 x 4096 10.1 and 11.3, 16 x 4096 x 4096 7.8 and 7.0.
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "gemm_tile.h"
@@ -468,77 +468,131 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restri
   }
 }
 
-// The layer for at most MR <= 4 tokens in one launch: every workgroup quantizes the tokens for itself, into LDS, while its
-// first weights are on their way; then as above, against 16 columns.  Rows in LDS lie 16 bytes (their scales 4) apart beyond
-// their own length, so that their reads do not meet in one bank.  (16 tokens so: 16 x 4096 x 4096 9.0 us, in two launches 8.1.)
-using mx::kOneLaunch;
-__host__ __device__ constexpr int lds_codes(int groups) { return groups * kStage + 16; }
-__host__ __device__ constexpr int lds_scales(int groups) { return groups * 8 + 4; }
+// The layer for at most 16 tokens in one launch: every workgroup quantizes them for itself, into LDS, then as above, against 16 CT
+// columns.  Its first loads of tokens are under way before those of its weights, since loads arrive in order, and its weights
+// while it quantizes.  Addresses are a wave's, in scalar registers, and rows of LDS whole units, so that a unit takes few
+// instructions besides the quantizer's own: 16 x 4096 x 4096 (M x N x K) 9.2 us with an index a lane, 8.2 so, 7.7 without
+// conditions on the stores.  Rows in LDS lie 16 bytes (their scales 4) apart beyond their units, so that their reads do not meet in one bank.
+__host__ __device__ constexpr int lds_codes(int pairs) { return pairs * 2 * kStage + 16; }
+__host__ __device__ constexpr int lds_scales(int pairs) { return pairs * 16 + 4; }
 
-template <class T, int MR, bool VEC>
+template <class T, int CT, bool VEC>
 __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                            const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
                                                            const uint16_t* __restrict__ bias, int M, int N, int K,
                                                            int groups, uint16_t* __restrict__ Y) {
-  extern __shared__ __attribute__((aligned(16))) float shared[];   // sums [waves][16 tokens][16 columns], codes, scales
+  constexpr int kTokens = 8, kFlight = kBatch / CT;            // units of tokens and groups of weights in flight
+  extern __shared__ __attribute__((aligned(16))) uint8_t shared[];   // codes and scales; sums [waves][CT][16 tokens][16 columns]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * 16;
+  const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * (16 * CT);
   const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
-  const Operand w(Wq, sw, N, min(n0 + l16, N - 1), q, groups);
-  i32x4 b[kBatch][2];
-  int eb[kBatch];
+
+  // A unit is 512 elements of a token, two groups: a wave's load.
+  const int per = (groups + 1) / 2, units = M * per;
+  struct At {
+    int row, col;
+  };
+  const At step = {waves / per, waves % per};
+  auto next = [&](At& a) __attribute__((always_inline)) {
+    const int col = a.col + step.col, over = col >= per;
+    a = At{a.row + step.row + over, col - (over ? per : 0)};
+  };
+  u32x4 x[kTokens];
+  auto tokens = [&](At a) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k, next(a)) {
+      if (a.row >= M) continue;
+      if constexpr (VEC) {
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(X + a.row * ldx), (short)0, K * 2, 0x00020000);
+        x[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, a.col * 1024 + lane * 16, 0, 0));
+      } else {
+        x[k] = w8a8::load8<false>(X + a.row * ldx, a.col * 64 + lane, K);
+      }
+    }
+  };
+  At at = {wave / per, wave % per};
+  tokens(at);
+  __builtin_amdgcn_sched_barrier(0);
+
+  i32x4 b[kFlight][CT][2];
+  int eb[kFlight][CT];
+  const int columns = min(16 * CT, N - n0), bytes = groups * kStage;
+  const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(Wq + (size_t)n0 * bytes), (short)0, columns * bytes, 0x00020000);
+  int vw[CT], vs[CT];
+#pragma unroll
+  for (int j = 0; j < CT; ++j) {
+    const int r = min(16 * j + l16, columns - 1);
+    vw[j] = r * bytes + 32 * q;
+    vs[j] = r * 8 + 2 * q;
+  }
   auto load = [&](int u) __attribute__((always_inline)) {      // past the range's end: the last group again, not multiplied
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < kFlight; ++k) {
       const int g = min(u + k, max(ub, 1) - 1);
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc((void*)(sw + ((size_t)g * N + n0) * 8), (short)0, columns * 8, 0x00020000);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) b[k][t] = w.block(g, t);
-      eb[k] = w.scale(g);
+      for (int j = 0; j < CT; ++j) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) b[k][j][t] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, vw[j] + 16 * t, g * kStage, 0));
+        eb[k][j] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, vs[j], 0, 0);
+      }
     }
   };
   load(ua);
   __builtin_amdgcn_sched_barrier(0);
 
-  uint8_t* codes = reinterpret_cast<uint8_t*>(shared + waves * 256);
-  uint8_t* scales = codes + MR * lds_codes(groups);
-  const int chunks = groups * 32;                               // of eight elements: whole groups, so whole blocks a wave
-  for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
-    u32x4 x[MR];
+  uint8_t* codes = shared;
+  uint8_t* scales = codes + M * lds_codes(per);
+  auto quantize = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int m = 0; m < MR; ++m) x[m] = w8a8::load8<VEC>(X + (int64_t)min(m, M - 1) * ldx, c, K);
-#pragma unroll
-    for (int m = 0; m < MR; ++m) {
+    for (int k = 0; k < kTokens; ++k, next(at)) {
+      if (at.row >= M) continue;
       uint32_t byte;
-      const uint32_t code = mx::quantize8<T>(x[m], byte);
-      *reinterpret_cast<uint32_t*>(codes + m * lds_codes(groups) + 4 * c) = code;
-      if ((c & 3) == 0) scales[m * lds_scales(groups) + (c >> 2)] = (uint8_t)byte;
+      const uint32_t code = mx::quantize8<T>(x[k], byte);
+      const int c = at.col * 64 + lane;
+      *reinterpret_cast<uint32_t*>(codes + at.row * lds_codes(per) + 4 * c) = code;
+      scales[at.row * lds_scales(per) + (c >> 2)] = (uint8_t)byte;       // (the same from a block's four lanes)
     }
+  };
+  quantize();
+  while (at.row < M) {
+    tokens(at);
+    quantize();
   }
   __syncthreads();
 
-  const uint8_t* row = codes + min(l16, MR - 1) * lds_codes(groups) + 32 * q;
-  const uint8_t* row_scales = scales + min(l16, MR - 1) * lds_scales(groups) + 2 * q;
-  f32x4 acc = {};
-  for (int u = ua; u < ub; u += kBatch) {
+  const uint8_t* own = codes + min(l16, M - 1) * lds_codes(per) + 32 * q;
+  const uint8_t* own_scales = scales + min(l16, M - 1) * lds_scales(per) + 2 * q;
+  f32x4 acc[CT];
+#pragma unroll
+  for (int j = 0; j < CT; ++j) acc[j] = f32x4{};
+  for (int u = ua; u < ub; u += kFlight) {
     if (u > ua) load(u);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < kFlight; ++k) {
       if (u + k < ub) {
-        const i32x4 a0 = *reinterpret_cast<const i32x4*>(row + (u + k) * kStage);
-        const i32x4 a1 = *reinterpret_cast<const i32x4*>(row + (u + k) * kStage + 16);
-        const int ea = *reinterpret_cast<const uint16_t*>(row_scales + (u + k) * 8);
-        acc = mma16<0>(b[k][0], a0, acc, eb[k], ea);
-        acc = mma16<1>(b[k][1], a1, acc, eb[k], ea);
+        const i32x4 a0 = *reinterpret_cast<const i32x4*>(own + (u + k) * kStage);
+        const i32x4 a1 = *reinterpret_cast<const i32x4*>(own + (u + k) * kStage + 16);
+        const int ea = *reinterpret_cast<const uint16_t*>(own_scales + (u + k) * 8);
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+          acc[j] = mma16<0>(b[k][j][0], a0, acc[j], eb[k][j], ea);
+          acc[j] = mma16<1>(b[k][j][1], a1, acc[j], eb[k][j], ea);
+        }
       }
     }
   }
-  *reinterpret_cast<f32x4*>(shared + (wave * 16 + l16) * 16 + 4 * q) = acc;
+  __syncthreads();                                             // the sums take the codes' place
+  float* sums = reinterpret_cast<float*>(shared);
+#pragma unroll
+  for (int j = 0; j < CT; ++j) *reinterpret_cast<f32x4*>(sums + ((wave * CT + j) * 16 + l16) * 16 + 4 * q) = acc[j];
   __syncthreads();
-  for (int e = threadIdx.x; e < MR * 16; e += blockDim.x) {
-    const int m = e >> 4, n = n0 + (e & 15);
-    if (m < M && n < N) {
+  for (int e = threadIdx.x; e < M * 16 * CT; e += blockDim.x) {
+    const int m = e / (16 * CT), j = e / 16 % CT, n = n0 + e % (16 * CT);
+    if (n < N) {
       float sum = 0.0f;
-      for (int v = 0; v < waves; ++v) sum += shared[v * 256 + e];
+      for (int v = 0; v < waves; ++v) sum += sums[((v * CT + j) * 16 + m) * 16 + (e & 15)];
       Y[(size_t)m * N + n] = T::store(biased(sum, bias ? T::load(bias[n]) : 0.0f));
     }
   }
@@ -588,17 +642,25 @@ void launch(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8
 template <class T, bool VEC>
 void launch_rows(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias, int M,
                  int N, int K, uint16_t* Y, hipStream_t st) {
-  const int groups = mx::padded(K) / mx::kGroup, waves = rows_waves(groups), rows = M == 1 ? 1 : kOneLaunch;
+  const int groups = mx::padded(K) / mx::kGroup, pairs = (groups + 1) / 2;
+  const mx::RowsPlan p = mx::rows_plan(M, N, K, compute_units());
+  const int lds = max(p.waves * p.columns * 1024, M * (lds_codes(pairs) + lds_scales(pairs)));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((N + 15) / 16), dim3(64 * waves), waves * 1024 + rows * (lds_codes(groups) + lds_scales(groups)),
-                       st, X, ldx, Wq, sw, bias, M, N, K, groups, Y);
+    hipLaunchKernelGGL(kernel, dim3((N + 16 * p.columns - 1) / (16 * p.columns)), dim3(64 * p.waves), lds, st, X, ldx, Wq, sw, bias, M, N,
+                       K, groups, Y);
   };
-  rows == 1 ? go(linear_rows_kernel<T, 1, VEC>) : go(linear_rows_kernel<T, kOneLaunch, VEC>);
+  switch (p.columns) {
+    case 1: return go(linear_rows_kernel<T, 1, VEC>);
+    case 2: return go(linear_rows_kernel<T, 2, VEC>);
+    case 3: return go(linear_rows_kernel<T, 3, VEC>);
+    default: return go(linear_rows_kernel<T, 4, VEC>);
+  }
 }
 
 }  // namespace
 
 MxPlan mx_plan(int M, int N, int K) { return mx::plan(M, N, K, compute_units()); }
+bool mx_one_launch(int M, int N, int K) { return mx::rows_fit(M, N, K, compute_units()); }
 
 int64_t mx_workspace_bytes(const MxPlan& p) {
   return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0;

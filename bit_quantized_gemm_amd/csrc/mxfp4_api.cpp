@@ -21,8 +21,8 @@ bool plan_of(int32_t M, int32_t N, int32_t K, atom::MxPlan& plan) {
   plan = atom::mx_plan(M, N, K);
   return plan.tiles > 0;
 }
-int64_t linear_bytes(int32_t M, int32_t K, const atom::MxPlan& plan) {
-  if (atom::mx::rows_fit(M, K)) return 0;
+int64_t linear_bytes(int32_t M, int32_t N, int32_t K, const atom::MxPlan& plan) {
+  if (atom::mx_one_launch(M, N, K)) return 0;
   return (int64_t)(code_bytes(M, K) + up16(scale_bytes(M, K))) + atom::mx_workspace_bytes(plan);
 }
 
@@ -127,7 +127,7 @@ int atom_gemm_mxfp4(const void* Xq, const void* sx, const void* Wq, const void* 
 int64_t atom_linear_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K) {
   atom::MxPlan plan;
   if (!plan_of(M, N, K, plan)) return -(int64_t)ATOM_E_SHAPE;
-  return linear_bytes(M, K, plan);
+  return linear_bytes(M, N, K, plan);
 }
 
 int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq, const void* sw, const void* bias, int32_t M,
@@ -136,7 +136,7 @@ int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq,
   atom::MxPlan plan;
   if (!plan_of(M, N, K, plan) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
   if (!valid_x(X, ldx, M, K)) return aligned(X, 2) ? ATOM_E_SHAPE : ATOM_E_ALIGN;
-  const int64_t need = linear_bytes(M, K, plan);
+  const int64_t need = linear_bytes(M, N, K, plan);
   if (need > 0 && !workspace) return ATOM_E_NULL;
   if (workspace_bytes < need) return ATOM_E_SHAPE;
   if (!aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y) || (need > 0 && !aligned16(workspace)))

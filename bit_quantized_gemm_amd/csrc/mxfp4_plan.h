@@ -8,7 +8,7 @@ namespace atom {
 namespace mx {
 
 constexpr int kBatch = 4;        // groups of K whose loads a wave of the few-rows kernels has in flight
-constexpr int kOneLaunch = 4;    // most tokens that one launch quantizes and multiplies
+constexpr int kOneLaunch = 16;   // most tokens that one launch quantizes and multiplies
 
 // The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
 constexpr int kRowKinds = 2, kKinds = 7;
@@ -93,9 +93,41 @@ inline Plan plan(int M, int N, int K, int cus) {
   return best;
 }
 
-// One launch or two (us, M x N x K): 1 x 4096 x 4096 4.9 and 6.5, 1 x 28672 x 8192 25 and 33, 1 x 8192 x 28672 27 and 30; 4 x 11008 x 4096 9.5
-// and 10.5, 4 x 8192 x 8192 12.5 and 12.4, 2 x 8192 x 16384 21.6 and 20.4, 4 x 8192 x 16384 22.8 and 21.2.
-inline bool rows_fit(int M, int K) { return M == 1 || (M <= kOneLaunch && (int64_t)M * K <= 32768); }
+// Whether one launch quantizes the tokens, in every workgroup, and multiplies.  One launch and two (us, M x N x K): 1 x 4096 x 4096 4.5
+// and 6.3, 1 x 28672 x 8192 23.9 and 31.8, 4 x 11008 x 1155 5.2 and 8.4, 8 x 4096 x 4096 5.8 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192
+// 12.4 and 12.4.  Against two where many tokens or long ones meet few columns: 16 x 4096 x 4096 7.8 and 7.0, 8 x 4096 x 8192 9.1 and 8.8;
+// called one by one from Python these are 7.8 and 8.9, 9.1 and 9.1, since the second launch is 4 us of the host's time.  More tokens
+// than eight against more columns than the units hold at a time: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5.
+inline bool rows_fit(int M, int N, int K, int cus) {
+  return M == 1 || (M <= kOneLaunch && (int64_t)M * K <= 65536 && (M <= 8 || N <= 64 * cus));
+}
+
+// Its workgroups: `columns` times 16 columns each, K's groups divided among `waves`.
+//   Columns: as few as give each unit one workgroup (the tokens are quantized once for all of them); one for long rows of few
+//     tokens, whose weights take longer than the quantizing (us, one and three: 1 x 11008 x 4096 7.3 and 7.9, 16 x 11008 x 2048 10 and 6.1).
+//   Waves: what each costs its unit, how often each waits for weights and how many units of 512 elements it quantizes.
+// Fitted on 256 units to 190 shapes (1 to 16 tokens, 1024 to 28672 columns, K 512 to 11008): the choice is 1.3% slower than the best of
+// one to four columns and 4 to 16 waves on average.
+struct RowsPlan {
+  int columns, waves;
+};
+inline RowsPlan rows_plan(int M, int N, int K, int cus) {
+  const int groups = (K + 255) / 256, tiles = (N + 15) / 16, units = M * ((groups + 1) / 2);
+  const int fit = (tiles + cus - 1) / cus;
+  const int columns = (K >= 4096 && (int64_t)M * K <= 24576) ? 1 : fit < 4 ? fit : 4;
+  const double full = (double)((tiles + columns - 1) / columns) / cus, each = full > 1.0 ? full : 1.0;
+  RowsPlan best = {columns, 4};
+  double least = -1.0;
+  for (int w = 4; w <= 16; w += 4) {
+    const int flight = kBatch / columns, turns = ((groups + w - 1) / w + flight - 1) / flight;
+    const double time = 4.0 * w * each + 16.0 * turns + 3.0 * ((units + w - 1) / w);
+    if (least < 0.0 || time < least) {
+      least = time;
+      best.waves = w;
+    }
+  }
+  return best;
+}
 
 }  // namespace mx
 }  // namespace atom

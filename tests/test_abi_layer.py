@@ -92,9 +92,10 @@ def test_gemm_and_linear_validation(lib):
     assert g(m=64, n=4096, k=11008, ws=E, nws=need) == E_OVERLAP
     assert lib.atom_gemm_mxfp4_workspace_bytes(0, 4, 4) == lib.atom_linear_mxfp4_workspace_bytes(4, 0, 4) == -E_SHAPE
     assert bq.atom_linear_mxfp4_workspace_bytes(4, 4, 256) == 0          # one launch: nothing to keep
-    need = bq.atom_linear_mxfp4_workspace_bytes(8, 4, 256)
-    assert need >= 8 * 128 + 64
-    f = caller(lib.atom_linear_mxfp4, dict(x=A, ldx=256, t=0, wq=C, sw=D, bias=None, m=8, n=4, k=256, y=E, ws=F, nws=need, s=S))
+    assert bq.atom_linear_mxfp4_workspace_bytes(16, 4, 4096) == 0 < bq.atom_linear_mxfp4_workspace_bytes(16, 4, 4097)
+    need = bq.atom_linear_mxfp4_workspace_bytes(17, 4, 256)
+    assert need >= 17 * 128 + 136
+    f = caller(lib.atom_linear_mxfp4, dict(x=A, ldx=256, t=0, wq=C, sw=D, bias=None, m=17, n=4, k=256, y=E, ws=F, nws=need, s=S))
     for n in ("x", "wq", "sw", "y", "ws"):
         assert f(**{n: None}) == E_NULL
     assert f(nws=need - 1) == f(ldx=255) == f(t=-1) == f(k=0) == E_SHAPE
@@ -185,7 +186,7 @@ def test_binding_refusals(lib, monkeypatch):
         lambda: bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, 300, workspace=z((8, 8), dtype=u8)),
         lambda: bq.linear_mxfp4(X, z((6, 150), dtype=u8), sw),
         lambda: bq.linear_mxfp4(X, Wq, sw[:, :5]),
-        lambda: bq.linear_mxfp4(z((8, 300), dtype=f16), Wq, sw, workspace=z((16,), dtype=u8)),
+        lambda: bq.linear_mxfp4(z((17, 300), dtype=f16), Wq, sw, workspace=z((16,), dtype=u8)),
         lambda: bq.atom_rmsnorm_w8a8(X, W[:299]),
         lambda: bq.atom_rmsnorm_w8a8(X, W, residual=X[:3]),
         lambda: bq.atom_rmsnorm_w8a8(X, W, residual=X, H=X[:, :200]),

@@ -222,29 +222,93 @@ def test_scales_of_the_whole_range():
         torch.testing.assert_close(Y, y.float().bfloat16(), rtol=0, atol=0)
 
 
+# Layers of one launch: every number of columns and of waves, batches of tokens that end everywhere, rows of one group and of odd numbers.
+ONE = [(1, 33, 16384), (2, 20, 8192), (3, 48, 5461), (4, 65, 4096), (4, 16, 4097), (1, 70, 16385), (2, 5, 1), (4, 1, 129), (3, 4096, 513),
+       (1, 300, 255), (1, 33, 65536), (4, 20, 8192), (2, 20, 16384), (1, 5000, 300), (2, 8200, 1030), (7, 6001, 777), (16, 6000, 4096),
+       (16, 4100, 2048), (16, 9000, 256), (9, 12300, 1200), (16, 12400, 300), (5, 16390, 2000), (8, 16400, 1500), (8, 20001, 8192), (13, 47, 5000),
+       (16, 16384, 4096), (6, 11000, 10000), (15, 1, 4369), (8, 100, 31), (2, 4100, 32768), (1, 5000, 4097), (1, 12400, 3000), (1, 30000, 520)]
+
+
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("M,N,K", [(1, 33, 16384), (2, 20, 8192), (3, 48, 5461), (4, 65, 4096), (4, 16, 4097), (1, 70, 16385), (2, 5, 1),
-                                   (4, 1, 129), (3, 4096, 513), (1, 300, 255), (1, 33, 65536), (4, 20, 8192), (2, 20, 16384)])
-def test_up_to_four_tokens_equal_two_steps(M, N, K, dtype):
-    """Quantized and multiplied in one launch, at the ends of what that takes: the bits of the two steps, also from rows
-    that lie apart and start at odd elements."""
+@pytest.mark.parametrize("M,N,K", ONE)
+def test_one_launch_equals_two_steps(M, N, K, dtype):
+    """Quantized and multiplied in one launch: the bits of the two steps where every sum is exact, also from rows that lie apart
+    and start at odd elements.  Blocks' largest elements are in [4, 8) units, so that codes are halves up to 6 of one unit, and a
+    sum's terms multiples of its quarter up to 36: of 2^16 terms every partial sum has 24 bits, in any order."""
     say(f"[mxfp4 one launch] {M}x{N}x{K} {dtype}")
     t = TYPES[dtype]
-    Wq, sw = bq.atom_quantize_mxfp4(make(N, K, t, 1, 0.02))
-    wide = make(M, K + 9, t, 2)
-    wide[M - 1, 3:] = 0                              # a row of zeros
-    wide[0, K // 2] = 1000                           # and one with an outlier
+    K_all = K + 9
+
+    def blocks(rows, n, seed, unit, lead):
+        g = torch.Generator().manual_seed(seed)
+        v = make(rows, n, t, seed).clamp(-3, 3)
+        for first in lead:                           # of every block, wherever the rows begin
+            at = v[:, first::32]
+            v[:, first::32] = (4 + 3.9 * torch.rand(at.shape, generator=g)).to(t).cuda()
+        return v * unit
+
+    Wq, sw = bq.atom_quantize_mxfp4(blocks(N, K, 1, 2.0**-6, (0,)))
+    wide = blocks(M, K_all, 2, 1, (0, 1, 3, 5, 8))
+    if M > 1:
+        wide[M - 1, 3:] = 0                          # a row of zeros
+    wide[0, K // 2] = 7.75
     for first in (0, 1, 3, 8):
         x = wide[:, first:first + K]
         Y = bq.linear_mxfp4(x, Wq, sw)
         torch.testing.assert_close(Y, bq.atom_gemm_mxfp4(*bq.atom_quantize_mxfp4(x), Wq, sw, K, dtype=t), rtol=0, atol=0)
         torch.testing.assert_close(Y, bq.linear_mxfp4(x.contiguous(), Wq, sw), rtol=0, atol=0)
         ws = torch.empty(bq.atom_linear_mxfp4_workspace_bytes(M, N, K), dtype=torch.uint8, device="cuda")
+        assert ws.numel() == 0
         torch.testing.assert_close(Y, bq.linear_mxfp4(x, Wq, sw, Y=torch.empty_like(Y), workspace=ws), rtol=0, atol=0)
-    odd = torch.full((M, K + 9), float("nan"), dtype=t, device="cuda")       # what lies around the rows is not read into them
+    odd = torch.full((M, K_all), float("nan"), dtype=t, device="cuda")       # what lies around the rows is not read into them
     odd[:, 5:5 + K] = wide[:, 5:5 + K]
     torch.testing.assert_close(bq.linear_mxfp4(odd[:, 5:5 + K], Wq, sw), bq.linear_mxfp4(wide[:, 5:5 + K].contiguous(), Wq, sw),
                                rtol=0, atol=0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", [s for s in ONE if s[1] < 10000])
+def test_one_launch_of_any_values(M, N, K, dtype):
+    """Values of any size, an outlier and a row of zeros, with a bias: within the bound of the steps."""
+    t = TYPES[dtype]
+    Wq, sw = bq.atom_quantize_mxfp4(make(N, K, t, 1, 0.02))
+    x = make(M, K, t, 2)
+    if M > 1:
+        x[M - 1, 3:] = 0
+    x[0, K // 2] = 1000
+    b = make(1, N, t, 3)[0]
+    xd, wd = (values(*q)[:, :K] for q in (bq.atom_quantize_mxfp4(x), (Wq, sw)))
+    check_y(bq.linear_mxfp4(x, Wq, sw, bias=b), xd, wd, b, K, f"{M}x{N}x{K}")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_every_value_against_every_scale(dtype):
+    """Every finite value of the type in a block whose largest has each exponent from its own up: the code that the formula gives."""
+    t = TYPES[dtype]
+    v = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(t).cuda()
+    v = torch.where(v.isfinite(), v, 0.0)
+    v = torch.cat([v, torch.zeros(-v.numel() % 31, dtype=t, device="cuda")]).view(-1, 31)
+    low, high = (-24, 15) if dtype == "fp16" else (-133, 127)
+    border = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64, device="cuda")
+    for first in range(low, high + 1, 40):
+        tops = torch.tensor([2.0**e for e in range(first, min(first + 40, high + 1))], dtype=torch.float64, device="cuda")
+        x = torch.where(v.double().abs()[None] < 2 * tops[:, None, None], v[None], 0.0)          # the exponent of the top, or less
+        x = torch.cat([x, tops.to(t)[:, None, None].expand(-1, v.shape[0], 1)], 2).reshape(-1, 32)
+        x = torch.cat([x, torch.zeros(-x.shape[0] % 64, 32, dtype=t, device="cuda")])
+        Xq, sx = bq.atom_quantize_mxfp4(x.view(-1, 2048))
+        scale = sx.permute(1, 0, 2).reshape(-1)
+        e = torch.clamp(torch.frexp(x.abs().amax(1).double())[1] - 1 - 2, -127, 125)
+        e = torch.where((x != 0).any(1), e, -127)
+        assert torch.equal(scale.int(), (e + 127).int())
+        u = x.double().abs() * torch.exp2(-e.double())[:, None]
+        code = torch.bucketize(u, border)                                   # borders below u: ties to the even code
+        tie = (code < 7) & (u == border[code.clamp(max=6)]) & (code % 2 == 1)
+        code = code + tie.long()
+        sign = torch.signbit(x)
+        got = Xq.view(-1, 16)
+        got = torch.stack([got & 15, got >> 4], 2).view(-1, 32).long()
+        assert torch.equal(got & 7, code)
+        assert torch.equal((got >> 3)[code > 0].bool(), sign[code > 0])
 
 
 def test_two_graphs_and_eager_calls_between():

@@ -16,7 +16,9 @@ int main() {
   int a[3];                                    // M N K
   while (scanf("%d %d %d", a, a + 1, a + 2) == 3) {
     const atom::mx::Plan p = atom::mx::plan(a[0], a[1], a[2], 256);
-    printf("%d %d %d %d %d\n", p.kind, p.tiles, p.splits, atom::mx::rows_waves((a[2] + 255) / 256), (int)atom::mx::rows_fit(a[0], a[2]));
+    const bool one = atom::mx::rows_fit(a[0], a[1], a[2], 256);
+    const atom::mx::RowsPlan r = one ? atom::mx::rows_plan(a[0], a[1], a[2], 256) : atom::mx::RowsPlan{0, 0};
+    printf("%d %d %d %d %d %d\n", p.kind, p.tiles, p.splits, atom::mx::rows_waves((a[2] + 255) / 256), r.columns, r.waves);
   }
   return 0;
 }
@@ -25,7 +27,8 @@ int main() {
 
 @pytest.fixture(scope="module")
 def plans(tmp_path_factory):
-    """A function from shapes (M, N, K) to their (kind, tiles, splits, waves of a few-rows workgroup, one launch)."""
+    """A function from shapes (M, N, K) to their (kind, tiles, splits, waves of a few-rows workgroup, and of one launch: times
+    16 columns, or 0 where it takes two, and waves)."""
     cxx = shutil.which("g++")
     if not cxx:
         pytest.skip("no g++")
@@ -48,7 +51,7 @@ def test_plans_fit_a_launch(plans):
              1 << 22, (1 << 24) - 1, 1 << 24]
     shapes = [(m, n, k) for m in sizes for n in sizes for k in (1, 256, 257, 1024, 4096, 11008, 65536)
               if m * n <= 1 << 39 and -(-m // 128) * -(-n // 128) <= 1 << 26]
-    for (M, N, K), (kind, tiles, splits, waves, _) in zip(shapes, plans(shapes)):
+    for (M, N, K), (kind, tiles, splits, waves, _, _) in zip(shapes, plans(shapes)):
         bm, bn = TILES.get(kind, (16 * (kind + 1), 16))
         assert tiles == -(-M // bm) * -(-N // bn) > 0, (M, N, K)
         assert tiles * splits * (64 * waves if kind < 2 else 256) < 1 << 32
@@ -58,18 +61,21 @@ def test_plans_fit_a_launch(plans):
 
 
 def test_one_launch_fits_lds(plans):
-    """Sums, codes and scales of the tokens that one launch takes stay below 64 KB for every K."""
-    shapes = [(m, 64, k) for m in (1, 2, 3, 4, 5) for k in (1, 256, 4096, 8192, 10922, 10923, 16384, 16385, 32768, 65536)]
-    for (M, _, K), (_, _, _, waves, one) in zip(shapes, plans(shapes)):
-        groups = -(-K // 256)
-        if one:
-            assert M <= 4 and waves * 1024 + (1 if M == 1 else 4) * (groups * 136 + 20) <= 65536, (M, K)
-        assert one == (M == 1 or (M <= 4 and M * K <= 32768))
+    """Sums, codes and scales of the tokens that one launch takes stay within 64 KB for every K, and its tiles in a grid."""
+    shapes = [(m, n, k) for m in range(1, 18) for n in (1, 64, 4096, 8192, 11008, 16384, 16385, 1 << 20, 1 << 24)
+              for k in (1, 256, 257, 4095, 4096, 4097, 8192, 10922, 10923, 16384, 16385, 32768, 65536)]
+    for (M, N, K), (_, _, _, _, columns, waves) in zip(shapes, plans(shapes)):
+        pairs = (-(-K // 256) + 1) // 2
+        assert (columns > 0) == (M == 1 or (M <= 16 and M * K <= 65536 and (M <= 8 or N <= 16384))), (M, N, K)
+        if columns:
+            assert columns <= 4 and waves in (4, 8, 12, 16)
+            assert max(waves * columns * 1024, M * (pairs * 272 + 20)) <= 65536, (M, N, K)
+            assert -(-N // (16 * columns)) * 64 * waves < 1 << 32
 
 
 def test_the_kernel_of_each_tested_shape(plans):
     """The GPU tests' shapes reach every kernel, every division of K, and every ending of each ring of stage buffers."""
-    from test_gpu_mxfp4 import RINGS, SHAPES
+    from test_gpu_mxfp4 import ONE, RINGS, SHAPES
     got = plans(SHAPES)
     assert {p[0] for p in got} == set(range(7))
     assert {p[2] for p in got if p[0] == 2} == {1, 2, 3, 4}
@@ -80,12 +86,14 @@ def test_the_kernel_of_each_tested_shape(plans):
     assert {g % 6 for g in ends[2]} == {g % 6 for g in ends[3]} == {g % 6 for g in ends[5]} == set(range(6))
     assert {g % 2 for g in ends[4]} == {g % 2 for g in ends[6]} == {0, 1}
     assert min(ends[2]) == min(ends[3]) == min(ends[4]) == 1
+    one = plans(ONE)
+    assert {(p[4], p[5]) for p in one} >= {(c, w) for c in (1, 2, 3, 4) for w in (4, 8)} and {p[5] for p in one} == {4, 8, 12, 16}
 
 
 def test_workspace_follows_the_plan(plans):
     if not os.path.exists(bq.lib_path()):
         pytest.skip("libatom.so not built (python -m bit_quantized_gemm_amd.build)")
     shapes = [(64, 4096, 8192), (777, 777, 7000), (16, 4096, 4096), (1024, 11008, 4096), (100, 260, 65536)]
-    for (M, N, K), (_, tiles, splits, _, one) in zip(shapes, plans(shapes)):
+    for (M, N, K), (_, tiles, splits, _, one, _) in zip(shapes, plans(shapes)):
         assert bq.atom_gemm_mxfp4_workspace_bytes(M, N, K) == (splits * tiles * 64 * 64 * 4 if splits > 1 else 0)
         assert bq.atom_linear_mxfp4_workspace_bytes(M, N, K) > bq.atom_gemm_mxfp4_workspace_bytes(M, N, K) or one
