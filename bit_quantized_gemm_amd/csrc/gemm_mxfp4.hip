@@ -26,8 +26,9 @@
 //     waves divide K, each loads its operands straight into registers, all of them at once where K is short; the waves' sums
 //     meet in LDS.  Weights from HBM: 16 x 4096 x 4096 5.0 us, 16 x 11008 x 4096 9.6 us (2.5 TB/s; as many bytes of codes from
 //     the L2), 1 x 11008 x 4096 7.7 us.
-//   linear_rows_kernel: the same for at most 16 tokens with the quantizer in front, one launch for two (us): 1 x 4096 x 4096 4.5 and
-//     6.3, 4 x 11008 x 4096 8.2 and 10.1, 16 x 11008 x 4096 10.1 and 11.3, 16 x 4096 x 4096 7.8 and 7.0.
+//   linear_rows_kernel: the same with the quantizer in front, where one round of workgroups holds all outputs: one launch for two (us),
+//     1 x 4096 x 4096 4.5 and 6.3, 4 x 11008 x 4096 8.2 and 10.1, 16 x 11008 x 4096 10.1 and 11.3, 16 x 4096 x 4096 7.8 and 7.0,
+//     256 x 1024 x 2048 6.1 and 8.0.
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "gemm_tile.h"
@@ -468,8 +469,8 @@ __global__ __launch_bounds__(1024) void gemm_rows_kernel(const uint8_t* __restri
   }
 }
 
-// The layer for at most 16 tokens in one launch: every workgroup quantizes them for itself, into LDS, then as above, against 16 CT
-// columns.  Its first loads of tokens are under way before those of its weights, since loads arrive in order, and its weights
+// The layer of few outputs in one launch: every workgroup quantizes its 16 tokens (blockIdx.y) for itself, into LDS, then as above,
+// against 16 CT columns.  Its first loads of tokens are under way before those of its weights, since loads arrive in order, and its weights
 // while it quantizes.  Addresses are a wave's, in scalar registers, and rows of LDS whole units, so that a unit takes few
 // instructions besides the quantizer's own: 16 x 4096 x 4096 (M x N x K) 9.2 us with an index a lane, 8.2 so, 7.7 without
 // conditions on the stores.  Rows in LDS lie 16 bytes (their scales 4) apart beyond their units, so that their reads do not meet in one bank.
@@ -479,16 +480,19 @@ __host__ __device__ constexpr int lds_scales(int pairs) { return pairs * 16 + 4;
 template <class T, int CT, bool VEC>
 __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __restrict__ X, int64_t ldx,
                                                            const uint8_t* __restrict__ Wq, const uint8_t* __restrict__ sw,
-                                                           const uint16_t* __restrict__ bias, int M, int N, int K,
+                                                           const uint16_t* __restrict__ bias, int rows, int N, int K,
                                                            int groups, uint16_t* __restrict__ Y) {
-  constexpr int kTokens = 8, kFlight = kBatch / CT;            // units of tokens and groups of weights in flight
+  const int m0 = blockIdx.y * mx::kTokens, M = min(rows - m0, mx::kTokens);   // this workgroup's tokens
+  X += m0 * ldx;
+  Y += (size_t)m0 * N;
+  constexpr int kUnits = 8, kFlight = kBatch / CT;             // units of tokens and groups of weights in flight
   extern __shared__ __attribute__((aligned(16))) uint8_t shared[];   // codes and scales; sums [waves][CT][16 tokens][16 columns]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
   const int l16 = lane & 15, q = lane >> 4, n0 = blockIdx.x * (16 * CT);
   const int ua = groups * wave / waves, ub = groups * (wave + 1) / waves;
 
   // A unit is 512 elements of a token, two groups: a wave's load.
-  const int per = (groups + 1) / 2, units = M * per;
+  const int per = (groups + 1) / 2;
   struct At {
     int row, col;
   };
@@ -497,10 +501,10 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
     const int col = a.col + step.col, over = col >= per;
     a = At{a.row + step.row + over, col - (over ? per : 0)};
   };
-  u32x4 x[kTokens];
+  u32x4 x[kUnits];
   auto tokens = [&](At a) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k, next(a)) {
+    for (int k = 0; k < kUnits; ++k, next(a)) {
       if (a.row >= M) continue;
       if constexpr (VEC) {
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(X + a.row * ldx), (short)0, K * 2, 0x00020000);
@@ -546,7 +550,7 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
   uint8_t* scales = codes + M * lds_codes(per);
   auto quantize = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < kTokens; ++k, next(at)) {
+    for (int k = 0; k < kUnits; ++k, next(at)) {
       if (at.row >= M) continue;
       uint32_t byte;
       const uint32_t code = mx::quantize8<T>(x[k], byte);
@@ -644,10 +648,10 @@ void launch_rows(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_
                  int N, int K, uint16_t* Y, hipStream_t st) {
   const int groups = mx::padded(K) / mx::kGroup, pairs = (groups + 1) / 2;
   const mx::RowsPlan p = mx::rows_plan(M, N, K, compute_units());
-  const int lds = max(p.waves * p.columns * 1024, M * (lds_codes(pairs) + lds_scales(pairs)));
+  const int lds = max(p.waves * p.columns * 1024, min(M, mx::kTokens) * (lds_codes(pairs) + lds_scales(pairs)));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((N + 16 * p.columns - 1) / (16 * p.columns)), dim3(64 * p.waves), lds, st, X, ldx, Wq, sw, bias, M, N,
-                       K, groups, Y);
+    hipLaunchKernelGGL(kernel, dim3((N + 16 * p.columns - 1) / (16 * p.columns), (M + mx::kTokens - 1) / mx::kTokens), dim3(64 * p.waves),
+                       lds, st, X, ldx, Wq, sw, bias, M, N, K, groups, Y);
   };
   switch (p.columns) {
     case 1: return go(linear_rows_kernel<T, 1, VEC>);

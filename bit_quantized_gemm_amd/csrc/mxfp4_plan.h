@@ -8,7 +8,7 @@ namespace atom {
 namespace mx {
 
 constexpr int kBatch = 4;        // groups of K whose loads a wave of the few-rows kernels has in flight
-constexpr int kOneLaunch = 16;   // most tokens that one launch quantizes and multiplies
+constexpr int kTokens = 16;      // tokens of a workgroup that quantizes them itself
 
 // The kinds of kernel: few rows, then the tiled kernel's tile sizes, smallest first.
 constexpr int kRowKinds = 2, kKinds = 7;
@@ -93,13 +93,15 @@ inline Plan plan(int M, int N, int K, int cus) {
   return best;
 }
 
-// Whether one launch quantizes the tokens, in every workgroup, and multiplies.  One launch and two (us, M x N x K): 1 x 4096 x 4096 4.5
-// and 6.3, 1 x 28672 x 8192 23.9 and 31.8, 4 x 11008 x 1155 5.2 and 8.4, 8 x 4096 x 4096 5.8 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192
-// 12.4 and 12.4.  Against two where many tokens or long ones meet few columns: 16 x 4096 x 4096 7.8 and 7.0, 8 x 4096 x 8192 9.1 and 8.8;
-// called one by one from Python these are 7.8 and 8.9, 9.1 and 9.1, since the second launch is 4 us of the host's time.  More tokens
-// than eight against more columns than the units hold at a time: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5.
+// Whether one launch quantizes the tokens, 16 in every workgroup, and multiplies: where their codes leave room in LDS and one round of
+// workgroups holds all outputs (or there are few tokens).  One launch and two (us, M x N x K): 1 x 4096 x 4096 4.5 and 6.3, 1 x 28672 x 8192
+// 23.9 and 31.8, 4 x 11008 x 1155 5.2 and 8.4, 8 x 4096 x 4096 5.8 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192 12.4 and 12.4, 64 x 4096 x 2048
+// 6.3 and 8.4, 256 x 1024 x 2048 6.1 and 8.0, 1024 x 256 x 256 4.8 and 5.7.  Against two where 16 long tokens meet few columns: 16 x 4096 x 4096 7.8
+// and 7.0, 17 x 256 x 4096 6.6 and 6.4; called one by one from Python these are 7.8 and 8.9, 6.6 and 8.9, since the second launch is
+// 4 us of the host's time.  Past a round: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5, 128 x 4096 x 2048 9.1 and 8.5.
 inline bool rows_fit(int M, int N, int K, int cus) {
-  return M == 1 || (M <= kOneLaunch && (int64_t)M * K <= 65536 && (M <= 8 || N <= 64 * cus));
+  const int64_t tokens = M < kTokens ? M : kTokens;
+  return M == 1 || (tokens * K <= 65536 && (M <= 8 || ((int64_t)N + 63) / 64 * ((M + kTokens - 1) / kTokens) <= cus));
 }
 
 // Its workgroups: `columns` times 16 columns each, K's groups divided among `waves`.
@@ -112,10 +114,12 @@ struct RowsPlan {
   int columns, waves;
 };
 inline RowsPlan rows_plan(int M, int N, int K, int cus) {
-  const int groups = (K + 255) / 256, tiles = (N + 15) / 16, units = M * ((groups + 1) / 2);
-  const int fit = (tiles + cus - 1) / cus;
-  const int columns = (K >= 4096 && (int64_t)M * K <= 24576) ? 1 : fit < 4 ? fit : 4;
-  const double full = (double)((tiles + columns - 1) / columns) / cus, each = full > 1.0 ? full : 1.0;
+  const int tokens = M < kTokens ? M : kTokens, groups = (K + 255) / 256, units = tokens * ((groups + 1) / 2);
+  const int64_t tiles = (N + 15) / 16, blocks = (M + kTokens - 1) / kTokens;
+  int columns = 1;
+  if (K < 4096 || (int64_t)M * K > 24576)
+    while (columns < 4 && (tiles + columns - 1) / columns * blocks > cus) ++columns;
+  const double full = (double)((tiles + columns - 1) / columns * blocks) / cus, each = full > 1.0 ? full : 1.0;
   RowsPlan best = {columns, 4};
   double least = -1.0;
   for (int w = 4; w <= 16; w += 4) {

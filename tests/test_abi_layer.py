@@ -93,12 +93,12 @@ def test_gemm_and_linear_validation(lib):
     assert lib.atom_gemm_mxfp4_workspace_bytes(0, 4, 4) == lib.atom_linear_mxfp4_workspace_bytes(4, 0, 4) == -E_SHAPE
     assert bq.atom_linear_mxfp4_workspace_bytes(4, 4, 256) == 0          # one launch: nothing to keep
     assert bq.atom_linear_mxfp4_workspace_bytes(16, 4, 4096) == 0 < bq.atom_linear_mxfp4_workspace_bytes(16, 4, 4097)
-    need = bq.atom_linear_mxfp4_workspace_bytes(17, 4, 256)
-    assert need >= 17 * 128 + 136
-    f = caller(lib.atom_linear_mxfp4, dict(x=A, ldx=256, t=0, wq=C, sw=D, bias=None, m=17, n=4, k=256, y=E, ws=F, nws=need, s=S))
+    need = bq.atom_linear_mxfp4_workspace_bytes(17, 4, 4352)
+    assert need >= 17 * (2176 + 136)
+    f = caller(lib.atom_linear_mxfp4, dict(x=A, ldx=4352, t=0, wq=C, sw=D, bias=None, m=17, n=4, k=4352, y=E, ws=F, nws=need, s=S))
     for n in ("x", "wq", "sw", "y", "ws"):
         assert f(**{n: None}) == E_NULL
-    assert f(nws=need - 1) == f(ldx=255) == f(t=-1) == f(k=0) == E_SHAPE
+    assert f(nws=need - 1) == f(ldx=4351) == f(t=-1) == f(k=0) == E_SHAPE
     assert f(x=A + 1) == f(ws=F + 8) == f(y=E + 2) == f(sw=D + 8) == E_ALIGN
     assert f(y=F) == f(ws=A) == f(y=C) == f(y=D) == E_OVERLAP
 
@@ -186,7 +186,7 @@ def test_binding_refusals(lib, monkeypatch):
         lambda: bq.atom_gemm_mxfp4(Xq, sx, Wq, sw, 300, workspace=z((8, 8), dtype=u8)),
         lambda: bq.linear_mxfp4(X, z((6, 150), dtype=u8), sw),
         lambda: bq.linear_mxfp4(X, Wq, sw[:, :5]),
-        lambda: bq.linear_mxfp4(z((17, 300), dtype=f16), Wq, sw, workspace=z((16,), dtype=u8)),
+        lambda: bq.linear_mxfp4(z((9, 8000), dtype=f16), z((6, 4096), dtype=u8), z((32, 6, 8), dtype=u8), workspace=z((16,), dtype=u8)),
         lambda: bq.atom_rmsnorm_w8a8(X, W[:299]),
         lambda: bq.atom_rmsnorm_w8a8(X, W, residual=X[:3]),
         lambda: bq.atom_rmsnorm_w8a8(X, W, residual=X, H=X[:, :200]),

@@ -181,7 +181,7 @@ def test_refusals_on_the_device():
             (z(), Wq, sw), (X[0], Wq, sw), (z(0, 300), Wq, sw), (z(4, 0), Wq, sw), (X, Wq[:, :150], sw), (X, Wq[0], sw), (X, Wq, sw[:1]),
             (X, Wq, sw[:, :5]), (X, Wq, z()), (X, Wq, sw, z()), (X, Wq, sw, z(6).bfloat16()), (X.float(), Wq, sw), (X, Wq.cpu(), sw),
             (X, Wq, sw.cpu()), (X[:1].expand(4, 300), Wq, sw), (z(300, 4).t(), Wq, sw), (X, Wq.view(i8), sw), (X, Wq, sw, None, z(4, 5)),
-            (X, Wq, sw, None, None, z()), (z(17, 300), Wq, sw, None, None, z(8, dtype=u8)))),
+            (X, Wq, sw, None, None, z()), (z(9, 8000), z(6, 4096, dtype=u8), z(32, 6, 8, dtype=u8), None, None, z(8, dtype=u8)))),
         *(lambda a=a: bq.atom_quantize_mxfp4(*a) for a in ((z(),), (X[0],), (z(0, 300),), (X.float(),), (z(300, 4).t(),), (X, z(4, 150, dtype=u8)),
                                                            (X, None, z(2, 3, 8, dtype=u8)), (X[:, ::2],), (X[:1].expand(4, 300),))),
         *(lambda a=a: bq.atom_dequantize_mxfp4(*a) for a in ((Xq, sx, 0), (Xq, sx, 600), (Xq, sx, 200), (Xq, sx[:1], 300), (Xq.view(i8), sx, 300),
