@@ -105,10 +105,10 @@ inline bool rows_fit(int M, int N, int K, int cus) {
 }
 
 // Its workgroups: `columns` times 16 columns each, K's groups divided among `waves`.
-//   Columns: as few as give each unit one workgroup (the tokens are quantized once for all of them); one for long rows of few
-//     tokens, whose weights take longer than the quantizing (us, one and three: 1 x 11008 x 4096 7.3 and 7.9, 16 x 11008 x 2048 10 and 6.1).
+//   Columns: as few as give each unit one workgroup (the tokens are quantized once for all of them); one for long rows of one or two
+//     tokens, whose weights take longer than the quantizing (us, one and three: 1 x 11008 x 4096 7.3 and 7.9, 4 x 11008 x 4096 8.5 and 8.2).
 //   Waves: what each costs its unit, how often each waits for weights and how many units of 512 elements it quantizes.
-// Fitted on 256 units to 190 shapes (1 to 16 tokens, 1024 to 28672 columns, K 512 to 11008): the choice is 1.3% slower than the best of
+// Fitted on 256 units to 190 shapes (1 to 16 tokens, 1024 to 28672 columns, K 512 to 11008): the choice is 1.2% slower than the best of
 // one to four columns and 4 to 16 waves on average.
 struct RowsPlan {
   int columns, waves;
@@ -117,7 +117,7 @@ inline RowsPlan rows_plan(int M, int N, int K, int cus) {
   const int tokens = M < kTokens ? M : kTokens, groups = (K + 255) / 256, units = tokens * ((groups + 1) / 2);
   const int64_t tiles = (N + 15) / 16, blocks = (M + kTokens - 1) / kTokens;
   int columns = 1;
-  if (K < 4096 || (int64_t)M * K > 24576)
+  if (K < 4096 || M > 2)
     while (columns < 4 && (tiles + columns - 1) / columns * blocks > cus) ++columns;
   const double full = (double)((tiles + columns - 1) / columns * blocks) / cus, each = full > 1.0 ? full : 1.0;
   RowsPlan best = {columns, 4};
