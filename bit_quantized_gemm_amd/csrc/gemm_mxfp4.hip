@@ -510,7 +510,7 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)(X + a.row * ldx), (short)0, K * 2, 0x00020000);
         x[k] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, a.col * 1024 + lane * 16, 0, 0));
       } else {
-        x[k] = w8a8::load8<false>(X + a.row * ldx, a.col * 64 + lane, K);
+        x[k] = K < 8 ? w8a8::load8<false>(X + a.row * ldx, a.col * 64 + lane, K) : mx::load8_any(X + a.row * ldx, a.col * 64 + lane, K);
       }
     }
   };
@@ -553,8 +553,9 @@ __global__ __launch_bounds__(1024) void linear_rows_kernel(const uint16_t* __res
     for (int k = 0; k < kUnits; ++k, next(at)) {
       if (at.row >= M) continue;
       uint32_t byte;
-      const uint32_t code = mx::quantize8<T>(x[k], byte);
       const int c = at.col * 64 + lane;
+      if (!VEC && K >= 8 && at.col == per - 1) x[k] = mx::behind(x[k], c, K);
+      const uint32_t code = mx::quantize8<T>(x[k], byte);
       *reinterpret_cast<uint32_t*>(codes + at.row * lds_codes(per) + 4 * c) = code;
       scales[at.row * lds_scales(per) + (c >> 2)] = (uint8_t)byte;       // (the same from a block's four lanes)
     }

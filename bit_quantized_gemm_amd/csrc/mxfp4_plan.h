@@ -94,14 +94,17 @@ inline Plan plan(int M, int N, int K, int cus) {
 }
 
 // Whether one launch quantizes the tokens, 16 in every workgroup, and multiplies: where their codes leave room in LDS and one round of
-// workgroups holds all outputs (or there are few tokens).  One launch and two (us, M x N x K): 1 x 4096 x 4096 4.5 and 6.3, 1 x 28672 x 8192
-// 23.9 and 31.8, 4 x 11008 x 1155 5.2 and 8.4, 8 x 4096 x 4096 5.8 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192 12.4 and 12.4, 64 x 4096 x 2048
-// 6.3 and 8.4, 256 x 1024 x 2048 6.1 and 8.0, 1024 x 256 x 256 4.8 and 5.7.  Against two where 16 long tokens meet few columns: 16 x 4096 x 4096 7.8
-// and 7.0, 17 x 256 x 4096 6.6 and 6.4; called one by one from Python these are 7.8 and 8.9, 6.6 and 8.9, since the second launch is
-// 4 us of the host's time.  Past a round: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5, 128 x 4096 x 2048 9.1 and 8.5.
+// workgroups of at most 64 columns holds all outputs, or one and a half of 48, of which a unit holds two if rows are short (or
+// there are few tokens).  One launch and two (us, M x N x K): 1 x 4096 x 4096 4.4 and 6.3, 1 x 28672 x 8192 23.9 and 31.8, 4 x 11008 x 1155 5.2 and 8.4,
+// 8 x 4096 x 4096 5.7 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192 12.4 and 12.4, 64 x 4096 x 2048 6.3 and 8.4, 256 x 1024 x 2048 6.1 and 8.0,
+// 250 x 777 x 1155 6.4 and 10.4, 333 x 777 x 2048 8.1 and 9.1.  Against two where 16 long tokens meet few columns: 16 x 4096 x 4096 7.8 and 7.0, 17 x 256 x 4096
+// 6.6 and 6.4, 333 x 777 x 1155 8.3 and 8.0; called one by one from Python these are 7.8 and 8.9, 6.6 and 8.9, 8.3 and 9.4, since the second
+// launch is 4 us of the host's time.  Past that: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5, 128 x 4096 x 2048 9.1 and 8.5, 512 x 1024 x 1155
+// 8.9 and 7.2.
 inline bool rows_fit(int M, int N, int K, int cus) {
-  const int64_t tokens = M < kTokens ? M : kTokens;
-  return M == 1 || (tokens * K <= 65536 && (M <= 8 || ((int64_t)N + 63) / 64 * ((M + kTokens - 1) / kTokens) <= cus));
+  const int64_t tokens = M < kTokens ? M : kTokens, blocks = (M + kTokens - 1) / kTokens;
+  return M == 1 || (tokens * K <= 65536 && (M <= 8 || ((int64_t)N + 63) / 64 * blocks <= cus ||
+                                            (K <= 2048 && ((int64_t)N + 47) / 48 * blocks * 2 <= 3 * cus)));
 }
 
 // Its workgroups: `columns` times 16 columns each, K's groups divided among `waves`.
@@ -119,6 +122,7 @@ inline RowsPlan rows_plan(int M, int N, int K, int cus) {
   int columns = 1;
   if (K < 4096 || M > 2)
     while (columns < 4 && (tiles + columns - 1) / columns * blocks > cus) ++columns;
+  if (M > 8 && (tiles + columns - 1) / columns * blocks > cus) columns = 3;   // one and a half rounds
   const double full = (double)((tiles + columns - 1) / columns * blocks) / cus, each = full > 1.0 ? full : 1.0;
   RowsPlan best = {columns, 4};
   double least = -1.0;

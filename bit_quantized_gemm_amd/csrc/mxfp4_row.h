@@ -47,6 +47,22 @@ __device__ __forceinline__ uint32_t codes8(const float (&u)[8]) {
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, u[6], u[7], 1.0f, 3);
 }
 
+// Elements 8 c .. 8 c + 7 of a row of K >= 8 that may begin at any element, in two steps, so that nothing waits between loads: past
+// the row's end its last eight are loaded, and `behind` moves those that are wanted into place, zeros behind them.
+__device__ __forceinline__ u32x4 load8_any(const uint16_t* x, int c, int K) {
+  return *reinterpret_cast<const w8a8::Unaligned*>(x + min(8 * c, K - 8));
+}
+__device__ __forceinline__ u32x4 behind(u32x4 w, int c, int K) {
+  const int s = 8 * c + 8 - K;                          // elements of the eight that are not there
+  if (s <= 0) return w;
+  uint64_t lo = (uint64_t)w[1] << 32 | w[0], hi = (uint64_t)w[3] << 32 | w[2];
+  if (s & 4) lo = hi, hi = 0;
+  const int b = 16 * (s & 3);
+  lo = lo >> b | (hi << 1) << (63 - b);
+  hi >>= b;
+  return s < 8 ? u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)} : u32x4{0, 0, 0, 0};
+}
+
 // The largest magnitude of eight 16-bit elements, as bits.
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t max8(u32x4 w) {

@@ -228,7 +228,8 @@ ONE = [(1, 33, 16384), (2, 20, 8192), (3, 48, 5461), (4, 65, 4096), (4, 16, 4097
        (1, 300, 255), (1, 33, 65536), (4, 20, 8192), (2, 20, 16384), (1, 5000, 300), (2, 8200, 1030), (7, 6001, 777), (16, 6000, 4096),
        (16, 4100, 2048), (16, 9000, 256), (9, 12300, 1200), (16, 12400, 300), (5, 16390, 2000), (8, 16400, 1500), (8, 20001, 8192), (13, 47, 5000),
        (16, 16384, 4096), (6, 11000, 10000), (15, 1, 4369), (8, 100, 31), (2, 4100, 32768), (1, 5000, 4097), (1, 12400, 3000), (1, 30000, 520), (17, 64, 256), (333, 250, 1155),
-       (64, 4096, 4096), (128, 1000, 2048), (100, 1000, 300), (1000, 64, 520), (4095, 5, 70), (256, 1024, 1025), (31, 8190, 100)]
+       (64, 4096, 4096), (128, 1000, 2048), (100, 1000, 300), (1000, 64, 520), (4095, 5, 70), (256, 1024, 1025), (31, 8190, 100), (333, 777, 1155),
+       (250, 777, 2047), (20, 300, 8), (40, 64, 9), (3, 33, 15)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)

@@ -62,14 +62,15 @@ def test_plans_fit_a_launch(plans):
 
 def test_one_launch_fits_lds(plans):
     """Sums, codes and scales of the tokens that one launch takes stay within 64 KB for every K, and its tiles in a grid."""
-    shapes = [(m, n, k) for m in (*range(1, 18), 33, 256, 1000, 4096, 4097, 1 << 24) for n in (1, 64, 65, 777, 4096, 11008, 16384, 16385, 1 << 20, 1 << 24)
+    shapes = [(m, n, k) for m in (*range(1, 18), 33, 256, 333, 1000, 4096, 4097, 1 << 24) for n in (1, 64, 65, 777, 784, 4096, 11008, 16384, 16385, 1 << 20, 1 << 24)
               for k in (1, 256, 257, 4095, 4096, 4097, 8192, 10922, 10923, 16384, 16385, 32768, 65536)]
     for (M, N, K), (_, _, _, _, columns, waves) in zip(shapes, plans(shapes)):
         pairs = (-(-K // 256) + 1) // 2
         tokens, blocks = min(M, 16), -(-M // 16)
-        assert (columns > 0) == (M == 1 or (tokens * K <= 65536 and (M <= 8 or -(-N // 64) * blocks <= 256))), (M, N, K)
+        round_ = -(-N // 64) * blocks <= 256 or (K <= 2048 and -(-N // 48) * blocks <= 384)
+        assert (columns > 0) == (M == 1 or (tokens * K <= 65536 and (M <= 8 or round_))), (M, N, K)
         if columns:
-            assert M <= 16 or -(-N // (16 * columns)) * blocks <= 256
+            assert M <= 8 or -(-N // (16 * columns)) * blocks <= (384 if columns == 3 and K <= 2048 else 256)
             assert columns <= 4 and waves in (4, 8, 12, 16)
             assert max(waves * columns * 1024, tokens * (pairs * 272 + 20)) <= 65536, (M, N, K)
             assert -(-N // (16 * columns)) * 64 * waves < 1 << 32
