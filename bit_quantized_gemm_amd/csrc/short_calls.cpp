@@ -1,14 +1,16 @@
 // Python extension module `_short`: the short way into libatom for calls whose tensors are all well-formed.
 //
-// A call from Python through ctypes spends most of a small operator's time on the host: each new tensor is 1.3 us, the checks 2 to
-// 3 us, the launch itself 3.  Each function here checks what its namesake in the Python binding documents, allocates the
-// outputs on the current stream and calls the C ABI.  Anything that is not well-formed, or that the C ABI refuses, returns None,
-// and the binding's full checks name the problem.  Host time of a call (us), the same checks in Python and here: linear_mxfp4 of one
-// token 7.2 and 5.1, of 16 11.0 and 8.9, atom_rmsnorm_w8a8 10.6 and 6.3, atom_kv4_extend 10.6 and 7.2.
+// A call from Python through ctypes spends most of a small operator's time on the host: each new tensor is 1.3 us (0.5 from
+// torch's factory called here, 0.2 as `fresh` makes it), the checks 2 to 3 us, the launch itself 3.3.  Each function here checks what its
+// namesake in the Python binding documents, allocates the outputs on the current stream and calls the C ABI.  Anything that is
+// not well-formed, or that the C ABI refuses, returns None, and the binding's full checks name the problem.  Host time of a call
+// (us), the same checks in Python and here: linear_mxfp4 of one token 7.2 and 4.8, atom_rmsnorm_w8a8 10.6 and 5.1, atom_kv4_extend 10.6 and
+// 5.5, atom_kv4_release 8.3 and 5.0.
 //
 // The addresses of the C entry points come from the binding (`bind`), so this module loads without the library.
 #include <Python.h>
 
+#include <ATen/EmptyTensor.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/impl/VirtualGuardImpl.h>
@@ -96,8 +98,11 @@ bool vector(const Here& h, PyObject* o, at::ScalarType type, int64_t n, const vo
   p = t->data_ptr();
   return true;
 }
-at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Here& h) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(h.device));
+// A new tensor on the current device, as torch's factory makes it when it has found its way there: from the allocator that the
+// factory takes.
+at::Tensor fresh(at::IntArrayRef shape, at::ScalarType type) {
+  static c10::Allocator* const allocator = at::empty({1}, at::TensorOptions().device(c10::DeviceType::CUDA)).storage().allocator();
+  return at::Tensor(at::detail::empty_generic(shape, allocator, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt));
 }
 
 // The status of call(stream), without the interpreter's lock: a launch may wait for its queue.
@@ -135,8 +140,8 @@ PyObject* linear_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {   // X, Wq
     return otherwise();
   const int64_t need = lib.atom_linear_mxfp4_workspace_bytes((int32_t)M, (int32_t)N, (int32_t)K);
   if (need < 0) return otherwise();
-  at::Tensor y = fresh({M, N}, x->scalar_type(), h), work;
-  if (need) work = fresh({need}, at::kByte, h);
+  at::Tensor y = fresh({M, N}, x->scalar_type()), work;
+  if (need) work = fresh({need}, at::kByte);
   void* const p = need ? work.data_ptr() : nullptr;
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_linear_mxfp4(x->data_ptr(), ld, kind(*x), w->data_ptr(), s->data_ptr(), bias, (int32_t)M, (int32_t)N, (int32_t)K,
@@ -164,7 +169,7 @@ PyObject* gemm_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {   // Xq, sx,
     scratch = tensor(a[7]);
     if (!scratch || scratch->dim() != 1 || !dense(h, scratch, at::kByte, {scratch->numel()})) return otherwise();
   }
-  at::Tensor y = fresh({M, N}, bf16 ? at::kBFloat16 : at::kHalf, h);
+  at::Tensor y = fresh({M, N}, bf16 ? at::kBFloat16 : at::kHalf);
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_gemm_mxfp4(x->data_ptr(), s->data_ptr(), w->data_ptr(), t->data_ptr(), bias, (int32_t)M, (int32_t)N, (int32_t)K, bf16,
                                y.data_ptr(), scratch ? scratch->data_ptr() : nullptr, scratch ? scratch->numel() : 0, stream);
@@ -181,7 +186,7 @@ PyObject* quantize_mxfp4(PyObject*, PyObject* const* a, Py_ssize_t n) {   // X
   int64_t ld;
   if (!rows2d(h, x, ld)) return otherwise();
   const int64_t rows = x->size(0), K = x->size(1), g = groups_of(K);
-  at::Tensor q = fresh({rows, g * (ATOM_MX_GROUP / 2)}, at::kByte, h), s = fresh({g, rows, 8}, at::kByte, h);
+  at::Tensor q = fresh({rows, g * (ATOM_MX_GROUP / 2)}, at::kByte), s = fresh({g, rows, 8}, at::kByte);
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_quantize_mxfp4(x->data_ptr(), ld, kind(*x), (int32_t)rows, (int32_t)K, q.data_ptr(), s.data_ptr(), stream);
   });
@@ -201,7 +206,7 @@ PyObject* dequantize(PyObject* const* a, Py_ssize_t n, bool mx) {
          : !lib.atom_dequantize_w8a8 || !dense(h, q, at::kChar, {rows, (K + 127) / 128 * 128}) || !dense(h, s, at::kFloat, {rows}))
     return otherwise();
   const bool bf16 = PyObject_IsTrue(a[3]) == 1;
-  at::Tensor x = fresh({rows, K}, bf16 ? at::kBFloat16 : at::kHalf, h);
+  at::Tensor x = fresh({rows, K}, bf16 ? at::kBFloat16 : at::kHalf);
   const int status = on_stream(h, [&](void* stream) {
     return mx ? lib.atom_dequantize_mxfp4(q->data_ptr(), s->data_ptr(), (int32_t)rows, (int32_t)K, bf16, x.data_ptr(), stream)
               : lib.atom_dequantize_w8a8(q->data_ptr(), static_cast<const float*>(s->data_ptr()), (int32_t)rows, (int32_t)K, bf16,
@@ -235,9 +240,9 @@ PyObject* rmsnorm(PyObject* const* a, Py_ssize_t n, bool mx) {
     if (!rows2d(h, r, ldr) || r->scalar_type() != x->scalar_type() || r->sizes() != x->sizes()) return otherwise();
   }
   const double eps = PyFloat_AS_DOUBLE(a[2]);
-  at::Tensor q = mx ? fresh({rows, g * (ATOM_MX_GROUP / 2)}, at::kByte, h) : fresh({rows, (K + 127) / 128 * 128}, at::kChar, h);
-  at::Tensor s = mx ? fresh({g, rows, 8}, at::kByte, h) : fresh({rows}, at::kFloat, h), sum;
-  if (r) sum = fresh({rows, K}, x->scalar_type(), h);
+  at::Tensor q = mx ? fresh({rows, g * (ATOM_MX_GROUP / 2)}, at::kByte) : fresh({rows, (K + 127) / 128 * 128}, at::kChar);
+  at::Tensor s = mx ? fresh({g, rows, 8}, at::kByte) : fresh({rows}, at::kFloat), sum;
+  if (r) sum = fresh({rows, K}, x->scalar_type());
   const void* const pr = r ? r->data_ptr() : nullptr;
   void* const ph = r ? sum.data_ptr() : nullptr;
   const int status = on_stream(h, [&](void* stream) {
@@ -289,8 +294,8 @@ PyObject* kv4_extend(PyObject*, PyObject* const* a, Py_ssize_t n) {   // lens, n
   const Here h;
   State s;
   if (!s.of(h, a[0], a[2], a[3], a[4]) || !dense(h, more, at::kInt, {s.batch})) return otherwise();
-  at::Tensor slots = fresh({total}, at::kLong, h), start = fresh({s.batch + 1}, at::kInt, h), lens = fresh({s.batch}, at::kInt, h),
-             state = fresh({2}, at::kInt, h);
+  at::Tensor slots = fresh({total}, at::kLong), start = fresh({s.batch + 1}, at::kInt), lens = fresh({s.batch}, at::kInt),
+             state = fresh({2}, at::kInt);
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_kv4_extend(ptr<int32_t>(*s.lens), ptr<int32_t>(*more), ptr<int32_t>(*s.table), s.batch, s.width, (int32_t)page,
                                ptr<int32_t>(*s.free), s.capacity, ptr<int32_t>(*s.state), ptr<int64_t>(slots), (int32_t)total,
@@ -310,7 +315,7 @@ PyObject* kv4_release(PyObject*, PyObject* const* a, Py_ssize_t n) {   // done, 
   const Here h;
   State s;
   if (!s.of(h, a[1], a[2], a[3], a[4]) || !dense(h, done, at::kBool, {s.batch})) return otherwise();
-  at::Tensor lens = fresh({s.batch}, at::kInt, h), state = fresh({2}, at::kInt, h);
+  at::Tensor lens = fresh({s.batch}, at::kInt), state = fresh({2}, at::kInt);
   const int status = on_stream(h, [&](void* stream) {
     return lib.atom_kv4_release(ptr<uint8_t>(*done), ptr<int32_t>(*s.lens), ptr<int32_t>(*s.table), s.batch, s.width, (int32_t)page,
                                 ptr<int32_t>(*s.free), s.capacity, ptr<int32_t>(*s.state), ptr<int32_t>(lens), ptr<int32_t>(state), stream);
