@@ -16,7 +16,7 @@ constexpr int kDividedKind = 2;  // the tile size whose plans may divide K
 constexpr int kBM[kKinds] = {16, 32, 64, 64, 128, 256, 256}, kBN[kKinds] = {16, 16, 64, 128, 128, 128, 256};
 
 // Waves of a few-rows workgroup, which divide K's groups: as few turns of whole batches as possible, then as little behind
-// the ranges' ends.  (1 x 4096 x 4096, 16 groups: 4 waves 4.9 us, 8 5.3, 16 6.8; 1 x 4096 x 11008, 43 groups: 4 11.5, 8 9.7, 11 7.9.)
+// the ranges' ends.  (1 x 4096 x 4096, 16 groups: 4 waves 4.0 us, 8 5.0, 16 5.8; 1 x 4096 x 11008, 43 groups: 4 8.6, 8 8.6, 11 7.2, 16 8.3.)
 inline int rows_waves(int groups) {
   int best = 4, turns = 1 << 30, loaded = 1 << 30;
   for (int w = 4; w <= 16; ++w) {
@@ -110,9 +110,10 @@ inline bool rows_fit(int M, int N, int K, int cus) {
 // Its workgroups: `columns` times 16 columns each, K's groups divided among `waves`.
 //   Columns: as few as give each unit one workgroup (the tokens are quantized once for all of them); one for long rows of one or two
 //     tokens, whose weights take longer than the quantizing (us, one and three: 1 x 11008 x 4096 7.3 and 7.9, 4 x 11008 x 4096 8.5 and 8.2).
-//   Waves: what each costs its unit, how often each waits for weights and how many units of 512 elements it quantizes.
-// Fitted on 256 units to 190 shapes (1 to 16 tokens, 1024 to 28672 columns, K 512 to 11008): the choice is 1.2% slower than the best of
-// one to four columns and 4 to 16 waves on average.
+//   Waves: what each costs its unit, how often each waits for weights and how many units of 512 elements it quantizes.  Where several
+//     workgroups come to a unit these wait for each other's weights: four (us, 4, 8 and 12: 8 x 28672 x 8192 30.0, 31.5, 34.2).
+// On 256 units, over 245 shapes (1 to 512 tokens, 300 to 28672 columns, K 512 to 11008): the choice is 0.8% slower than the best of one to
+// four columns and 4 to 16 waves on average, and two launches take 1.27 times its time.
 struct RowsPlan {
   int columns, waves;
 };
@@ -126,7 +127,7 @@ inline RowsPlan rows_plan(int M, int N, int K, int cus) {
   const double full = (double)((tiles + columns - 1) / columns * blocks) / cus, each = full > 1.0 ? full : 1.0;
   RowsPlan best = {columns, 4};
   double least = -1.0;
-  for (int w = 4; w <= 16; w += 4) {
+  for (int w = 4; w <= (each > 1.5 ? 4 : 16); w += 4) {
     const int flight = kBatch / columns, turns = ((groups + w - 1) / w + flight - 1) / flight;
     const double time = 4.0 * w * each + 16.0 * turns + 3.0 * ((units + w - 1) / w);
     if (least < 0.0 || time < least) {
