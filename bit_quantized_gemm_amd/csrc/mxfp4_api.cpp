@@ -21,8 +21,7 @@ bool plan_of(int32_t M, int32_t N, int32_t K, atom::MxPlan& plan) {
   plan = atom::mx_plan(M, N, K);
   return plan.tiles > 0;
 }
-int64_t linear_bytes(int32_t M, int32_t N, int32_t K, const atom::MxPlan& plan) {
-  if (atom::mx_one_launch(M, N, K)) return 0;
+int64_t linear_bytes(int32_t M, int32_t K, const atom::MxPlan& plan) {
   return (int64_t)(code_bytes(M, K) + up16(scale_bytes(M, K))) + atom::mx_workspace_bytes(plan);
 }
 
@@ -125,18 +124,21 @@ int atom_gemm_mxfp4(const void* Xq, const void* sx, const void* Wq, const void* 
 }
 
 int64_t atom_linear_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K) {
+  if (!valid_gemm8(M, N, K)) return -(int64_t)ATOM_E_SHAPE;
+  if (atom::mx_one_launch(M, N, K)) return 0;
   atom::MxPlan plan;
-  if (!plan_of(M, N, K, plan)) return -(int64_t)ATOM_E_SHAPE;
-  return linear_bytes(M, N, K, plan);
+  return plan_of(M, N, K, plan) ? linear_bytes(M, K, plan) : -(int64_t)ATOM_E_SHAPE;
 }
 
 int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq, const void* sw, const void* bias, int32_t M,
                       int32_t N, int32_t K, void* Y, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!X || !Wq || !sw || !Y) return ATOM_E_NULL;
-  atom::MxPlan plan;
-  if (!plan_of(M, N, K, plan) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  if (!valid_gemm8(M, N, K) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  const bool one = atom::mx_one_launch(M, N, K);
+  atom::MxPlan plan = {};
+  if (!one && !plan_of(M, N, K, plan)) return ATOM_E_SHAPE;
   if (!valid_x(X, ldx, M, K)) return aligned(X, 2) ? ATOM_E_SHAPE : ATOM_E_ALIGN;
-  const int64_t need = linear_bytes(M, N, K, plan);
+  const int64_t need = one ? 0 : linear_bytes(M, K, plan);
   if (need > 0 && !workspace) return ATOM_E_NULL;
   if (workspace_bytes < need) return ATOM_E_SHAPE;
   if (!aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y) || (need > 0 && !aligned16(workspace)))
@@ -147,7 +149,7 @@ int atom_linear_mxfp4(const void* X, int64_t ldx, int32_t dtype, const void* Wq,
   if (int s = check_overlap(in, bias ? 4 : 3, out, need > 0 ? 2 : 1)) return s;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const uint8_t *wq = static_cast<const uint8_t*>(Wq), *ws = static_cast<const uint8_t*>(sw);
-  if (need == 0)
+  if (one)
     return hip_status(atom::launch_linear_rows_mxfp4(static_cast<const uint16_t*>(X), ldx, wq, ws,
                                                      static_cast<const uint16_t*>(bias), M, N, K, dtype == ATOM_BF16,
                                                      static_cast<uint16_t*>(Y), st));

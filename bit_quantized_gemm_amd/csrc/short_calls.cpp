@@ -4,7 +4,7 @@
 // torch's factory called here, 0.2 as `fresh` makes it), the checks 2 to 3 us, the launch itself 3.3.  Each function here checks what its
 // namesake in the Python binding documents, allocates the outputs on the current stream and calls the C ABI.  Anything that is
 // not well-formed, or that the C ABI refuses, returns None, and the binding's full checks name the problem.  Host time of a call
-// (us), the same checks in Python and here: linear_mxfp4 of one token 7.2 and 4.8, atom_rmsnorm_w8a8 10.6 and 5.1, atom_kv4_extend 10.6 and
+// (us), the same checks in Python and here: linear_mxfp4 of one token 7.2 and 4.6, atom_rmsnorm_w8a8 10.6 and 5.1, atom_kv4_extend 10.6 and
 // 5.5, atom_kv4_release 8.3 and 5.0.
 //
 // The addresses of the C entry points come from the binding (`bind`), so this module loads without the library.
