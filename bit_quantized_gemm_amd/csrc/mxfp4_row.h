@@ -1,5 +1,5 @@
-// Pieces of the MXFP4 row quantizer (atom_mxfp4.h), shared by its kernel, the norm in front of it and the product of
-// very few tokens, which quantizes them itself.  Eight elements a lane, four lanes a block, 32 lanes a group.
+// Pieces of the MXFP4 row quantizer (atom_mxfp4.h), shared by its kernel, the norm in front of it and the product that
+// quantizes its tokens itself.  Eight elements a lane, four lanes a block, 32 lanes a group.
 #pragma once
 
 #include "serve_internal.h"

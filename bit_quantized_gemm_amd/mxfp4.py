@@ -156,7 +156,7 @@ def atom_gemm_mxfp4(Xq, sx, Wq, sw, K, bias=None, Y=None, dtype=None, workspace=
 def linear_mxfp4(X, Wq, sw, bias=None, Y=None, workspace=None, stream=None):
     """The layer: X (fp16 / bf16 [M, K]; rows may lie apart) quantized and multiplied with packed weights in
     one call.  Y has X's type.  `workspace`: 1-D uint8 of at least ``atom_linear_mxfp4_workspace_bytes``
-    bytes (calls that may overlap need one each; none for the few tokens that take one launch), else a torch buffer is
+    bytes (calls that may overlap need one each; none for few tokens or outputs, which take one launch), else a torch buffer is
     taken for the call when one is needed."""
     if stream is None and Y is None and workspace is None and _bq._SHORT is not None:
         Y = _bq._SHORT.linear_mxfp4(X, Wq, sw, bias)

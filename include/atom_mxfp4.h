@@ -70,8 +70,8 @@ int atom_gemm_mxfp4(const void *Xq, const void *sx, const void *Wq, const void *
                     void *stream);
 
 /*
- * The layer in one call: quantizes X into the workspace, then Y as above; the few tokens that take one launch
- * need none (0 bytes, NULL).  The workspace holds at least atom_linear_mxfp4_workspace_bytes(M, N, K) bytes
+ * The layer in one call: quantizes X into the workspace, then Y as above; few tokens, or few outputs, take
+ * one launch that needs none (0 bytes, NULL).  The workspace holds at least atom_linear_mxfp4_workspace_bytes(M, N, K) bytes
  * (ATOM_E_SHAPE otherwise); its contents on entry do not matter, and calls that may overlap in time need one each.
  */
 int64_t atom_linear_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K);
