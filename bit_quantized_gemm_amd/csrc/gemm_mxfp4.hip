@@ -360,16 +360,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WAVES))) vo
     const int r = it * (64 / kChunks) + lane / kChunks, m = m0 + wm * WM + r;
     u32x4 v = *reinterpret_cast<const u32x4*>(own + (r * kChunks + (c ^ (r & (kChunks - 1)))) * 16);
     if ((it * (64 / kChunks)) & 16) v = u32x4{v[2], v[3], v[0], v[1]};
-    if (m < M) {
-      uint16_t* dst = Y + (size_t)m * N + n;
-      if ((N & 7) == 0) {
-        if (n < N) *reinterpret_cast<u32x4*>(dst) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (n + e < N) dst[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
-      }
-    }
+    if (m < M) mx::store8(Y + (size_t)m * N + n, v, N - n);
   }
 }
 
@@ -391,8 +382,9 @@ __global__ __launch_bounds__(256) void finish_kernel(const float* __restrict__ p
   float y[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = biased(a[e], bias ? T::load(bias[min(n + e, N - 1)]) : 0.0f);
-  if (n + 4 <= N && (N & 3) == 0) {
-    *reinterpret_cast<u32x2*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
+  if (n + 4 <= N) {
+    typedef u32x2 Unaligned __attribute__((aligned(2)));
+    *reinterpret_cast<Unaligned*>(dst) = u32x2{pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3])};
   } else {
     for (int e = 0; e < 4; ++e)
       if (n + e < N) dst[e] = T::store(y[e]);

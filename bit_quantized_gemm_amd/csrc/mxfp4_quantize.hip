@@ -70,15 +70,8 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(const uint8_t* __r
       const float a = m < 4 ? 0.5f * (float)m : (float)(2 + (m & 1)) * (m < 6 ? 1.0f : 2.0f);
       v[j] = (q & 8 ? -a : a) * scale;
     }
-    uint16_t* dst = X + (int64_t)row * K + 8 * c;
-    if (VEC) {
-      *reinterpret_cast<u32x4*>(dst) =
-          u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (8 * c + j < K) dst[j] = T::store(v[j]);
-    }
+    mx::store8(X + (int64_t)row * K + 8 * c, u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])},
+               VEC ? 8 : K - 8 * c);
   }
 }
 

@@ -88,13 +88,7 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
         asm("" : "+v"(lo), "+v"(hi));                   // two roundings, as two steps have them: never one fused one
         h[i][j] = pack2<T>(lo, hi);
       }
-      if (VEC) {
-        if (8 * c < a.K) *reinterpret_cast<u32x4*>(dst + 8 * c) = h[i];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (8 * c + j < a.K) dst[8 * c + j] = (uint16_t)(h[i][j / 2] >> (16 * (j & 1)));
-      }
+      if (!VEC || 8 * c < a.K) mx::store8(dst + 8 * c, h[i], VEC ? 8 : a.K - 8 * c);
     }
   } else {
 #pragma unroll
@@ -255,15 +249,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* __restric
     v[j] = (float)(int8_t)(q[j / 4] >> (8 * (j & 3))) * s;
     asm("" : "+v"(v[j]));
   }
-  uint16_t* dst = X + (size_t)row * K + 8 * c;
-  if (VEC) {
-    *reinterpret_cast<u32x4*>(dst) =
-        u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])};
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (8 * c + j < K) dst[j] = T::store(v[j]);
-  }
+  mx::store8(X + (size_t)row * K + 8 * c, u32x4{pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7])},
+             VEC ? 8 : K - 8 * c);
 }
 
 }  // namespace
