@@ -5,16 +5,21 @@
 // the threads that share it, and leaves as codes.  With a residual: 8192 x 8192 to int8 84 us, to MXFP4 82 us (5.6 and 5.3 TB/s, a copy of
 // memory reaches 4.75 to 5.1), 2048 x 11008 34 and 37 us, 16 x 4096 3.1 and 3.3 us, of which the launch is more than half.
 //
-// Exact codes.  p = h * w is exact in fp32 (two 8- or 11-bit significands), so y = p / sqrt(mean + eps) is one row factor
-// away from exact: the sum of squares and the factor are fp64, and each code is made from p times that factor in fp32.  Its
-// error is at most two roundings, 2^-23 of the value, so only values that close to the border of two codes can come out
-// wrong: they are seen by their distance to it, and the wave makes that chunk's codes again in fp64.  (A norm rounded to 32
-// bits gives other codes for one value in about 2^16, and for a block's exponent the whole block's.)
+// Exact codes.  p = h * w is exact in fp32 (two 8- or 11-bit significands), so y = p / root, root = sqrt(mean + eps), is one
+// row's number away from exact: the sum of squares and the root are fp64, and each code is made from p times one factor in
+// fp32.  Its error is two roundings (three for int8) of 2^-24, so only values that close to the border of two codes can come out
+// wrong: they are seen by their distance to it, and the wave makes that chunk's codes again in fp64.  A factor puts a value that
+// lies on a border (a row of +-3 has whole halves) a step of 2^-53 beside it: what even fp64 leaves that near is made by the
+// formula's own divisions, behind everything else.  (A norm rounded to 32 bits gives other codes for one value in about 2^16,
+// and for a block's exponent the whole block's.)
 #include "mxfp4_row.h"
+#include "norm_steps.h"
 #include "w8a8_rows.h"
 
 namespace atom {
 namespace {
+
+using rms::divided;
 
 struct Norm {
   const uint16_t *X, *R, *W;
@@ -51,11 +56,71 @@ __device__ __forceinline__ float wave_top(float v) {
   return __builtin_bit_cast(float, max(b, (uint32_t)__shfl_xor((int)b, 32)));
 }
 
-// Code of one value in fp64 units of its scale: nearest, ties to the even code, saturating.
-__device__ __forceinline__ uint32_t fp4_code(double y) {
-  const double a = __builtin_fabs(y);
-  const uint32_t m = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
-  return m | (uint32_t)(__builtin_bit_cast(uint64_t, y) >> 63) << 3;
+// Code of one magnitude in fp64 units of its scale: nearest, ties to the even code, saturating.
+__device__ __forceinline__ uint32_t fp4_code(double a) {
+  return (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5.0);
+}
+// Whether a number is within eight units in the last place of one with `zeros` zeros at the end of its significand.
+__device__ __forceinline__ bool beside(double a, int zeros) {
+  return ((__builtin_bit_cast(uint64_t, a) + 8) & (((uint64_t)1 << zeros) - 1)) < 16;
+}
+
+// The scale of a block whose largest |y| this is: its byte, and 1 / scale.
+struct Block {
+  uint32_t byte;
+  double unit;
+  __device__ __forceinline__ explicit Block(double y) {
+    const int e = (int)(__builtin_bit_cast(uint64_t, y) >> 52);
+    byte = e == 2047 ? mx::kNanScale : (uint32_t)min(max(e - 1023 - 2 + 127, 0), 252);
+    unit = __builtin_bit_cast(double, (uint64_t)(1023 + 127 - (int)byte) << 52);
+  }
+};
+
+// The wave's chunks of `which` again, by the formula's own steps.  Rare, and so behind everything else: a loop over h and w as they
+// are in memory, which leaves the common way its registers and its code (inside it, 4096 x 4097 to int8 takes 32.0 us, 29.4 so).
+template <class T, int THREADS, bool VEC, bool MX>
+__device__ __forceinline__ void again(const Norm& a, int row, int t, uint32_t which, float top, double root, double rstd) {
+  const uint16_t* from = a.R ? a.H + (size_t)row * a.ldh : a.X + (size_t)row * a.ldx;
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (; which; which &= which - 1) {
+    const int c = t + __builtin_ctz(which) * THREADS;
+    const u32x4 h = w8a8::load8<VEC>(from, c, a.K), w = w8a8::load8<VEC>(a.W, c, a.K);
+    float p[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      p[j] = elem<T>(h[j / 2], j & 1) * elem<T>(w[j / 2], j & 1);
+      m = max(m, __builtin_bit_cast(uint32_t, p[j]) & 0x7FFFFFFFu);
+    }
+    if constexpr (!MX) {
+      const int Kp = (a.K + 127) / 128 * 128;
+      const float s = (float)divided(divided((double)top, root, rstd), 127.0, 1.0 / 127.0);
+      const double per = s > 0.0f ? 1.0 / (double)s : 0.0;
+      u32x2 o = {0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const double u = divided(divided((double)p[j], root, rstd), (double)s, per);
+        o[j / 4] |= ((uint32_t)(int)__builtin_fmin(__builtin_fmax(__builtin_rint(u), -127.0), 127.0) & 0xFFu) << (8 * (j & 3));
+      }
+      if (8 * c < Kp) *reinterpret_cast<u32x2*>(a.Xq + (size_t)row * Kp + 8 * c) = o;
+    } else {
+      const int Kp = mx::padded(a.K);
+      const Block k(divided((double)__builtin_bit_cast(float, mx::block_max(m)), root, rstd));
+      uint32_t code = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        code |= (fp4_code(divided((double)__builtin_fabsf(p[j]), root, rstd) * k.unit) | __builtin_bit_cast(uint32_t, p[j]) >> 31 << 3)
+                << (4 * j);
+      if (k.byte == mx::kNanScale) code = 0;
+      const uint32_t four = mx::gather_scales(k.byte, lane);
+      if (8 * c < Kp) {
+        *reinterpret_cast<uint32_t*>(a.Xq + (size_t)row * (Kp / 2) + 4 * c) = code;
+        if ((lane & 15) == 0)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.sx) + ((int64_t)(c >> 5) * a.rows + row) * 8 + ((c >> 4) & 1) * 4) = four;
+      }
+    }
+  }
 }
 
 template <class T, int THREADS, int CH, bool VEC, bool MX>
@@ -122,15 +187,16 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       if (!MX) top = __builtin_fmaxf(top, tops[i]);
     }
   }
-  const double rstd = 1.0 / __builtin_sqrt(total * a.inv_k + a.eps);
+  const double root = __builtin_sqrt(divided(total, (double)a.K, a.inv_k) + a.eps), rstd = 1.0 / root;
+  uint32_t undecided = 0;                               // the wave's chunks (bit i) with a value next to a border in 64 bits too
 
   if constexpr (!MX) {
     const int Kp = (a.K + 127) / 128 * 128;
-    const float s = (float)((double)top * rstd / 127.0);
+    const float s = (float)divided(divided((double)top, root, rstd), 127.0, 1.0 / 127.0);
     if (t == 0) static_cast<float*>(a.sx)[row] = s;
-    const double f = s > 0.0f ? rstd / (double)s : 0.0;
-    const float f32 = (float)f;
-    // A factor beyond fp32, or a scale whose own rounding can carry a code past 127: all codes in fp64.
+    // y / s without the norm, which cancels but for s's own rounding: no code waits for the sum of squares
+    const float f32 = 127.0f / top;
+    // a factor beyond fp32, or a scale whose own rounding can carry a code past 127
     const bool extreme = !(f32 < 0x1p100f) || s < 0x1p-100f;
     uint8_t* q = a.Xq + (size_t)row * Kp;
 #pragma unroll
@@ -145,13 +211,17 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
         far = __builtin_fmaxf(far, __builtin_fabsf(u - (k - 12582912.0f)));
         b[j] = __builtin_bit_cast(uint32_t, k);
       }
-      // |u| <= 127 (1 + 2^-23), so u is within 2^-15.9 of the exact value
-      if (__builtin_amdgcn_ballot_w64(extreme || far >= 0.5f - 0x1p-15f)) {
+      // three roundings (of the factor, of u and of s) of at most 127: u is within 381 x 2^-24 of the exact value, 2.27e-5
+      if (__builtin_amdgcn_ballot_w64(extreme || far >= 0.5f - 0x1.9p-16f)) {
+        const double f = rstd / (double)s;
+        double beside = 0.0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const double u = (double)(elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1)) * f;
-          b[j] = (uint32_t)(int)__builtin_fmin(__builtin_fmax(__builtin_rint(u), -127.0), 127.0);
+          const double u = (double)(elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1)) * f, k = __builtin_rint(u);
+          beside = __builtin_fmax(beside, __builtin_fabs(u - k));
+          b[j] = (uint32_t)(int)k;
         }
+        if (__builtin_amdgcn_ballot_w64(extreme || beside >= 0.5 - 0x1p-40)) undecided |= 1u << i;
       }
       if (8 * c < Kp) {
         u32x2 o;
@@ -175,11 +245,10 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
         p[j] = elem<T>(h[i][j / 2], j & 1) * elem<T>(w[i][j / 2], j & 1);
         m = max(m, __builtin_bit_cast(uint32_t, p[j]) & 0x7FFFFFFFu);
       }
-      // the block's largest |y| in fp64, and its exponent
-      const double y = (double)__builtin_bit_cast(float, mx::block_max(m)) * rstd;
-      const int e = (int)(__builtin_bit_cast(uint64_t, y) >> 52);
-      const uint32_t byte = e == 2047 ? mx::kNanScale : (uint32_t)min(max(e - 1023 - 2 + 127, 0), 252);
-      const double f = rstd * __builtin_bit_cast(double, (uint64_t)(1023 + 127 - (int)byte) << 52);
+      m = mx::block_max(m);
+      const double y = (double)__builtin_bit_cast(float, m) * rstd;
+      const Block k(y);
+      const double f = rstd * k.unit;
       const float f32 = (float)f;
       float u[8];
       uint32_t near = 8;                                // distance to a border, in units of the last place
@@ -193,12 +262,18 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       uint32_t code = mx::codes8(u);
       // (the last: a factor beyond fp32)
       if (__builtin_amdgcn_ballot_w64(near < 8 || !(f32 < 0x1p100f))) {
+        bool tie = m != 0 && beside(y, 52);             // the exponent's: a power of two is 4 or 8 of the scale, a border here too
         code = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) code |= fp4_code((double)p[j] * f) << (4 * j);
+        for (int j = 0; j < 8; ++j) {
+          const double v = __builtin_fabs((double)p[j] * f);
+          tie |= v >= 0.125 && beside(v, 50);
+          code |= (fp4_code(v) | __builtin_bit_cast(uint32_t, p[j]) >> 31 << 3) << (4 * j);
+        }
+        if (__builtin_amdgcn_ballot_w64(tie)) undecided |= 1u << i;
       }
-      if (byte == mx::kNanScale) code = 0;
-      const uint32_t four = mx::gather_scales(byte, lane);
+      if (k.byte == mx::kNanScale) code = 0;
+      const uint32_t four = mx::gather_scales(k.byte, lane);
       if (8 * c < Kp) {
         *reinterpret_cast<uint32_t*>(q + 4 * c) = code;
         if ((lane & 15) == 0)
@@ -207,6 +282,7 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       }
     }
   }
+  if (undecided) again<T, THREADS, VEC, MX>(a, row, t, undecided, top, root, rstd);
 }
 
 template <class T, bool MX, int THREADS, int CH>

@@ -6,9 +6,11 @@
  *   h = round(fl32(x + r)) in the rows' own type (h = x without a residual),
  *   y = h * w / sqrt(mean(h^2) + eps), not rounded,
  * and y's codes and scales are those of atom_quantize_w8a8 (s = fl32(max|y| / 127), code = clamp(
- * rint_even(y / s), -127, 127)) or of atom_quantize_mxfp4.  The sum of squares and the norm are taken in 64
- * bits, the products h * w in fp32 (exact for fp16; for bf16 while they lie between 2^-110 and 2^127),
- * and a code or exponent that 32 bits leave undecided is made in 64: codes and scales are those of the formulas bit for bit.
+ * rint_even(y / s), -127, 127)) or of atom_quantize_mxfp4.  The products h * w are taken in fp32 (exact for fp16; for
+ * bf16 while they lie between 2^-110 and 2^127), everything else in 64 bits with one rounding a step: the sum of squares (in an
+ * order of the kernel's own), its division by K, the root, the division by it and by s.  Codes and scales are those of these
+ * steps bit for bit: a value on the border of two codes goes the formulas' way wherever the sum of squares is exact, and
+ * else one within a few 2^-53 of a border may go either way.
  * A row that holds an inf or NaN, or an h * w beyond fp32, gets unspecified codes and scales (no fault).
  *
  * The conventions of atom.h hold, with those of atom_w8a8.h for `dtype` and rows: X, residual and H rows
