@@ -21,4 +21,12 @@ NORM_FN double divided(double a, double b, double r) {
   return __builtin_fma(__builtin_fma(-q, b, a), r, q);
 }
 
+// Distance of an fp32 number (as bits) from the nearest border of two MXFP4 codes, or of two exponents (4 and 8): in units of its last
+// place, offset by 4, so that up to four below to three above are 0 to 7.  All of these have 21 zeros at the end of their
+// significands; smaller numbers than the lowest border, 0.25, are none whatever their bits: zeros, above all.
+NORM_FN uint32_t border_distance(uint32_t bits) {
+  const uint32_t a = bits & 0x7FFFFFFFu;
+  return a < 0x3E000000u ? 0x1FFFFFu : (a + 4) & 0x1FFFFFu;
+}
+
 }  // namespace rms

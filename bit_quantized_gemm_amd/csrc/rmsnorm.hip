@@ -2,8 +2,9 @@
 // (formulas: atom_norm.h).
 //
 // What bounds it: HBM.  A row is read once (twice its bytes with a residual, and once out again), kept in registers by
-// the threads that share it, and leaves as codes.  With a residual: 8192 x 8192 to int8 84 us, to MXFP4 82 us (5.6 and 5.3 TB/s, a copy of
-// memory reaches 4.75 to 5.1), 2048 x 11008 34 and 37 us, 16 x 4096 3.1 and 3.3 us, of which the launch is more than half.
+// the threads that share it, and leaves as codes.  With a residual, graph replays over rows from HBM: 8192 x 8192 to int8 84.5 us, to
+// MXFP4 81.1 us (5.6 and 5.4 TB/s; a copy of memory reaches 4.75 to 5.1), 2048 x 11008 30.0 and 31.6 us, 16 x 4096 3.1 and 3.2 us, of
+// which the launch is more than half.
 //
 // Exact codes.  p = h * w is exact in fp32 (two 8- or 11-bit significands), so y = p / root, root = sqrt(mean + eps), is one
 // row's number away from exact: the sum of squares and the root are fp64, and each code is made from p times one factor in
@@ -249,7 +250,7 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       const double y = (double)__builtin_bit_cast(float, m) * rstd;
       const Block k(y);
       const double f = rstd * k.unit;
-      const float f32 = (float)f;
+      const float f32 = m ? (float)f : 0.0f;            // a block of zeros, as behind K: any factor
       float u[8];
       uint32_t near = 8;                                // distance to a border, in units of the last place
 #pragma unroll
@@ -262,15 +263,20 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       uint32_t code = mx::codes8(u);
       // (the last: a factor beyond fp32)
       if (__builtin_amdgcn_ballot_w64(near < 8 || !(f32 < 0x1p100f))) {
-        bool tie = m != 0 && beside(y, 52);             // the exponent's: a power of two is 4 or 8 of the scale, a border here too
-        code = 0;
+        near = 8;                                       // (zeros come as far as here: sums that cancel are one in 10^4 of fp16 rows)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double v = __builtin_fabs((double)p[j] * f);
-          tie |= v >= 0.125 && beside(v, 50);
-          code |= (fp4_code(v) | __builtin_bit_cast(uint32_t, p[j]) >> 31 << 3) << (4 * j);
+        for (int j = 0; j < 8; ++j) near = min(near, rms::border_distance(__builtin_bit_cast(uint32_t, u[j])));
+        if (__builtin_amdgcn_ballot_w64(near < 8 || !(f32 < 0x1p100f))) {
+          bool tie = m != 0 && beside(y, 52);           // the exponent's: a power of two is 4 or 8 of the scale, a border here too
+          code = 0;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const double v = __builtin_fabs((double)p[j] * f);
+            tie |= v >= 0.125 && beside(v, 50);
+            code |= (fp4_code(v) | __builtin_bit_cast(uint32_t, p[j]) >> 31 << 3) << (4 * j);
+          }
+          if (__builtin_amdgcn_ballot_w64(tie)) undecided |= 1u << i;
         }
-        if (__builtin_amdgcn_ballot_w64(tie)) undecided |= 1u << i;
       }
       if (k.byte == mx::kNanScale) code = 0;
       const uint32_t four = mx::gather_scales(k.byte, lane);

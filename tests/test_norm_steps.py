@@ -64,3 +64,35 @@ def test_divided_is_the_division(tmp_path):
     bad, count, product = map(int, run(tmp_path, DIVIDED))
     assert count > 2e7 and product > count // 10
     assert bad == 0
+
+
+BORDERS = r"""
+#include <stdio.h>
+#include "norm_steps.h"
+int main() {                                                          // numbers in, distances out
+  float f;
+  int step;
+  while (scanf("%f %d", &f, &step) == 2) {
+    uint32_t b;
+    __builtin_memcpy(&b, &f, 4);
+    printf("%u\n", rms::border_distance(b + step));
+  }
+}
+"""
+
+
+def test_borders_are_seen_and_nothing_else(tmp_path):
+    """Each border and its neighbours of either sign; no zero, none of the padding's, nothing far from a border."""
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("no g++")
+    (tmp_path / "b.cpp").write_text(BORDERS)
+    subprocess.run([cxx, "-O1", "-std=c++17", "-Wall", "-Werror", "-I" + CSRC, str(tmp_path / "b.cpp"), "-o", str(tmp_path / "b")], check=True)
+
+    def distances(pairs):
+        text = "\n".join(f"{f!r} {s}" for f, s in pairs)
+        return list(map(int, subprocess.run([str(tmp_path / "b")], input=text, capture_output=True, text=True, check=True).stdout.split()))
+    borders = [s * b for b in (0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 4.0, 8.0) for s in (1.0, -1.0)]
+    assert all(d < 8 for d in distances([(b, s) for b in borders for s in range(-4, 4)]))
+    assert all(d >= 8 for d in distances([(b, s) for b in borders for s in (-20, -5, 4, 20, 1000)]))
+    assert all(d >= 8 for d in distances([(0.0, 0), (-0.0, 0), (1e-30, 0), (0.0625, 0), (0.125, -1), (1.1, 0), (2.9, 0), (5.9, 0)]))
