@@ -126,12 +126,27 @@ def _bind_short(lib, names):
     return _short
 
 
+def _c_int(n) -> int:
+    """A size as the C ABI's 32-bit argument: -1, which every entry point refuses, for one that does not fit (ctypes would
+    pass its low bits)."""
+    n = int(n)
+    return n if -1 << 31 <= n < 1 << 31 else -1
+
+
+def _size(n, name) -> int:
+    """A size that fits the C ABI's 32-bit arguments, else AtomError."""
+    n = int(n)
+    if not -1 << 31 <= n < 1 << 31:
+        raise AtomError(f"{name}={n} is not within 2**31")
+    return n
+
+
 def atom_row_bytes(K: int) -> int:
-    return int(load_library().atom_row_bytes(K))
+    return int(load_library().atom_row_bytes(_c_int(K)))
 
 
 def atom_num_groups(K: int) -> int:
-    return int(load_library().atom_num_groups(K))
+    return int(load_library().atom_num_groups(_c_int(K)))
 
 
 def atom_strerror(status: int) -> str:
@@ -219,7 +234,10 @@ def _mat(t, name):
     """(rows, cols) of a 2-D tensor argument."""
     if getattr(t, "dim", lambda: -1)() != 2:
         raise AtomError(f"{name} must be a 2-D tensor")
-    return int(t.shape[0]), int(t.shape[1])
+    rows, cols = t.shape
+    if rows >= 1 << 31 or cols >= 1 << 31:
+        raise AtomError(f"{name} has shape {(rows, cols)}, its sizes must be below 2**31")
+    return int(rows), int(cols)
 
 
 @functools.lru_cache(maxsize=64)

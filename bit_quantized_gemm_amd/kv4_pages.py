@@ -65,7 +65,7 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
     the pool's state, which are then replaced (more than 1024 rows take a second launch for it).  If the pool holds
     too few pages nothing is taken: all slots are -1, lengths and pool stay, state_out[1] says how many are missing."""
     free, state = _pool(pool)
-    total, page = int(total), int(page)
+    total, page = _bq._size(total, "total"), _bq._size(page, "page")
     if stream is None and slots is None and q_start is None and lens_out is None and state_out is None and _bq._SHORT is not None:
         out = _bq._SHORT.kv4_extend(lens, new, table, free, state, page, total)
         if out is not None:
@@ -84,7 +84,7 @@ def atom_kv4_extend(lens, new, table, pool, page, total, slots=None, q_start=Non
                   (q_start, "q_start", i32, (batch + 1,)), (lens_out, "lens_out", i32, (batch,)),
                   (state_out, "state_out", i32, (2,)))
     with on_device(table):
-        _bq._check(_bq.load_library().atom_kv4_extend(p[0], p[1], p[2], batch, width, page, p[3], int(free.shape[0]), p[4],
+        _bq._check(_bq.load_library().atom_kv4_extend(p[0], p[1], p[2], batch, width, page, p[3], _bq._c_int(free.shape[0]), p[4],
                                                       p[5], total, p[6], p[7], p[8], _bq._stream(stream, table.device)),
                    "atom_kv4_extend")
     return slots, q_start, lens_out, state_out
@@ -95,7 +95,7 @@ def atom_kv4_release(done, lens, table, pool, page, lens_out=None, state_out=Non
     pages.  Returns (lens_out, state_out): lengths, 0 where done, and the pool's new state; either may be given as its input,
     which is then replaced (more than 64 sequences take a second launch for it)."""
     free, state = _pool(pool)
-    page = int(page)
+    page = _bq._size(page, "page")
     if stream is None and lens_out is None and state_out is None and _bq._SHORT is not None:
         out = _bq._SHORT.kv4_release(done, lens, table, free, state, page)
         if out is not None:
@@ -109,6 +109,6 @@ def atom_kv4_release(done, lens, table, pool, page, lens_out=None, state_out=Non
                   (free, "free", i32, None), (state, "state", i32, (2,)), (lens_out, "lens_out", i32, (batch,)),
                   (state_out, "state_out", i32, (2,)))
     with on_device(table):
-        _bq._check(_bq.load_library().atom_kv4_release(p[0], p[1], p[2], batch, width, page, p[3], int(free.shape[0]), p[4],
+        _bq._check(_bq.load_library().atom_kv4_release(p[0], p[1], p[2], batch, width, page, p[3], _bq._c_int(free.shape[0]), p[4],
                                                        p[5], p[6], _bq._stream(stream, table.device)), "atom_kv4_release")
     return lens_out, state_out

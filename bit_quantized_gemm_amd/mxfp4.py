@@ -43,11 +43,11 @@ def signatures():
 
 
 def atom_mxfp4_row_bytes(K: int) -> int:
-    return int(_bq.load_library().atom_mxfp4_row_bytes(K))
+    return int(_bq.load_library().atom_mxfp4_row_bytes(_bq._c_int(K)))
 
 
 def atom_mxfp4_groups(K: int) -> int:
-    return int(_bq.load_library().atom_mxfp4_groups(K))
+    return int(_bq.load_library().atom_mxfp4_groups(_bq._c_int(K)))
 
 
 @functools.lru_cache(maxsize=256)

@@ -107,14 +107,14 @@ def check_device(t, name):
 
 
 def _bytes(what, M, N, K):
-    r = getattr(_bq.load_library(), what)(M, N, K)
+    r = getattr(_bq.load_library(), what)(_bq._c_int(M), _bq._c_int(N), _bq._c_int(K))
     if r < 0:
         raise _bq.AtomError(f"{what}: {_bq.atom_strerror(-r)}")
     return r
 
 
 def atom_w8a8_row_bytes(K: int) -> int:
-    return int(_bq.load_library().atom_w8a8_row_bytes(K))
+    return int(_bq.load_library().atom_w8a8_row_bytes(_bq._c_int(K)))
 
 
 @functools.lru_cache(maxsize=256)
