@@ -656,12 +656,10 @@ void launch_rows(const uint16_t* X, int64_t ldx, const uint8_t* Wq, const uint8_
 
 }  // namespace
 
-MxPlan mx_plan(int M, int N, int K) { return mx::plan(M, N, K, compute_units()); }
+MxPlan mx_plan(int M, int N, int K, int64_t scratch) { return mx::plan_within(M, N, K, compute_units(), scratch); }
 bool mx_one_launch(int M, int N, int K) { return mx::rows_fit(M, N, K, compute_units()); }
 
-int64_t mx_workspace_bytes(const MxPlan& p) {
-  return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0;
-}
+int64_t mx_workspace_bytes(const MxPlan& p) { return mx::part_bytes(p); }
 
 hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,
                              int M, int N, int K, bool bf16, uint16_t* Y, float* part, const MxPlan& plan,

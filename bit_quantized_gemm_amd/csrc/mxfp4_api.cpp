@@ -15,10 +15,10 @@ uint64_t row_bytes4(int32_t K) { return groups_of(K) * (ATOM_MX_GROUP / 2); }
 uint64_t code_bytes(int32_t rows, int32_t K) { return (uint64_t)rows * row_bytes4(K); }
 uint64_t scale_bytes(int32_t rows, int32_t K) { return (uint64_t)rows * groups_of(K) * 8; }
 
-// The plan of a valid shape; false where no launch would hold it.
-bool plan_of(int32_t M, int32_t N, int32_t K, atom::MxPlan& plan) {
+// The plan of a valid shape with as much scratch memory; false where no launch would hold it.
+bool plan_of(int32_t M, int32_t N, int32_t K, atom::MxPlan& plan, int64_t scratch = INT64_MAX) {
   if (!valid_gemm8(M, N, K)) return false;
-  plan = atom::mx_plan(M, N, K);
+  plan = atom::mx_plan(M, N, K, scratch);
   return plan.tiles > 0;
 }
 int64_t linear_bytes(int32_t M, int32_t K, const atom::MxPlan& plan) {
@@ -103,14 +103,10 @@ int atom_gemm_mxfp4(const void* Xq, const void* sx, const void* Wq, const void* 
                     int32_t K, int32_t dtype, void* Y, void* workspace, int64_t workspace_bytes, void* stream) {
   if (!Xq || !sx || !Wq || !sw || !Y) return ATOM_E_NULL;
   atom::MxPlan plan;
-  if (!plan_of(M, N, K, plan) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
+  if (!plan_of(M, N, K, plan, workspace ? workspace_bytes : 0) || !valid_dtype(dtype)) return ATOM_E_SHAPE;
   if (!aligned16(Xq) || !aligned16(sx) || !aligned16(Wq) || !aligned16(sw) || !aligned16(bias) || !aligned16(Y))
     return ATOM_E_ALIGN;
-  int64_t need = atom::mx_workspace_bytes(plan);
-  if (need > 0 && (!workspace || workspace_bytes < need)) {   // too little scratch: undivided
-    plan.splits = 1;
-    need = 0;
-  }
+  const int64_t need = atom::mx_workspace_bytes(plan);
   if (need > 0 && !aligned16(workspace)) return ATOM_E_ALIGN;
   const Range in[5] = {range_of(Xq, code_bytes(M, K)), range_of(sx, scale_bytes(M, K)), range_of(Wq, code_bytes(N, K)),
                        range_of(sw, scale_bytes(N, K)), range_of(bias, bias ? (uint64_t)N * 2 : 0)};

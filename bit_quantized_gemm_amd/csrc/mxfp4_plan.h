@@ -47,7 +47,7 @@ struct Plan {
 // 7.0 (16 rows at a time), 6.3 (32), 10.7, 12.8, 13.9; 256 x 11008 x 4096 18.6, 19.3, 17.0, 21.8, 32 (tiles); 1024 x 11008 x 4096 56, 47, 38, 43, 35;
 // 2048 x 4096 x 11008 97, 76, 57, 53, 72; 4096 x 28672 x 8192 925, 760, 537, 535, 449.  64 x 4096 x 11008 whole, two, three and four ways 24.7,
 // 17.9, 16.3 and 15.6; 777 x 777 x 8192 21.3, 17, 15.7 and 17.
-inline Plan plan(int M, int N, int K, int cus) {
+inline Plan plan(int M, int N, int K, int cus, bool divide = true) {
   auto tiles = [&](int kind) {
     return (int64_t)((M + kBM[kind] - 1) / kBM[kind]) * ((N + kBN[kind] - 1) / kBN[kind]);
   };
@@ -78,7 +78,7 @@ inline Plan plan(int M, int N, int K, int cus) {
   for (int kind = kRowKinds; kind < kKinds; ++kind) {
     const Cost& c = cost[kind];
     const int64_t t = tiles(kind);
-    for (int splits = 1; splits <= (kind == kDividedKind ? 4 : 1); ++splits) {
+    for (int splits = 1; splits <= (divide && kind == kDividedKind ? 4 : 1); ++splits) {
       if (splits > 1 && (groups < 4 * splits || t * splits > c.slots * cus)) break;
       const int64_t per = (t * splits + cus - 1) / cus;    // workgroups of the busiest unit
       const int64_t full = per / c.slots, rest = per % c.slots;
@@ -91,6 +91,15 @@ inline Plan plan(int M, int N, int K, int cus) {
     }
   }
   return best;
+}
+
+// Bytes of a plan's parts, and the plan of a shape for as much scratch memory: where that is too little for the parts, the one of
+// least time that has none, which is often another kernel than the divided one (us, divided, its kernel whole, and so: 100 x 260 x
+// 65536 38, 126, 35; 333 x 512 x 28672 22.5, 61, 46; 64 x 4096 x 8192 13.2, 19.9, 15.8).
+inline int64_t part_bytes(const Plan& p) { return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0; }
+inline Plan plan_within(int M, int N, int K, int cus, int64_t scratch) {
+  const Plan p = plan(M, N, K, cus);
+  return part_bytes(p) > scratch ? plan(M, N, K, cus, false) : p;
 }
 
 // Whether one launch quantizes the tokens, 16 in every workgroup, and multiplies: where their codes leave room in LDS and one round of

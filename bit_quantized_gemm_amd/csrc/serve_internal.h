@@ -79,7 +79,7 @@ hipError_t launch_quantize_mxfp4(const uint16_t* X, int64_t ldx, bool bf16, int 
 hipError_t launch_dequantize_mxfp4(const uint8_t* Xq, const uint8_t* sx, int rows, int K, bool bf16, uint16_t* X,
                                    hipStream_t stream);
 using MxPlan = mx::Plan;
-MxPlan mx_plan(int M, int N, int K);                     // for this device's compute units
+MxPlan mx_plan(int M, int N, int K, int64_t scratch);   // for this device's compute units and as much scratch memory
 bool mx_one_launch(int M, int N, int K);                 // whether launch_linear_rows_mxfp4 takes the layer
 int64_t mx_workspace_bytes(const MxPlan& plan);
 hipError_t launch_gemm_mxfp4(const uint8_t* Xq, const uint8_t* sx, const uint8_t* Wq, const uint8_t* sw, const uint16_t* bias,

@@ -62,7 +62,7 @@ int atom_dequantize_mxfp4(const void *Xq, const void *sx, int32_t rows, int32_t 
  *   Y  : fp16 / bf16 [M, N]                                                   (output)
  * workspace: atom_gemm_mxfp4_workspace_bytes(M, N, K) bytes let a grid of few output tiles divide K
  * among workgroups (fp32 parts added in a fixed order: repeated calls agree bit for bit); with less (or
- * NULL) it runs undivided.  Contents on entry do not matter.
+ * NULL) the fastest kernel that needs none takes the call, in up to twice the time where K is long.  Contents on entry do not matter.
  */
 int64_t atom_gemm_mxfp4_workspace_bytes(int32_t M, int32_t N, int32_t K);
 int atom_gemm_mxfp4(const void *Xq, const void *sx, const void *Wq, const void *sw, const void *bias, int32_t M,
