@@ -38,11 +38,14 @@ struct Plan {
 // The plan of a shape: the kernel whose estimated time (us) is least.
 //   Few rows: a start, and for each 16 columns of a compute unit a rate for K's groups and its end.
 //   Tiles: a round of the grid takes `fixed` us (first stages, epilogue) and `full` us for each group of K when every unit
-//     holds `slots` workgroups, `one` us when it holds one; reading the weights sets a floor (`read` bytes a us).
+//     holds `slots` workgroups, `one` us when it holds one, and `far` us where that one waits for HBM: operands past 5 MB (measured
+//     over sets of 40 products in turn: smaller ones were still in the last-level cache); reading the weights sets a floor (`read`
+//     bytes a us).
 //   64 x 64 tiles with K divided two to four ways, at least four groups each: the second kernel's 2.3 us and the parts' way
 //     through memory on top.
-// Fitted on 256 units to 137 shapes of products alone (1 to 4096 rows, 64 to 28672 columns, K 256 to 11008, weights that come from
-// HBM): the choice is 1.7% slower than the best kernel on average, over 10% on six.  Measured (us), few rows and the tiles from
+// Fitted on 256 units to 137 shapes of products alone (1 to 4096 rows, 64 to 28672 columns, K 256 to 11008), `far` to 127 more with K up to
+// 28672: over these and 45 of the others the choice is 1.7% slower than the best kernel on average, over 10% on nine, most (47%) on
+// 512 x 260 x 2048, a little more than one round of 32-token workgroups.  Measured (us), few rows and the tiles from
 // 64 x 64 up (M x N x K): 16 x 4096 x 4096 5.0, 10.5, 12.5, 13.6, 17.4, 25.4; 16 x 28672 x 8192 37, 28, 30, 31, 39, 48; 32 x 4096 x 4096
 // 7.0 (16 rows at a time), 6.3 (32), 10.7, 12.8, 13.9; 256 x 11008 x 4096 18.6, 19.3, 17.0, 21.8, 32 (tiles); 1024 x 11008 x 4096 56, 47, 38, 43, 35;
 // 2048 x 4096 x 11008 97, 76, 57, 53, 72; 4096 x 28672 x 8192 925, 760, 537, 535, 449.  64 x 4096 x 11008 whole, two, three and four ways 24.7,
@@ -57,11 +60,12 @@ inline Plan plan(int M, int N, int K, int cus, bool divide = true) {
   constexpr Rows rows[kRowKinds] = {{2.1, 0.118, 0.515}, {1.6, 0.155, 1.4}};
   struct Cost {
     int slots;
-    double full, one, fixed, read;
+    double full, one, far, fixed, read;
   };
-  constexpr Cost cost[kKinds] = {{}, {}, {3, 0.91, 0.38, 2.8, 3.6e6}, {2, 0.88, 0.55, 3.3, 4.6e6}, {2, 1.25, 0.70, 4.1, 4.5e6},
-                                 {1, 0.90, 0.90, 6.8, 3.4e6}, {1, 1.45, 1.45, 12.8, 5.7e6}};
+  constexpr Cost cost[kKinds] = {{}, {}, {3, 0.91, 0.38, 0.52, 2.8, 3.6e6}, {2, 0.88, 0.55, 0.55, 3.3, 4.6e6},
+                                 {2, 1.25, 0.70, 0.70, 4.1, 4.5e6}, {1, 0.90, 0.90, 0.90, 6.8, 3.4e6}, {1, 1.45, 1.45, 1.45, 12.8, 5.7e6}};
   const int groups = (K + 255) / 256;
+  const bool hbm = ((int64_t)M + N) * groups * 136 > 5000000;
   Plan best = {0, 0, 1};
   double least = -1.0;
   // (a launch has less than 2^32 threads, and at most 65535 workgroups in y)
@@ -82,7 +86,8 @@ inline Plan plan(int M, int N, int K, int cus, bool divide = true) {
       if (splits > 1 && (groups < 4 * splits || t * splits > c.slots * cus)) break;
       const int64_t per = (t * splits + cus - 1) / cus;    // workgroups of the busiest unit
       const int64_t full = per / c.slots, rest = per % c.slots;
-      const double part = rest ? c.one + (c.full - c.one) * (rest - 1) / (c.slots > 1 ? c.slots - 1 : 1) : 0.0;
+      const double one = hbm ? c.far : c.one;
+      const double part = rest ? one + (c.full - one) * (rest - 1) / (c.slots > 1 ? c.slots - 1 : 1) : 0.0;
       const double multiply = (groups + splits - 1) / splits * (full * c.full + part);
       const double read = (double)N * groups * 136 / (splits > 1 ? 5.6e6 : c.read);
       double time = 0.3 + (multiply > read ? multiply : read) + (full + (rest ? 1 : 0)) * c.fixed;
@@ -94,8 +99,8 @@ inline Plan plan(int M, int N, int K, int cus, bool divide = true) {
 }
 
 // Bytes of a plan's parts, and the plan of a shape for as much scratch memory: where that is too little for the parts, the one of
-// least time that has none, which is often another kernel than the divided one (us, divided, its kernel whole, and so: 100 x 260 x
-// 65536 38, 126, 35; 333 x 512 x 28672 22.5, 61, 46; 64 x 4096 x 8192 13.2, 19.9, 15.8).
+// least time that has none, which is often another kernel than the divided one (us, divided, its kernel whole, and so: 333 x 512 x
+// 28672 22.5, 61, 46; 200 x 1024 x 14336 15.0, 31.6, 25.6; 64 x 4096 x 8192 13.2, 19.9, 15.8).
 inline int64_t part_bytes(const Plan& p) { return p.splits > 1 ? (int64_t)p.splits * p.tiles * kBM[p.kind] * kBN[p.kind] * 4 : 0; }
 inline Plan plan_within(int M, int N, int K, int cus, int64_t scratch) {
   const Plan p = plan(M, N, K, cus);

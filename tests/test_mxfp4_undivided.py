@@ -27,7 +27,7 @@ int main() {
 }
 """
 
-# Us of products whose plan divides K, run whole by each kind of kernel (graph replays, operands from HBM; kinds 0 and 1: 16 and 32
+# Us of products of long K, run whole by each kind of kernel (graph replays, operands from HBM; kinds 0 and 1: 16 and 32
 # tokens, from 2 up the tiles).
 WHOLE = {(64, 4096, 11008): (25.4, 21.3, 25.1, 27.8, 33.6, 38.9, 56.9), (64, 4096, 8192): (19.7, 15.8, 19.9, 22.0, 26.3, 30.7, 45.1),
          (100, 260, 65536): (34.6, 50.2, 125.6, 135.7, 189.6, 198.6, 293.4), (333, 512, 28672): (46.3, 47.2, 61.3, 62.6, 85.8, 101.0, 161.8),
@@ -70,4 +70,16 @@ def test_scratch_decides(plans):
 def test_the_choice_without_scratch(plans):
     """Within a fifth of the fastest kernel measured."""
     for (s, us), p in zip(WHOLE.items(), plans(list(WHOLE))):
-        assert p[2] > 1 and us[p[4]] <= 1.2 * min(us), (s, p)
+        assert us[p[4]] <= 1.2 * min(us), (s, p)
+
+
+# Us of 64 x 64 tiles whole, and K divided two, three and four ways (as above), where a unit holds one workgroup of the whole product.
+DIVIDED = {(777, 777, 8192): (20.2, 17.3, 15.5, 17.0), (777, 777, 7000): (17.1, 15.7, 14.3, 15.7), (64, 4096, 8192): (19.9, 15.3, 13.6, 13.2),
+           (64, 4096, 11008): (25.1, 18.3, 15.6, 14.5), (160, 4096, 8192): (19.8, 18.3, 20.6, 20.0), (512, 1024, 8192): (17.8, 15.1, 14.5, 14.2),
+           (1024, 512, 11008): (25.4, 18.6, 18.4, 16.7), (333, 512, 28672): (61.3, 36.0, 26.8, 22.5), (200, 1024, 14336): (31.6, 20.7, 16.8, 15.0)}
+
+
+def test_long_products_are_divided(plans):
+    """A lone workgroup a unit waits for HBM at every stage: the division that is chosen is within 15% of the best measured."""
+    for (s, us), p in zip(DIVIDED.items(), plans(list(DIVIDED))):
+        assert p[0] == 2 and us[p[2] - 1] <= 1.15 * min(us), (s, p)
