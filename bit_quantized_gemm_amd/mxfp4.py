@@ -121,7 +121,8 @@ def atom_dequantize_mxfp4(Xq, sx, K, dtype=None, X=None, stream=None):
 
 def atom_gemm_mxfp4(Xq, sx, Wq, sw, K, bias=None, Y=None, dtype=None, workspace=None, stream=None):
     """Y [M, N] of packed operands; its type is Y's, or the bias's, or `dtype` (default fp16).  With a
-    workspace (1-D uint8, ``atom_gemm_mxfp4_workspace_bytes``) grids of few output tiles divide K."""
+    workspace (1-D uint8, ``atom_gemm_mxfp4_workspace_bytes``) grids of few output tiles divide K; without one, or with less, they
+    take up to twice as long (``linear_mxfp4`` takes one for itself).  Calls that may overlap need one each."""
     torch = _bq._torch()
     if stream is None and Y is None and _bq._SHORT is not None:
         kind = dtype if dtype is not None else getattr(bias, "dtype", torch.float16)
