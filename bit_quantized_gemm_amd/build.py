@@ -47,15 +47,26 @@ def _compile(src: str) -> str:
     return obj
 
 
+class Unavailable(RuntimeError):
+    """Something that the extension module is built with is not there (the C library needs none of it)."""
+
+
 def _build_short() -> None:
     """The extension module, against the headers and libraries of the torch that will load it."""
     import sysconfig
 
-    import torch
-    from torch.utils import cpp_extension
-
-    cxx = os.environ.get("CXX", shutil.which("g++") or "c++")
-    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        raise Unavailable(f"torch is not importable ({e})") from None
+    cxx = os.environ.get("CXX") or shutil.which("g++") or shutil.which("c++")
+    if not cxx or not shutil.which(cxx):
+        raise Unavailable("there is no host C++ compiler (g++, or CXX)")
+    python = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(python, "Python.h")):
+        raise Unavailable(f"Python's headers are not installed ({python})")
+    include = [*cpp_extension.include_paths(), python]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [cxx, "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            f"-I{INCLUDE}", *(a for i in include for a in ("-isystem", i)), os.path.join(CSRC, "short_calls.cpp"), "-o", SHORT + ".tmp",
@@ -67,19 +78,28 @@ def _build_short() -> None:
 
 
 def build(verbose: bool = False) -> str:
+    """Both libraries.  The C library needs hipcc alone: it is linked first, and where the extension module cannot be built for want of
+    torch, a host compiler or Python's headers, that is said on stderr and an older one removed (the binding works without)."""
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=8) as ex:
         short = ex.submit(_build_short)
         objs = list(ex.map(_compile, SOURCES))
-        short.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    built = [LIB]
+    try:
+        short.result()
+        built.append(SHORT)
+    except Unavailable as e:
+        if os.path.exists(SHORT):
+            os.remove(SHORT)
+        print(f"{os.path.basename(SHORT)} is not built: {e}; calls take the binding's full checks", file=sys.stderr)
     if verbose:
-        print(f"built {LIB} and {SHORT}")
+        print("built " + " and ".join(built))
     return LIB
 
 
