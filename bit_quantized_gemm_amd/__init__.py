@@ -33,6 +33,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import sys
+import warnings
 
 __all__ = [
     "AtomError", "EXPORTS", "GROUP", "OUTLIERS", "MAX_K", "lib_path", "load_library",
@@ -115,12 +117,23 @@ def load_library():
     return lib
 
 
+def _built_for() -> str:
+    """The torch and the Python whose insides an extension module built now would hold: it takes tensors apart by inlined code."""
+    torch = _torch()
+    return f"torch {torch.__version__} {getattr(torch.version, 'git_version', None)}, {sys.implementation.cache_tag}"
+
+
 def _bind_short(lib, names):
-    """The extension module with the library's addresses, or None where it is not built."""
+    """The extension module with the library's addresses, or None where it is not built, or not for this torch and Python."""
     try:
         stream = _torch()._C._cuda_getCurrentRawStream
         from . import _short
     except (ImportError, AttributeError):
+        return None
+    built_for = getattr(_short, "built_for", "an unknown torch")
+    if built_for != _built_for():
+        warnings.warn(f"{_short.__file__} was built for {built_for}, this is {_built_for()}: calls take the full checks until "
+                      "`python -m bit_quantized_gemm_amd.build` builds it again", RuntimeWarning)
         return None
     _short.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names}, stream)
     return _short

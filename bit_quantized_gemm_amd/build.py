@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libatom.so")
-SHORT = os.path.join(HERE, "_short.so")
+SHORT = os.path.join(HERE, "_short" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["atom_api.cpp", "select.hip", "quantize.hip", "gemm.hip", "gemm_small.hip", "gemm_w4a8.hip",
            "serve_api.cpp", "w8a8_quantize.hip", "gemm_w8a8.hip", "kv4_cache.hip", "kv4_attention.hip",
@@ -53,8 +54,6 @@ class Unavailable(RuntimeError):
 
 def _build_short() -> None:
     """The extension module, against the headers and libraries of the torch that will load it."""
-    import sysconfig
-
     try:
         import torch
         from torch.utils import cpp_extension
@@ -66,15 +65,20 @@ def _build_short() -> None:
     python = sysconfig.get_paths()["include"]
     if not os.path.exists(os.path.join(python, "Python.h")):
         raise Unavailable(f"Python's headers are not installed ({python})")
+    from . import _built_for
+
     include = [*cpp_extension.include_paths(), python]
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [cxx, "-O2", "-fPIC", "-std=c++17", "-Wall", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           f"-I{INCLUDE}", *(a for i in include for a in ("-isystem", i)), os.path.join(CSRC, "short_calls.cpp"), "-o", SHORT + ".tmp",
+           f'-DATOM_BUILT_FOR="{_built_for()}"', f"-I{INCLUDE}", *(a for i in include for a in ("-isystem", i)), os.path.join(CSRC, "short_calls.cpp"), "-o", SHORT + ".tmp",
            f"-L{lib}", "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for short_calls.cpp:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(SHORT + ".tmp", SHORT)
+    untagged = os.path.join(os.path.dirname(SHORT), "_short.so")      # of builds that named no Python
+    if untagged != SHORT and os.path.exists(untagged):
+        os.remove(untagged)
 
 
 def build(verbose: bool = False) -> str:

@@ -7,7 +7,9 @@
 // (us), the same checks in Python and here: linear_mxfp4 of one token 7.2 and 4.6, atom_rmsnorm_w8a8 10.6 and 5.1, atom_kv4_extend 10.6 and
 // 5.5, atom_kv4_release 8.3 and 5.0.
 //
-// The addresses of the C entry points come from the binding (`bind`), so this module loads without the library.
+// The addresses of the C entry points come from the binding (`bind`), so this module loads without the library.  What it holds of
+// tensors is inlined from torch's headers: `built_for` names the torch and the Python that it was built with, and the binding
+// leaves a module of another one alone.
 #include <Python.h>
 
 #include <ATen/EmptyTensor.h>
@@ -333,4 +335,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_short", nullptr, -1, methods, nul
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__short(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__short(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", ATOM_BUILT_FOR) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

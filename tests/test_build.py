@@ -5,6 +5,7 @@ import sys
 
 import pytest
 
+import bit_quantized_gemm_amd as bq
 from bit_quantized_gemm_amd import build as b
 
 
@@ -48,8 +49,7 @@ def test_the_c_library_without_the_extension(recorded, monkeypatch, capsys, miss
         monkeypatch.delenv("CXX", raising=False)
         monkeypatch.setattr(b.shutil, "which", lambda name: None)
     if missing == "headers":
-        import sysconfig
-        monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+        monkeypatch.setattr(b.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
     with open(b.SHORT, "w"):
         pass
     assert b.build() == b.LIB and os.path.exists(b.LIB)
@@ -68,3 +68,41 @@ def test_a_module_that_does_not_compile_is_an_error(recorded, monkeypatch):
     with pytest.raises(RuntimeError, match="short_calls"):
         b.build()
     assert os.path.exists(b.LIB) and len(linked(recorded)) == 1
+
+
+# ---- the extension module holds torch's insides: it is used with the torch and the Python that it was built with alone
+@pytest.fixture
+def module():
+    pytest.importorskip("torch")
+    if not os.path.exists(bq.lib_path()):
+        pytest.skip("libatom.so not built (python -m bit_quantized_gemm_amd.build)")
+    bq.load_library()
+    if bq._SHORT is None:
+        pytest.skip("the extension module is not built")
+    return bq._SHORT
+
+
+def test_the_module_names_what_it_was_built_for(module):
+    import torch
+    assert module.built_for == bq._built_for() and torch.__version__ in module.built_for and "cpython" in module.built_for
+    assert os.path.basename(module.__file__) == os.path.basename(b.SHORT) == "_short" + b.sysconfig.get_config_var("EXT_SUFFIX")
+
+
+@pytest.mark.parametrize("other", ["version", "build", "python"])
+def test_a_module_of_another_torch_is_left_alone(module, monkeypatch, other):
+    """None, with a warning that names both; what was bound stays as it is."""
+    import torch
+    if other == "version":
+        monkeypatch.setattr(torch, "__version__", "9.9.9")
+    elif other == "build":
+        monkeypatch.setattr(torch.version, "git_version", "0" * 40)
+    else:
+        monkeypatch.setattr(bq.sys, "implementation", type("I", (), {"cache_tag": "cpython-399"}))
+    with pytest.warns(RuntimeWarning, match="was built for"):
+        assert bq._bind_short(bq._LIB, ("atom_linear_mxfp4",)) is None
+
+
+def test_a_module_that_says_nothing_is_left_alone(module, monkeypatch):
+    monkeypatch.delattr(module, "built_for")
+    with pytest.warns(RuntimeWarning, match="unknown torch"):
+        assert bq._bind_short(bq._LIB, ()) is None
