@@ -214,7 +214,7 @@ __global__ __launch_bounds__(w8a8::block_threads(THREADS)) void norm_kernel(Norm
       }
       // three roundings (of the factor, of u and of s) of at most 127: u is within 381 x 2^-24 of the exact value, 2.27e-5
       if (__builtin_amdgcn_ballot_w64(extreme || far >= 0.5f - 0x1.9p-16f)) {
-        const double f = rstd / (double)s;
+        const double f = divided(rstd, (double)s, (double)f32 * root);   // (from 2^-22 by two steps: 2^-52)
         double beside = 0.0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
