@@ -17,18 +17,18 @@
 //     straight into LDS (LDS-DMA).  At the largest sizes the power that random operands draw bounds it: 4096 x 28672 x 8192
 //     (M x N x K) takes 449 us, 4.3 PFLOP/s, with zeros 348 us; the same kernel without copies and LDS reads 327 and 266 us (the
 //     matrix cores alone at the clock that power leaves), without its stores 416 and 308.  The library's product reaches 3.0 PFLOP/s
-//     there.  Below that it is bound by how fast a compute unit gets lines that miss its L2: 2048 x 4096 x 11008 51 us (3.6
-//     PFLOP/s), 47 with zeros, 46 the copies alone.
+//     there.  Below that it is bound by how fast a compute unit gets lines that miss its L2: 2048 x 4096 x 11008 50.5 us (3.7
+//     PFLOP/s; 48 to 50 where the operands are in the last-level cache), 47 with zeros, 46 the copies alone.
 //     On the way there (4096 x 28672 x 8192 and 2048 x 4096 x 11008): 485 and 61 us with each wave's scale words loaded into
 //     registers and a stage's copies issued in one slice; 478 and 62 with all of a stage's operands in registers after its first slice
 //     (256 x 256 tiles); 449 and 53 with scales through LDS and copies spread over the slices.
 //   gemm_rows_kernel (few tokens, or few outputs): bound by reading the weights and the launch.  A workgroup owns 16 columns, its
 //     waves divide K, each loads its operands straight into registers, all of them at once where K is short; the waves' sums
-//     meet in LDS.  Weights from HBM: 16 x 4096 x 4096 5.0 us, 16 x 11008 x 4096 9.6 us (2.5 TB/s; as many bytes of codes from
-//     the L2), 1 x 11008 x 4096 7.7 us.
-//   linear_rows_kernel: the same with the quantizer in front, where one round of workgroups holds all outputs: one launch for two (us),
-//     1 x 4096 x 4096 4.5 and 6.3, 4 x 11008 x 4096 8.2 and 10.1, 16 x 11008 x 4096 10.1 and 11.3, 16 x 4096 x 4096 7.8 and 7.0,
-//     256 x 1024 x 2048 6.1 and 8.0.
+//     meet in LDS.  Weights from HBM: 16 x 4096 x 4096 5.0 us, 16 x 11008 x 4096 9.2 us (2.6 TB/s; as many bytes of codes from
+//     the L2), 1 x 11008 x 4096 7.0 us.
+//   linear_rows_kernel: the same with the quantizer in front, where one round of workgroups holds all outputs: one launch for two (us,
+//     weights from HBM), 1 x 4096 x 4096 4.7 and 6.3, 4 x 11008 x 4096 8.2 and 10.1, 16 x 11008 x 4096 10.2 and 11.3, 16 x 4096 x 4096
+//     7.8 to 8.3 and 7.0, 256 x 1024 x 2048 6.1 and 8.0.
 #include "lds_ring.h"
 #include "atom_internal.h"
 #include "gemm_tile.h"

@@ -43,8 +43,8 @@ struct Plan {
 //     bytes a us).
 //   64 x 64 tiles with K divided two to four ways, at least four groups each: the second kernel's 2.3 us and the parts' way
 //     through memory on top.
-// Fitted on 256 units to 137 shapes of products alone (1 to 4096 rows, 64 to 28672 columns, K 256 to 11008), `far` to 127 more with K up to
-// 28672: over these and 45 of the others the choice is 1.7% slower than the best kernel on average, over 10% on nine, most (47%) on
+// Fitted on 256 units to 137 shapes of products alone (1 to 4096 rows, 64 to 28672 columns, K 256 to 11008), `far` to 130 more with K up to
+// 28672: over these and 45 of the others the choice is 1.7% slower than the best kernel on average, over 10% on ten, most (47%) on
 // 512 x 260 x 2048, a little more than one round of 32-token workgroups.  Measured (us), few rows and the tiles from
 // 64 x 64 up (M x N x K): 16 x 4096 x 4096 5.0, 10.5, 12.5, 13.6, 17.4, 25.4; 16 x 28672 x 8192 37, 28, 30, 31, 39, 48; 32 x 4096 x 4096
 // 7.0 (16 rows at a time), 6.3 (32), 10.7, 12.8, 13.9; 256 x 11008 x 4096 18.6, 19.3, 17.0, 21.8, 32 (tiles); 1024 x 11008 x 4096 56, 47, 38, 43, 35;
@@ -113,7 +113,7 @@ inline Plan plan_within(int M, int N, int K, int cus, int64_t scratch) {
 // 8 x 4096 x 4096 5.7 and 6.6, 16 x 11008 x 2048 6.1 and 10.8, 8 x 8192 x 8192 12.4 and 12.4, 64 x 4096 x 2048 6.3 and 8.4, 256 x 1024 x 2048 6.1 and 8.0,
 // 250 x 777 x 1155 6.4 and 10.4, 333 x 777 x 2048 8.1 and 9.1.  Against two where 16 long tokens meet few columns: 16 x 4096 x 4096 7.8 and 7.0, 17 x 256 x 4096
 // 6.6 and 6.4, 333 x 777 x 1155 8.3 and 8.0; called one by one from Python these are 7.8 and 8.9, 6.6 and 8.9, 8.3 and 9.4, since the second
-// launch is 4 us of the host's time.  Past that: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5, 128 x 4096 x 2048 9.1 and 8.5, 512 x 1024 x 1155
+// launch is 4 us of the host's time.  So it is for few tokens of long rows: 8 x 4096 x 8192 9.3 and 8.8, 4 x 16384 x 8192 19.5 and 18.8.  Past that: 16 x 28672 x 1155 10.9 and 9.3, 16 x 28672 x 4096 18.9 and 17.5, 128 x 4096 x 2048 9.1 and 8.5, 512 x 1024 x 1155
 // 8.9 and 7.2.
 inline bool rows_fit(int M, int N, int K, int cus) {
   const int64_t tokens = M < kTokens ? M : kTokens, blocks = (M + kTokens - 1) / kTokens;

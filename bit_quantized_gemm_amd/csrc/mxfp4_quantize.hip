@@ -7,8 +7,9 @@
 // Scales lie group by group ([groups, rows, 8]), so a line of them belongs to 16 rows: a workgroup takes neighbouring rows,
 // whose pieces of it meet in one L2.
 //
-// Measured: 8192 x 8192 36 us (4.7 TB/s, a copy of memory reaches 4.75; 38 with the elements multiplied in fp32 before the conversion),
-// 2048 x 11008 13.3 us (14.6), 16 x 4096 2.1 us, of which the launch is most; back to values 8192 x 8192 38 us.
+// Measured: 8192 x 8192 37.8 us from HBM (4.5 TB/s; a copy of memory reaches 5.1), 2048 x 11008 14.4, with operands and codes in the
+// last-level cache 26.6 and 10.1, 16 x 4096 1.9 to 2.1 us, of which the launch is most; back to values 8192 x 8192 42 and 30 us.  With the
+// elements multiplied in fp32 before the conversion a tenth more (2048 x 11008 14.6 for 13.3, three sets in turn).
 #include "mxfp4_row.h"
 
 namespace atom {

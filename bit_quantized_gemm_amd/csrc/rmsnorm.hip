@@ -2,9 +2,9 @@
 // (formulas: atom_norm.h).
 //
 // What bounds it: HBM.  A row is read once (twice its bytes with a residual, and once out again), kept in registers by
-// the threads that share it, and leaves as codes.  With a residual, graph replays over rows from HBM: 8192 x 8192 to int8 84.5 us, to
-// MXFP4 81.1 us (5.6 and 5.4 TB/s; a copy of memory reaches 4.75 to 5.1), 2048 x 11008 30.0 and 31.6 us, 16 x 4096 3.1 and 3.2 us, of
-// which the launch is more than half.
+// the threads that share it, and leaves as codes.  With a residual, graph replays over rows from HBM: 8192 x 8192 to int8 84.7 us, to
+// MXFP4 81.3 us (5.6 and 5.4 TB/s; a copy of memory reaches 5.1; 96 us where calls lie apart), 2048 x 11008 30.1 and 31.7 us (34 and 35
+// over 800 MB of outputs too), 16 x 4096 3.1 and 3.2 us, of which the launch is more than half.
 //
 // Exact codes.  p = h * w is exact in fp32 (two 8- or 11-bit significands), so y = p / root, root = sqrt(mean + eps), is one
 // row's number away from exact: the sum of squares and the root are fp64, and each code is made from p times one factor in
